@@ -1,7 +1,9 @@
 /*
  * kvx.h -- C ABI of the kvx library: decode-step attention over a paged KV
  * cache with non-uniform per-head budgets, the coalesced KV gather and the
- * block pager behind it, and kept-set selection for sparse decode.
+ * block pager behind it, kept-set selection for sparse decode, and the steps
+ * of speculative decoding over the same pages (tables built on the GPU, K/V
+ * append, attention for a tree of drafted tokens, branch commit).
  *
  * Sources of the operations:
  *  - "Tangram: Unlocking Non-Uniform KV Cache for Efficient Multi-turn LLM
@@ -23,7 +25,8 @@
  *    host arrays passed in. The library owns only its opaque objects: the
  *    plan (host arrays plus a device copy made by kvx_plan_upload, freed by
  *    kvx_plan_destroy) and the frame (host view, two device descriptors and
- *    record buffers, freed by kvx_frame_destroy).
+ *    record buffers, freed by kvx_frame_destroy) and the cache handle (host
+ *    memory only, freed by kvx_cache_destroy).
  *  - Device calls are asynchronous on the stream passed as `void *stream`
  *    (a cudaStream_t; NULL = the legacy default stream). They never
  *    synchronise and never allocate device memory on the hot path (a frame
@@ -66,9 +69,13 @@ extern "C" {
 #define KVX_DEV_TIMEOUT 4u     /* a pipeline wait gave up after its time limit */
 #define KVX_DEV_BAD_BLOCK 8u   /* a block-table entry outside [0, num_phys_blocks);
                                   a kept index outside [0, Lmax) (packing,
-                                  kept-row attention) */
+                                  kept-row attention); a slot outside its pool
+                                  (append, branch commit) */
 #define KVX_DEV_BAD_LENGTH 16u /* num_blocks[s] outside [0, max_blocks] or the row;
-                                  a selection seq_len outside [0, Lmax] */
+                                  a selection seq_len outside [0, Lmax]; lengths, row
+                                  starts or an accepted path out of range (cache calls) */
+#define KVX_DEV_NO_PAGES 32u   /* kvx_build_tables: a free list holds fewer pages than
+                                  the lengths need */
 
 /* ---- element types --------------------------------------------------- */
 #define KVX_F32 0
@@ -123,6 +130,8 @@ extern "C" {
 #define KVX_MAX_GQA 8
 #define KVX_MAX_GATHER_TENSORS 4
 #define KVX_WS_HEADER_BYTES 256
+#define KVX_MAX_CACHE_SEQS 4096 /* sequences of a cache handle */
+#define KVX_MAX_TREE 128        /* new rows of a sequence in kvx_tree_attn */
 
 typedef struct kvx_shape {
   int32_t B;          /* sequences in the batch */
@@ -624,6 +633,179 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
                                 void *const *stagings,
                                 int64_t staging_row_bytes, int32_t flags,
                                 uint32_t *status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * One speculative-decoding step over the non-uniform paged cache.
+ *
+ * kvx_decode_attn attends with one query token per sequence, from a plan built
+ * on the host for fixed lengths. A step that verifies drafted tokens changes
+ * every length, has several query tokens per sequence and writes the cache.
+ * The calls below do that step with every length on the device, so that a
+ * captured step can be replayed while the lengths change:
+ *     kvx_build_tables   pages and slots for the step's new rows
+ *     kvx_append_kv      the new rows' K and V into their slots
+ *     kvx_tree_attn      attention of the new rows over cache and tree
+ *     kvx_tree_commit    the accepted branch made contiguous, the rest dropped
+ *
+ * Common arguments:
+ *   cache      handle below: shape, head groups, pools and page tables.
+ *   kv_len     device int32 [B][Hkv]: tokens n[b][h] each KV head has cached.
+ *   q_start    device int32 [B+1]: the new rows of sequence b are rows
+ *              q_start[b] .. q_start[b+1]-1 of every row array (T_b of them;
+ *              0 = none). New row i of sequence b is token n[b][h] + i of
+ *              head (b, h), for every head.
+ *   max_rows   host: rows the row arrays hold, >= q_start[B]. Rows from
+ *              q_start[B] on are neither read nor written. With 0 the row
+ *              arrays may be NULL.
+ *   slots      device int64 [max_rows][Hkv]: where the row's K and V of KV head
+ *              h are, as a row index into the pool of h's group:
+ *                  head-major pages:  (page * |G| + r) * P + t % P
+ *                  token-major pages: (page * P + t % P) * |G| + r
+ *              (token t, r = h's rank in its group; a row is D elements).
+ *   workspace  device, 256-byte aligned, zero-filled once; its first word is
+ *              the status word. At least KVX_WS_HEADER_BYTES, for
+ *              kvx_tree_attn at least kvx_tree_attn_workspace_bytes. Calls
+ *              whose work may overlap on the GPU (two streams, two graphs)
+ *              need workspaces of their own.
+ * Lengths are checked on the device. A sequence whose q_start entries are
+ * negative, descending or past max_rows, or whose kv_len is negative or
+ * does not fit its page table together with its new rows, is treated as
+ * having no new rows, and KVX_DEV_BAD_LENGTH is set.
+ * Launch: one kernel each, a programmatic dependent of the kernel before it
+ * on the stream that waits for that kernel before it reads or writes
+ * anything. All may be captured into a CUDA graph, also as their first call.
+ * ------------------------------------------------------------------------- */
+typedef struct kvx_cache kvx_cache;
+
+/* Describes a paged cache once, for all the calls above (host only; keeps the
+ * pointers, owns none of the device memory).
+ *   shape       B (at most KVX_MAX_CACHE_SEQS), Hq, Hkv, D, page_size,
+ *               num_groups, dtype, layout, with kvx_plan_create's limits.
+ *   head_group  host int32 [Hkv], as for kvx_plan_create.
+ *   k_pools, v_pools, pool_pages, page_tables, page_table_stride: host arrays
+ *               [num_groups], as for kvx_decode_attn; pools and tables are
+ *               written by kvx_append_kv, kvx_tree_commit and kvx_build_tables.
+ * Errors: KVX_EINVAL, KVX_EUNSUPPORTED, KVX_ERANGE (pool_pages >= 2^31 - 1;
+ * page_table_stride * page_size past int32), KVX_ENOMEM. */
+int kvx_cache_create(const kvx_shape *shape, const int32_t *head_group,
+                     void *const *k_pools, void *const *v_pools, const int64_t *pool_pages,
+                     int32_t *const *page_tables, const int32_t *page_table_stride,
+                     kvx_cache **out);
+void kvx_cache_destroy(kvx_cache *cache);
+
+/* ---------------------------------------------------------------------------
+ * kvx_build_tables -- page tables and slot maps from request lengths, on the
+ * GPU (Tangram, Fig. 8(b): every head group has its own table; a group needs
+ * the pages of its longest head).
+ *
+ * For group g and sequence b, with T_b = new_len[b]:
+ *     need = ceil((max_{h in g} kv_len[b][h] + T_b) / P),
+ *     or 0 when that length is 0,
+ * pages_in[g][b] pages are held. Pages past `need` are released, missing ones
+ * taken: the released pages of group g are pushed on its free list in
+ * ascending (b, page index) order; the missing pages are then popped from its
+ * end, in ascending (b, page index) order, and written to the table. So the
+ * call grows, trims (rejected drafts), starts (pages_in = 0) and ends
+ * (kv_len = new_len = 0) sequences alike, and its result does not depend on
+ * timing.
+ *   new_len     device int32 [B].
+ *   pages_in    device int32 [num_groups][B]; pages_out, the counts after the
+ *               call, must be another array.
+ *   free_pages  host array [num_groups] of device int32 pointers, each with
+ *               room for pool_pages[g] ids; entries [0, free_in[g]) are the
+ *               free pages.
+ *   free_in     device int32 [num_groups]; free_out likewise, another array.
+ *   q_start     written: exclusive sums of new_len, [B+1].
+ *   slots       written for rows [0, q_start[B]); -1 where the page id is
+ *               outside the pool (KVX_DEV_BAD_PAGE).
+ * Table entries past pages_out and free-list entries past free_out keep
+ * stale ids. A call repeated with the same inputs gives the same result (the
+ * counts are not updated in place), which lets a graph be replayed.
+ * If any length or count is out of range (KVX_DEV_BAD_LENGTH; also more than
+ * max_rows new rows) or a free list is too short (KVX_DEV_NO_PAGES), the call
+ * changes no table, list or slot: pages_out = pages_in, free_out = free_in,
+ * and q_start is all 0, so that the calls after it do nothing.
+ * Errors: KVX_EINVAL (also pages_out == pages_in or free_out == free_in),
+ * KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_build_tables(const kvx_cache *cache, const int32_t *kv_len, const int32_t *new_len,
+                     const int32_t *pages_in, int32_t *pages_out, int32_t *const *free_pages,
+                     const int32_t *free_in, int32_t *free_out, int32_t max_rows,
+                     int32_t *q_start, int64_t *slots, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/* ---------------------------------------------------------------------------
+ * kvx_append_kv -- writes the new rows' K and V into their slots:
+ *     pool_K(h)[slots[r][h]] = k_new[r][h],  same for V,  r < q_start[B].
+ *   k_new, v_new  device [max_rows] rows of Hkv * D elements of the cache's
+ *                 dtype, 16-byte aligned, k_stride / v_stride elements apart
+ *                 (>= Hkv * D, a multiple of 16 bytes): slices of a fused
+ *                 projection qualify.
+ * A slot outside its pool is not written (KVX_DEV_BAD_BLOCK; -1 silently is
+ * not). The slots of a call are distinct; of two equal ones either row, or
+ * 16-byte pieces of both, may remain.
+ * Errors: KVX_EINVAL, KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_append_kv(const kvx_cache *cache, const void *k_new, int64_t k_stride,
+                  const void *v_new, int64_t v_stride, const int32_t *q_start,
+                  const int64_t *slots, int32_t max_rows, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * kvx_tree_attn -- attention of a tree of drafted tokens over the cache.
+ *
+ * For sequence b, new row i < T_b (T_b <= max_q), query head j, KV head
+ * h = floor(j / g):
+ *     s_t = scale * <q[q_start[b] + i][j], k_t>
+ * over the cached tokens t < n[b][h], all visible, and the sequence's own new
+ * rows t = n[b][h] + u, u < T_b, visible if bit u of the row's mask is set;
+ *     out[q_start[b] + i][j] = sum over visible t of softmax(s)_t * v_t,
+ * and zeros for a row that sees nothing. What a row does not see has no
+ * influence on it, NaN and infinities included. K and V of the new rows are
+ * read from their pages (kvx_append_kv).
+ *   q          device [max_rows] rows of Hq * D elements of the cache's dtype,
+ *              16-byte aligned, q_stride elements apart (>= Hq * D, a multiple
+ *              of 16 bytes).
+ *   max_q      host: largest T_b, 1 .. KVX_MAX_TREE; a sequence with more new
+ *              rows is skipped (KVX_DEV_BAD_LENGTH).
+ *   mask       device uint32 [max_rows][W], W = ceil(max_q / 32): bit u % 32 of
+ *              word u / 32 of row q_start[b] + i says that row i sees draft u
+ *              (of a tree: its ancestors and itself). Bits from T_b on are
+ *              ignored. NULL: a chain, row i sees drafts 0 .. i.
+ *   scale      score scale; 0 means 1/sqrt(D).
+ *   out        device fp32 [max_rows][Hq][D], 16-byte aligned.
+ * T_b = 1 with mask NULL is one decode step with device lengths. The keys are
+ * split over the GPU from the lengths, on the device; pieces of a head
+ * are merged by log-sum-exp in a fixed order (equal inputs give equal bits).
+ * Page ids outside a pool read as zero rows (KVX_DEV_BAD_PAGE).
+ * Errors: KVX_EINVAL, KVX_ERANGE (max_q), KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_tree_attn_workspace_bytes(const kvx_cache *cache, int32_t max_q, size_t *bytes);
+
+int kvx_tree_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
+                  const int32_t *q_start, int32_t max_rows, int32_t max_q,
+                  const int32_t *kv_len, const uint32_t *mask, float scale, float *out,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * kvx_tree_commit -- keeps the accepted branch of every tree: for every head,
+ *     row n + j <- row n + path[b][j]  (K and V),  j < n_acc[b],
+ *     kv_len_out[b][h] = kv_len[b][h] + n_acc[b].
+ * The next kvx_build_tables, given kv_len_out, releases the pages past it.
+ *   path       device int32 [B][path_stride]: the accepted rows of the tree
+ *              (indices below T_b) in strictly ascending order, as any tree
+ *              whose parents precede their children has them.
+ *   n_acc      device int32 [B], each in [0, min(T_b, path_stride)].
+ *   kv_len_out device int32 [B][Hkv]; may be kv_len itself.
+ * A sequence whose n_acc or path is out of range or not ascending keeps its
+ * rows and its kv_len (KVX_DEV_BAD_LENGTH). A move whose source or target
+ * slot is outside its pool is skipped (KVX_DEV_BAD_BLOCK).
+ * Errors: KVX_EINVAL, KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_tree_commit(const kvx_cache *cache, const int32_t *q_start, const int64_t *slots,
+                    int32_t max_rows, const int32_t *path, int32_t path_stride,
+                    const int32_t *n_acc, const int32_t *kv_len, int32_t *kv_len_out,
+                    void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

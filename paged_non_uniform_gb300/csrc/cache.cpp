@@ -1,0 +1,254 @@
+// cache.cpp -- the cache handle and the entry points of a speculative-decoding
+// step over it: argument validation (everything is checked before anything is
+// launched) and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "kvx_internal.h"
+#include "tree.h"
+
+namespace kvx {
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+
+bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
+
+int elem_bytes(const kvx_cache *c) { return c->shape.dtype == KVX_BF16 ? 2 : 4; }
+
+// A row array's stride in bytes, or 0 if it is not usable.
+int64_t row_stride(const kvx_cache *c, int64_t stride, int heads) {
+  const int64_t es = elem_bytes(c);
+  if (stride < (int64_t)heads * c->shape.D || stride > ((int64_t)1 << 40) || stride * es % 16)
+    return 0;
+  return stride * es;
+}
+
+bool workspace_ok(const void *ws, size_t bytes, size_t need) {
+  return ws && aligned(ws, 256) && bytes >= need;
+}
+
+// Blocks of the attention kernel on the current device.
+int tree_blocks(const kvx_cache *, int *blocks) {
+  int32_t sms = 0;
+  const int rc = kvx_device_sm_count(&sms);
+  if (rc != KVX_OK) return rc;
+  *blocks = sms * tree_simt_blocks_per_sm();
+  return KVX_OK;
+}
+
+TreeWs tree_ws_layout(const kvx_cache *c, int max_q, int blocks, int *row_groups) {
+  const int rows = tree_simt_rows();
+  const size_t heads = (size_t)c->shape.B * c->shape.Hkv;
+  const int groups = (max_q * c->dev.g + rows - 1) / rows;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  TreeWs w;
+  w.counters = KVX_WS_HEADER_BYTES;
+  w.part_ml = w.counters + up(heads * groups * sizeof(int32_t));
+  w.part_o = w.part_ml + up((size_t)2 * blocks * rows * sizeof(float2));
+  w.total = w.part_o + up((size_t)2 * blocks * rows * c->shape.D * sizeof(float));
+  if (row_groups) *row_groups = groups;
+  return w;
+}
+
+}  // namespace
+}  // namespace kvx
+
+using namespace kvx;
+
+extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
+                                void *const *k_pools, void *const *v_pools,
+                                const int64_t *pool_pages, int32_t *const *page_tables,
+                                const int32_t *page_table_stride, kvx_cache **out) {
+  if (!out) return KVX_EINVAL;
+  *out = nullptr;
+  if (!s || !head_group || !k_pools || !v_pools || !pool_pages || !page_tables ||
+      !page_table_stride)
+    return KVX_EINVAL;
+  if (s->B < 1 || s->Hkv < 1 || s->Hq < 1 || s->num_groups < 1) return KVX_EINVAL;
+  if (s->B > KVX_MAX_CACHE_SEQS || s->Hkv > KVX_MAX_KV_HEADS ||
+      s->num_groups > KVX_MAX_GROUPS || s->num_groups > s->Hkv)
+    return KVX_EUNSUPPORTED;
+  if (s->Hq % s->Hkv != 0) return KVX_EINVAL;
+  if (s->Hq / s->Hkv > KVX_MAX_GQA) return KVX_EUNSUPPORTED;
+  if (s->D != 64 && s->D != 128) return KVX_EUNSUPPORTED;
+  if (!is_pow2(s->page_size) || s->page_size < 8 || s->page_size > 128) return KVX_EUNSUPPORTED;
+  if (s->dtype != KVX_F32 && s->dtype != KVX_BF16) return KVX_EUNSUPPORTED;
+  if (s->layout != KVX_LAYOUT_HEAD_MAJOR && s->layout != KVX_LAYOUT_TOKEN_MAJOR)
+    return KVX_EUNSUPPORTED;
+  const int G = s->num_groups, Hkv = s->Hkv;
+  int32_t size[KVX_MAX_GROUPS] = {0};
+  for (int h = 0; h < Hkv; ++h) {
+    if (head_group[h] < 0 || head_group[h] >= G) return KVX_EINVAL;
+    size[head_group[h]] += 1;
+  }
+  for (int gi = 0; gi < G; ++gi) {
+    if (size[gi] == 0) return KVX_EINVAL;
+    if (!k_pools[gi] || !v_pools[gi] || !page_tables[gi]) return KVX_EINVAL;
+    if (!aligned(k_pools[gi], 16) || !aligned(v_pools[gi], 16) || !aligned(page_tables[gi], 4))
+      return KVX_EINVAL;
+    if (pool_pages[gi] < 1 || page_table_stride[gi] < 1) return KVX_EINVAL;
+    if (pool_pages[gi] >= ((int64_t)1 << 31) - 1 ||
+        (int64_t)page_table_stride[gi] * s->page_size > INT32_MAX)
+      return KVX_ERANGE;
+  }
+  kvx_cache *c = new (std::nothrow) kvx_cache();
+  if (!c) return KVX_ENOMEM;
+  c->shape = *s;
+  CacheDev &d = c->dev;
+  std::memset(&d, 0, sizeof(d));
+  d.B = s->B;
+  d.Hq = s->Hq;
+  d.Hkv = Hkv;
+  d.D = s->D;
+  d.g = s->Hq / Hkv;
+  d.G = G;
+  d.P = s->page_size;
+  while ((1 << d.lgP) < d.P) ++d.lgP;
+  d.token_major = s->layout == KVX_LAYOUT_TOKEN_MAJOR;
+  d.row_bytes = s->D * elem_bytes(c);
+  int32_t seen[KVX_MAX_GROUPS] = {0};
+  for (int h = 0; h < Hkv; ++h) {
+    d.head_grp[h] = (int8_t)head_group[h];
+    d.head_row[h] = (int8_t)seen[head_group[h]]++;
+  }
+  for (int gi = 0; gi < G; ++gi)
+    d.grp[gi] = {page_tables[gi],  (char *)k_pools[gi],   (char *)v_pools[gi],
+                 pool_pages[gi],   page_table_stride[gi], size[gi]};
+  *out = c;
+  return KVX_OK;
+}
+
+extern "C" void kvx_cache_destroy(kvx_cache *c) { delete c; }
+
+extern "C" int kvx_build_tables(const kvx_cache *c, const int32_t *kv_len, const int32_t *new_len,
+                                const int32_t *pages_in, int32_t *pages_out,
+                                int32_t *const *free_pages, const int32_t *free_in,
+                                int32_t *free_out, int32_t max_rows, int32_t *q_start,
+                                int64_t *slots, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+  if (!c || !kv_len || !new_len || !pages_in || !pages_out || !free_pages || !free_in ||
+      !free_out || !q_start || max_rows < 0 || (max_rows > 0 && !slots))
+    return KVX_EINVAL;
+  if (pages_in == pages_out || free_in == free_out || !aligned(slots, 8)) return KVX_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  TablesParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  for (int gi = 0; gi < c->dev.G; ++gi) {
+    if (!free_pages[gi]) return KVX_EINVAL;
+    p.free_pages[gi] = free_pages[gi];
+  }
+  p.kv_len = kv_len;
+  p.new_len = new_len;
+  p.pages_in = pages_in;
+  p.pages_out = pages_out;
+  p.free_in = free_in;
+  p.free_out = free_out;
+  p.q_start = q_start;
+  p.slots = slots;
+  p.status = (uint32_t *)workspace;
+  p.max_rows = max_rows;
+  const cudaError_t e = launch_tables(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_append_kv(const kvx_cache *c, const void *k_new, int64_t k_stride,
+                             const void *v_new, int64_t v_stride, const int32_t *q_start,
+                             const int64_t *slots, int32_t max_rows, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  if (!c || !q_start || max_rows < 0) return KVX_EINVAL;
+  if (max_rows > 0 && (!k_new || !v_new || !slots)) return KVX_EINVAL;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8)) return KVX_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.k = (const char *)k_new;
+  p.v = (const char *)v_new;
+  p.k_stride = row_stride(c, k_stride, c->dev.Hkv);
+  p.v_stride = row_stride(c, v_stride, c->dev.Hkv);
+  if (!p.k_stride || !p.v_stride) return KVX_EINVAL;
+  p.q_start = q_start;
+  p.slots = slots;
+  p.status = (uint32_t *)workspace;
+  p.max_rows = max_rows;
+  const cudaError_t e = launch_append(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_tree_attn_workspace_bytes(const kvx_cache *c, int32_t max_q, size_t *bytes) {
+  if (!c || !bytes) return KVX_EINVAL;
+  if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
+  int blocks = 0;
+  const int rc = tree_blocks(c, &blocks);
+  if (rc != KVX_OK) return rc;
+  *bytes = tree_ws_layout(c, max_q, blocks, nullptr).total;
+  return KVX_OK;
+}
+
+extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride,
+                             const int32_t *q_start, int32_t max_rows, int32_t max_q,
+                             const int32_t *kv_len, const uint32_t *mask, float scale, float *out,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+  if (!c || !q_start || !kv_len || max_rows < 0) return KVX_EINVAL;
+  if (max_rows > 0 && (!q || !out)) return KVX_EINVAL;
+  if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
+  if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 4)) return KVX_EINVAL;
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.q_stride = row_stride(c, q_stride, c->dev.Hq);
+  if (!p.q_stride) return KVX_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  int blocks = 0;
+  const int rc = tree_blocks(c, &blocks);
+  if (rc != KVX_OK) return rc;
+  const TreeWs w = tree_ws_layout(c, max_q, blocks, &p.row_groups);
+  if (workspace_bytes < w.total) return KVX_EINVAL;
+  char *ws = (char *)workspace;
+  p.q = (const char *)q;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.mask = mask;
+  p.out = out;
+  p.status = (uint32_t *)ws;
+  p.counters = (int32_t *)(ws + w.counters);
+  p.part_ml = (float2 *)(ws + w.part_ml);
+  p.part_o = (float *)(ws + w.part_o);
+  p.max_rows = max_rows;
+  p.max_q = max_q;
+  p.words = (max_q + 31) / 32;
+  const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
+  p.scale_log2 = (float)((double)sc * 1.4426950408889634);
+  const cudaError_t e = launch_tree_simt(p, c->shape.dtype, blocks, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_tree_commit(const kvx_cache *c, const int32_t *q_start, const int64_t *slots,
+                               int32_t max_rows, const int32_t *path, int32_t path_stride,
+                               const int32_t *n_acc, const int32_t *kv_len, int32_t *kv_len_out,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+  if (!c || !q_start || !path || !n_acc || !kv_len || !kv_len_out || max_rows < 0 ||
+      (max_rows > 0 && !slots) || path_stride < 1)
+    return KVX_EINVAL;
+  if (!aligned(slots, 8)) return KVX_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  CommitParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.q_start = q_start;
+  p.slots = slots;
+  p.path = path;
+  p.n_acc = n_acc;
+  p.kv_len = kv_len;
+  p.kv_out = kv_len_out;
+  p.status = (uint32_t *)workspace;
+  p.max_rows = max_rows;
+  p.path_stride = path_stride;
+  const cudaError_t e = launch_commit(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}

@@ -1,0 +1,145 @@
+// rows.cu -- movement of new K/V rows: the append of a step's rows into their
+// slots and the compaction of accepted tree branches. Both copy 16-byte chunks
+// and do no arithmetic on them.
+#include "ptx.cuh"
+#include "tree.h"
+
+namespace kvx {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t pool_rows(const CacheDev &c, int grp) {
+  return c.grp[grp].pages * c.grp[grp].size * c.P;
+}
+
+// pool[slots[r][h]] = new[r][h] for K and V. One thread per 16-byte chunk of a
+// (row, head), K and V together.
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheDev &c = p.c;
+  const int cpr = c.row_bytes >> 4;  // chunks of a row: 8, 16 or 32
+  const int rows = min(__ldg(p.q_start + c.B), p.max_rows);
+  if (rows <= 0) return;
+  const int64_t total = (int64_t)rows * c.Hkv * cpr;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kThreads) {
+    const int64_t rh = i / cpr;
+    const int ch = (int)(i - rh * cpr);
+    const int64_t r = rh / c.Hkv;
+    const int h = (int)(rh - r * c.Hkv);
+    const int64_t slot = __ldg(p.slots + rh);
+    const int grp = c.head_grp[h];
+    if (slot < 0 || slot >= pool_rows(c, grp)) {
+      if (slot != -1 && ch == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
+      continue;
+    }
+    const int64_t src = (int64_t)h * c.row_bytes + ch * 16;
+    const uint4 kv = __ldg((const uint4 *)(p.k + r * p.k_stride + src));
+    const uint4 vv = __ldg((const uint4 *)(p.v + r * p.v_stride + src));
+    const int64_t dst = slot * c.row_bytes + ch * 16;
+    *(uint4 *)(c.grp[grp].k + dst) = kv;
+    *(uint4 *)(c.grp[grp].v + dst) = vv;
+  }
+}
+
+// row n + j <- row n + path[j]. One thread owns one 16-byte column of K or V of
+// one head and walks j upwards: path ascends strictly, so path[j] >= j and
+// every source of a later j lies past all targets written so far. A batch of
+// eight loads therefore may precede its eight stores, and no thread reads what
+// another writes.
+__global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheDev &c = p.c;
+  const int b = blockIdx.y;
+  const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1);
+  const int a = __ldg(p.n_acc + b);
+  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.max_rows;
+  const int *path = p.path + (size_t)b * p.path_stride;
+  bool ok = rows_ok && a >= 0 && a <= q1 - q0 && a <= p.path_stride;
+  if (ok) {
+    int bad = 0;
+    for (int j = threadIdx.x; j < a; j += kThreads) {
+      const int v = __ldg(path + j), before = j ? __ldg(path + j - 1) : -1;
+      bad |= v <= before || v >= q1 - q0;
+    }
+    ok = __syncthreads_or(bad) == 0;
+  }
+  if (blockIdx.x == 0) {
+    for (int h = threadIdx.x; h < c.Hkv; h += kThreads) {
+      const size_t i = (size_t)b * c.Hkv + h;
+      p.kv_out[i] = __ldg(p.kv_len + i) + (ok ? a : 0);
+    }
+    if (!ok && threadIdx.x == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
+  }
+  if (!ok || a == 0) return;
+  const int cpr = c.row_bytes >> 4;
+  const int per_head = 2 * cpr;  // K chunks, then V chunks
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  const int h = i / per_head;
+  if (h >= c.Hkv) return;
+  const int x = i - h * per_head;
+  const CacheGroup &g = c.grp[c.head_grp[h]];
+  char *pool = (x < cpr ? g.k : g.v) + (x < cpr ? x : x - cpr) * 16;
+  const int64_t limit = g.pages * g.size * c.P;
+  const int64_t *slots = p.slots + (size_t)q0 * c.Hkv + h;
+  for (int j0 = 0; j0 < a; j0 += 8) {
+    uint4 v[8];
+    int64_t to[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u;
+      to[u] = -1;
+      if (j >= a) continue;
+      const int s = __ldg(path + j);
+      if (s == j) continue;
+      const int64_t from = __ldg(slots + (size_t)s * c.Hkv), t = __ldg(slots + (size_t)j * c.Hkv);
+      if (from < 0 || from >= limit || t < 0 || t >= limit) {
+        if (x == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
+        continue;
+      }
+      to[u] = t;
+      v[u] = *(const uint4 *)(pool + from * c.row_bytes);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (to[u] >= 0) *(uint4 *)(pool + to[u] * c.row_bytes) = v[u];
+  }
+}
+
+cudaLaunchConfig_t config(dim3 grid, cudaStream_t st, cudaLaunchAttribute *attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams &p, cudaStream_t st) {
+  if (p.max_rows == 0) return cudaSuccess;
+  const int64_t chunks = (int64_t)p.max_rows * p.c.Hkv * (p.c.row_bytes >> 4);
+  const int64_t blocks = (chunks + kThreads - 1) / kThreads;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = config(dim3((unsigned)(blocks < 65536 ? blocks : 65536)), st, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_commit(const CommitParams &p, cudaStream_t st) {
+  const int threads = p.c.Hkv * 2 * (p.c.row_bytes >> 4);
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg =
+      config(dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)p.c.B), st, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, commit_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kvx

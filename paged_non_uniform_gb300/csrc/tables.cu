@@ -1,0 +1,230 @@
+// tables.cu -- page tables and slot maps from request lengths, on the GPU.
+//
+// Per head group g and sequence b, need = ceil(longest head / P) pages against
+// the `have` held: rel = max(0, have - need) pages go back to the group's free
+// list, alloc = max(0, need - have) come from it. With exclusive sums over b,
+// released page r lands at list position F + r and allocation k takes position
+// F + R - 1 - k (F free pages before the call, R released in all). So every
+// page's place follows from the sums alone: no atomics, no order of arrival.
+//
+// One launch. Every block computes the sums of one group by itself (a few
+// loads per thread; lengths are tiny and come from L2) and then does an equal
+// share of the group's moved pages and slots. A popped position at or past F
+// is a page released by this same call, perhaps by another block: it is found
+// in its owner's table through the sums instead of the list, so no block waits
+// for another. Table entries below `have` are never written, list entries below F
+// neither, which is what makes a repeated call give the same result.
+#include "ptx.cuh"
+#include "tree.h"
+
+namespace kvx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Exclusive sums of a[0..n), in place; a[n] becomes the total. n ints in
+// shared memory, all threads take part. Sums that pass int32 are caught by the
+// caller's 64-bit totals.
+__device__ void exclusive_scan(int *a, int n, int *warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + kThreads - 1) / kThreads;
+  const int lo = min(n, tid * per), hi = min(n, lo + per);
+  int s = 0;
+  for (int i = lo; i < hi; ++i) s += a[i];
+  int x = s;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  int run = before + x - s;
+  for (int i = lo; i < hi; ++i) {
+    const int v = a[i];
+    a[i] = run;
+    run += v;
+  }
+  if (tid == 0) a[n] = all;
+  __syncthreads();
+}
+
+// The entry b of exclusive sums s[0..n] with s[b] <= k < s[b + 1].
+__device__ __forceinline__ int owner(const int *s, int n, int k) {
+  int lo = 0, hi = n;  // s[lo] <= k < s[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s[mid] <= k)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesParams p) {
+  extern __shared__ int sm[];
+  __shared__ unsigned long long total[2][KVX_MAX_GROUPS];  // alloc, release
+  __shared__ unsigned long long rows_total;
+  __shared__ int warp_sum[kWarps];
+  __shared__ int8_t heads[KVX_MAX_KV_HEADS];  // heads by group
+  __shared__ int head_off[KVX_MAX_GROUPS + 1];
+  pdl_launch_dependents();
+  const CacheDev &c = p.c;
+  const int B = c.B, G = c.G, Hkv = c.Hkv, P = c.P, lgP = c.lgP, tid = threadIdx.x;
+  const int own = blockIdx.y;  // this block's group
+  int *a_start = sm, *r_start = sm + (B + 1), *q_start = sm + 2 * (B + 1);
+  if (tid < KVX_MAX_GROUPS) total[0][tid] = total[1][tid] = 0;
+  if (tid == 0) {
+    rows_total = 0;
+    int n = 0;
+    for (int g = 0; g < G; ++g) {
+      head_off[g] = n;
+      for (int h = 0; h < Hkv; ++h)
+        if (c.head_grp[h] == g) heads[n++] = (int8_t)h;
+    }
+    head_off[G] = n;
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // ---- lengths of every (group, sequence); sums of this block's group
+  int bad = 0;
+  for (int i = tid; i < G * B; i += kThreads) {
+    const int g = i / B, b = i - g * B;
+    const int t = __ldg(p.new_len + b);
+    const int have = __ldg(p.pages_in + i);
+    int64_t n = 0;
+    for (int k = head_off[g]; k < head_off[g + 1]; ++k) {
+      const int v = __ldg(p.kv_len + (size_t)b * Hkv + heads[k]);
+      bad |= v < 0;
+      n = max(n, (int64_t)v);
+    }
+    n += t;
+    bad |= t < 0 || have < 0 || have > c.grp[g].stride || n > ((int64_t)c.grp[g].stride << lgP);
+    const int need = (int)((n + P - 1) >> lgP);
+    const int alloc = max(0, need - have), rel = max(0, have - need);
+    if (alloc) atomicAdd(&total[0][g], (unsigned long long)alloc);
+    if (rel) atomicAdd(&total[1][g], (unsigned long long)rel);
+    if (g == own) {
+      a_start[b] = alloc;
+      r_start[b] = rel;
+      q_start[b] = t;
+      if (t > 0) atomicAdd(&rows_total, (unsigned long long)t);
+    }
+  }
+  bad = __syncthreads_or(bad);
+  int short_list = 0;
+  if (!bad) {
+    bad = rows_total > (unsigned long long)p.max_rows;
+    for (int g = 0; g < G; ++g) {
+      const int64_t f = __ldg(p.free_in + g);
+      const int64_t a = (int64_t)total[0][g], r = (int64_t)total[1][g];
+      bad |= f < 0 || f + r > c.grp[g].pages;
+      short_list |= a > f + r;
+    }
+  }
+  const bool first = blockIdx.x == 0;
+  if (bad || short_list) {  // the same verdict in every block: nothing changes
+    if (first) {
+      for (int b = tid; b < B; b += kThreads)
+        p.pages_out[(size_t)own * B + b] = __ldg(p.pages_in + (size_t)own * B + b);
+      if (tid == 0) p.free_out[own] = __ldg(p.free_in + own);
+      if (own == 0) {
+        for (int b = tid; b <= B; b += kThreads) p.q_start[b] = 0;
+        if (tid == 0) atomicOr(p.status, bad ? KVX_DEV_BAD_LENGTH : KVX_DEV_NO_PAGES);
+      }
+    }
+    return;
+  }
+  const int32_t *pages_in = p.pages_in + (size_t)own * B;
+  if (first)
+    for (int b = tid; b < B; b += kThreads)
+      p.pages_out[(size_t)own * B + b] = __ldg(pages_in + b) + a_start[b] - r_start[b];
+  __syncthreads();
+  exclusive_scan(a_start, B, warp_sum);
+  exclusive_scan(r_start, B, warp_sum);
+  exclusive_scan(q_start, B, warp_sum);
+  const CacheGroup &grp = c.grp[own];
+  int32_t *list = p.free_pages[own];
+  const int F = __ldg(p.free_in + own), A = a_start[B], R = r_start[B], N = q_start[B];
+  if (first) {
+    if (tid == 0) p.free_out[own] = F + R - A;
+    if (own == 0)
+      for (int b = tid; b <= B; b += kThreads) p.q_start[b] = q_start[b];
+  }
+  // Page j of sequence b after its release: the pages kept are the first
+  // have - rel.
+  auto released = [&](int r) {
+    const int b = owner(r_start, B, r);
+    const int j = __ldg(pages_in + b) - (r_start[b + 1] - r_start[b]) + (r - r_start[b]);
+    return grp.table[(size_t)b * grp.stride + j];
+  };
+  auto popped = [&](int k) {
+    const int at = F + R - 1 - k;
+    return at >= F ? released(at - F) : list[at];
+  };
+  const int step = (int)gridDim.x * kThreads, at0 = (int)blockIdx.x * kThreads + tid;
+  for (int64_t r = at0; r < R; r += step) list[F + r] = released((int)r);
+  for (int64_t k = at0; k < A; k += step) {
+    const int b = owner(a_start, B, (int)k);
+    const int j = __ldg(pages_in + b) + ((int)k - a_start[b]);
+    grp.table[(size_t)b * grp.stride + j] = popped((int)k);
+  }
+  // ---- slots of this group's heads
+  const int nh = grp.size;
+  const int64_t total_slots = (int64_t)N * nh;
+  int b = 0, b_end = 0;  // q_start[b + 1] of the sequence of the last row
+  for (int64_t i = at0; i < total_slots; i += step) {
+    const int row = (int)(i / nh), rank = (int)(i - (int64_t)row * nh);
+    if (row >= b_end) {
+      b = owner(q_start, B, row);
+      b_end = q_start[b + 1];
+    }
+    const int h = heads[head_off[own] + rank];
+    const int t = __ldg(p.kv_len + (size_t)b * Hkv + h) + (row - q_start[b]);
+    const int j = t >> lgP, have = __ldg(pages_in + b);
+    const int page = j < have ? grp.table[(size_t)b * grp.stride + j]
+                              : popped(a_start[b] + (j - have));
+    int64_t slot = -1;
+    if (page >= 0 && page < grp.pages)
+      slot = pool_row(c, grp, page, rank, t & (P - 1));
+    else
+      atomicOr(p.status, KVX_DEV_BAD_PAGE);
+    p.slots[(size_t)row * Hkv + h] = slot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tables(const TablesParams &p, cudaStream_t st) {
+  const int64_t slots = (int64_t)p.max_rows * p.c.Hkv;
+  const int64_t want = (slots / p.c.G + 4 * kThreads - 1) / (4 * kThreads);
+  const int most = 608 / p.c.G > 1 ? 608 / p.c.G : 1;
+  const unsigned blocks = (unsigned)(want < 1 ? 1 : want > most ? most : want);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, (unsigned)p.c.G);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 3 * (size_t)(p.c.B + 1) * sizeof(int);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  if (cfg.dynamicSmemBytes > 40 * 1024)  // (4096 + 1) * 12 bytes at most
+    e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             3 * (KVX_MAX_CACHE_SEQS + 1) * (int)sizeof(int));
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, tables_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kvx

@@ -1,0 +1,107 @@
+// tree.h -- structures shared by the cache handle, its entry points and the
+// kernels of a speculative-decoding step (tables, append, tree attention,
+// branch commit). Not part of the public interface.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvx.h"
+
+namespace kvx {
+
+// One head group of a cache: its page table [B][stride] and its pools.
+struct CacheGroup {
+  int32_t *table;
+  char *k, *v;
+  int64_t pages;  // in each pool
+  int32_t stride, size;
+};
+
+// The cache as the kernels see it (passed by value in their parameters).
+struct CacheDev {
+  CacheGroup grp[KVX_MAX_GROUPS];
+  int32_t B, Hq, Hkv, D, g, G;
+  int32_t P, lgP;       // page size and its log2
+  int32_t token_major;  // page layout
+  int32_t row_bytes;    // D elements
+  int8_t head_grp[KVX_MAX_KV_HEADS];
+  int8_t head_row[KVX_MAX_KV_HEADS];
+};
+
+// Row of a group's pool that holds token slot `off` of page `page` of the head
+// with rank r.
+__host__ __device__ inline int64_t pool_row(const CacheDev &c, const CacheGroup &g, int64_t page,
+                                            int r, int off) {
+  return c.token_major ? (page * c.P + off) * g.size + r
+                       : ((page * g.size + r) << c.lgP) + off;
+}
+
+struct TablesParams {
+  CacheDev c;
+  int32_t *free_pages[KVX_MAX_GROUPS];
+  const int32_t *kv_len, *new_len, *pages_in, *free_in;
+  int32_t *pages_out, *free_out, *q_start;
+  int64_t *slots;
+  uint32_t *status;
+  int32_t max_rows;
+};
+
+struct AppendParams {
+  CacheDev c;
+  const char *k, *v;
+  int64_t k_stride, v_stride;  // bytes
+  const int32_t *q_start;
+  const int64_t *slots;
+  uint32_t *status;
+  int32_t max_rows;
+};
+
+struct CommitParams {
+  CacheDev c;
+  const int32_t *q_start, *path, *n_acc, *kv_len;
+  const int64_t *slots;
+  int32_t *kv_out;
+  uint32_t *status;
+  int32_t max_rows, path_stride;
+};
+
+// Tree attention. A head's keys come in tiles, its query rows (new row i and
+// query head j of the KV head: row i * g + j) in groups; tree_split.cuh
+// says how the (row group, tile) units are cut over the blocks.
+struct TreeParams {
+  CacheDev c;
+  const char *q;
+  int64_t q_stride;  // bytes
+  const int32_t *q_start, *kv_len;
+  const uint32_t *mask;
+  float *out;
+  uint32_t *status;
+  int32_t *counters;  // [B * Hkv][row groups] finished pieces, back to 0 after the merge
+  float2 *part_ml;    // [2 * blocks][rows of a group] = (max in log2 units, sum)
+  float *part_o;      // [2 * blocks][rows of a group][D]
+  int32_t max_rows, max_q, words;  // words: uint32 words of a mask row
+  int32_t row_groups;              // most row groups of a head
+  float scale_log2;                // scale * log2(e)
+};
+
+// Workspace of tree attention: header | counters | partial (m, l) | partial o.
+struct TreeWs {
+  size_t counters, part_ml, part_o, total;
+};
+
+cudaError_t launch_tables(const TablesParams &p, cudaStream_t st);
+cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
+cudaError_t launch_commit(const CommitParams &p, cudaStream_t st);
+cudaError_t launch_tree_simt(const TreeParams &p, int dtype, int blocks, cudaStream_t st);
+int tree_simt_rows();           // query rows of a row group
+int tree_simt_blocks_per_sm();  // resident blocks
+
+}  // namespace kvx
+
+struct kvx_cache {
+  kvx_shape shape;
+  kvx::CacheDev dev;
+  int32_t sms;  // of the device current at the first attention call; 0: not asked yet
+};

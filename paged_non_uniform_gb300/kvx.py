@@ -34,6 +34,7 @@ KVX_DEV_BAD_BUDGET = 2
 KVX_DEV_TIMEOUT = 4
 KVX_DEV_BAD_BLOCK = 8
 KVX_DEV_BAD_LENGTH = 16
+KVX_DEV_NO_PAGES = 32
 
 KVX_F32 = 0
 KVX_BF16 = 1
@@ -51,6 +52,8 @@ KVX_LAYOUT_HEAD_MAJOR = 0
 KVX_LAYOUT_TOKEN_MAJOR = 1
 KVX_MAX_GROUPS = 16
 KVX_WS_HEADER_BYTES = 256
+KVX_MAX_CACHE_SEQS = 4096
+KVX_MAX_TREE = 128
 
 
 class KvxError(RuntimeError):
@@ -144,6 +147,19 @@ lib.kvx_frame_get_stats.argtypes = [_vp, _c.POINTER(kvx_frame_stats)]
 lib.kvx_gather_coalesce_noalloc.argtypes = [_vp, _vp, _c.c_int32, _c.c_int32, _c.c_int32, _vp,
                                             _c.c_int64, _c.c_int64, _vp, _c.c_int64,
                                             _c.c_int32, _vp, _vp]
+
+lib.kvx_cache_create.argtypes = [_c.POINTER(kvx_shape), _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _c.POINTER(_vp)]
+lib.kvx_cache_destroy.argtypes = [_vp]
+lib.kvx_cache_destroy.restype = None
+lib.kvx_build_tables.argtypes = [_vp] * 8 + [_c.c_int32, _vp, _vp, _vp, _c.c_size_t, _vp]
+lib.kvx_append_kv.argtypes = [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _vp, _vp, _c.c_int32, _vp,
+                              _c.c_size_t, _vp]
+lib.kvx_tree_attn_workspace_bytes.argtypes = [_vp, _c.c_int32, _c.POINTER(_c.c_size_t)]
+lib.kvx_tree_attn.argtypes = [_vp, _vp, _c.c_int64, _vp, _c.c_int32, _c.c_int32, _vp, _vp,
+                              _c.c_float, _vp, _vp, _c.c_size_t, _vp]
+lib.kvx_tree_commit.argtypes = [_vp, _vp, _vp, _c.c_int32, _vp, _c.c_int32, _vp, _vp, _vp, _vp,
+                                _c.c_size_t, _vp]
 
 
 def kvx_status_string(status: int) -> str:
@@ -480,3 +496,142 @@ class Frame:
         st = kvx_frame_stats()
         _check(lib.kvx_frame_get_stats(self.handle, _c.byref(st)), "kvx_frame_get_stats")
         return {k: int(getattr(st, k)) for k, _ in kvx_frame_stats._fields_}
+
+
+# ---------------------------------------------------------------------------
+# Speculative-decoding step (cache calls)
+
+def _dense(x, what: str, itemsize: int, count: int = 0):
+    """Address of a dense device array: integer addresses pass, tensors must be
+    contiguous, of the given item size and hold at least `count` items."""
+    if isinstance(x, int):
+        return x
+    if x is None or not x.is_cuda or x.element_size() != itemsize or not x.is_contiguous() \
+            or x.numel() < count:
+        raise KvxError(f"{what}: not a dense device array of {count} {itemsize}-byte items",
+                       KVX_EINVAL)
+    return x.data_ptr()
+
+
+def _rows(x, what: str, itemsize: int, width: int, max_rows: int):
+    """(address, row stride in elements) of [max_rows] rows of `width` elements:
+    a tensor [rows][width] or [rows][heads][D] whose rows are dense, a row
+    stride apart; for an integer address, the rows are dense."""
+    if isinstance(x, int):
+        return x, width
+    inner = 1
+    ok = x is not None and x.is_cuda and x.element_size() == itemsize and x.dim() >= 2 \
+        and x.shape[0] >= max_rows
+    if ok:
+        for n, st in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+            ok = ok and (st == inner or n == 1)
+            inner *= n
+    if not ok or inner != width:
+        raise KvxError(f"{what}: not {max_rows} device rows of {width} {itemsize}-byte items",
+                       KVX_EINVAL)
+    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else width)
+
+
+def _nbytes(workspace, nbytes):
+    if nbytes is None:
+        return workspace.numel() * workspace.element_size()
+    return int(nbytes)
+
+
+class Cache:
+    """Owner of one kvx_cache handle (kvx_cache_create): the shape, head groups,
+    pools and page tables of a paged cache. Keeps the tensors it was given
+    alive."""
+
+    def __init__(self, B, Hq, Hkv, D, page_size, num_groups, dtype, head_group, k_pools, v_pools,
+                 pool_pages, page_tables, page_table_stride, layout=KVX_LAYOUT_HEAD_MAJOR):
+        self.handle = None
+        self.shape = kvx_shape(B, Hq, Hkv, D, page_size, num_groups, dtype, layout)
+        self.item = 2 if dtype == KVX_BF16 else 4
+        hg, ps = _i32(head_group), _i32(page_table_stride)
+        pp = np.ascontiguousarray(np.asarray(pool_pages, dtype=np.int64))
+        if hg.size != Hkv or any(len(x) != num_groups
+                                 for x in (k_pools, v_pools, page_tables, pp, ps)):
+            raise KvxError("kvx_cache_create: array lengths", KVX_EINVAL)
+        h = _vp()
+        _check(lib.kvx_cache_create(_c.byref(self.shape), hg.ctypes.data, _ptr_array(k_pools),
+                                    _ptr_array(v_pools), pp.ctypes.data, _ptr_array(page_tables),
+                                    ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
+        self.handle = h.value
+        self._keep = (list(k_pools), list(v_pools), list(page_tables))
+
+    def destroy(self) -> None:
+        if self.handle:
+            lib.kvx_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pages, free_in,
+                     free_out, max_rows, q_start, slots, workspace, workspace_bytes=None,
+                     stream=None) -> None:
+    s = cache.shape
+    B, G, n = s.B, s.num_groups, int(max_rows)
+    if len(free_pages) != G:
+        raise KvxError("kvx_build_tables: one free list per head group", KVX_EINVAL)
+    rc = lib.kvx_build_tables(
+        cache.handle, _dense(kv_len, "kv_len", 4, B * s.Hkv), _dense(new_len, "new_len", 4, B),
+        _dense(pages_in, "pages_in", 4, G * B), _dense(pages_out, "pages_out", 4, G * B),
+        _ptr_array(free_pages), _dense(free_in, "free_in", 4, G),
+        _dense(free_out, "free_out", 4, G), n, _dense(q_start, "q_start", 4, B + 1),
+        _dense(slots, "slots", 8, n * s.Hkv), _dptr(workspace),
+        _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check(rc, "kvx_build_tables")
+
+
+def kvx_append_kv(cache: Cache, k_new, v_new, q_start, slots, max_rows, workspace,
+                  workspace_bytes=None, stream=None) -> None:
+    s = cache.shape
+    n = int(max_rows)
+    k, ks = _rows(k_new, "k_new", cache.item, s.Hkv * s.D, n)
+    v, vs = _rows(v_new, "v_new", cache.item, s.Hkv * s.D, n)
+    rc = lib.kvx_append_kv(cache.handle, k, ks, v, vs, _dense(q_start, "q_start", 4, s.B + 1),
+                           _dense(slots, "slots", 8, n * s.Hkv), n, _dptr(workspace),
+                           _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check(rc, "kvx_append_kv")
+
+
+def kvx_tree_attn_workspace_bytes(cache: Cache, max_q: int) -> int:
+    v = _c.c_size_t(0)
+    _check(lib.kvx_tree_attn_workspace_bytes(cache.handle, int(max_q), _c.byref(v)),
+           "kvx_tree_attn_workspace_bytes")
+    return int(v.value)
+
+
+def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale, out, workspace,
+                  workspace_bytes=None, stream=None) -> None:
+    s = cache.shape
+    n, T = int(max_rows), int(max_q)
+    qp, qs = _rows(q, "q", cache.item, s.Hq * s.D, n)
+    mp = None if mask is None else _dense(mask, "mask", 4, n * ((T + 31) // 32))
+    rc = lib.kvx_tree_attn(cache.handle, qp, qs, _dense(q_start, "q_start", 4, s.B + 1), n, T,
+                           _dense(kv_len, "kv_len", 4, s.B * s.Hkv), mp, float(scale),
+                           _dense(out, "out", 4, n * s.Hq * s.D), _dptr(workspace),
+                           _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check(rc, "kvx_tree_attn")
+
+
+def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len, kv_len_out,
+                    workspace, path_stride=None, workspace_bytes=None, stream=None) -> None:
+    s = cache.shape
+    n = int(max_rows)
+    if path_stride is None:
+        path_stride = path.shape[1]
+    rc = lib.kvx_tree_commit(
+        cache.handle, _dense(q_start, "q_start", 4, s.B + 1),
+        _dense(slots, "slots", 8, n * s.Hkv), n,
+        _dense(path, "path", 4, s.B * int(path_stride)), int(path_stride),
+        _dense(n_acc, "n_acc", 4, s.B), _dense(kv_len, "kv_len", 4, s.B * s.Hkv),
+        _dense(kv_len_out, "kv_len_out", 4, s.B * s.Hkv), _dptr(workspace),
+        _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check(rc, "kvx_tree_commit")
