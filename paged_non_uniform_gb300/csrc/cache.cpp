@@ -30,17 +30,46 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need) {
   return ws && aligned(ws, 256) && bytes >= need;
 }
 
+// A 5-D bf16 tensor map over one head group's pool, dims (innermost first)
+// {64 elements, P slots, D/64 halves, |G| heads, pages}; one box {64, P, 1, 1,
+// 1} is a page's rows of one head and half, 128-byte swizzled, zeros outside.
+bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g) {
+  typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void *f = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                       &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || !f) {
+    cudaGetLastError();
+    return false;
+  }
+  const cuuint64_t row = (cuuint64_t)c->dev.row_bytes, P = (cuuint64_t)c->dev.P;
+  const cuuint64_t n = (cuuint64_t)g.size;
+  const cuuint64_t dims[5] = {64, P, row / 128, n, (cuuint64_t)g.pages};
+  const cuuint64_t strides[4] = {c->dev.token_major ? row * n : row, 128,
+                                 c->dev.token_major ? row : row * P, row * P * n};
+  const cuuint32_t box[5] = {64, (cuuint32_t)P, 1, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+  return ((Encode)f)(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims,
+                     strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Blocks of the attention kernel on the current device.
-int tree_blocks(const kvx_cache *, int *blocks) {
+int tree_blocks(const kvx_cache *c, int *blocks) {
   int32_t sms = 0;
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
-  *blocks = sms * tree_simt_blocks_per_sm();
+  *blocks = sms * (c->shape.dtype == KVX_F32 ? tree_simt_blocks_per_sm() : 1);
   return KVX_OK;
 }
 
 TreeWs tree_ws_layout(const kvx_cache *c, int max_q, int blocks, int *row_groups) {
-  const int rows = tree_simt_rows();
+  const int rows =
+      c->shape.dtype == KVX_F32 ? tree_simt_rows() : tree_mma_rows(max_q * c->dev.g);
   const size_t heads = (size_t)c->shape.B * c->shape.Hkv;
   const int groups = (max_q * c->dev.g + rows - 1) / rows;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -117,6 +146,10 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
   for (int gi = 0; gi < G; ++gi)
     d.grp[gi] = {page_tables[gi],  (char *)k_pools[gi],   (char *)v_pools[gi],
                  pool_pages[gi],   page_table_stride[gi], size[gi]};
+  c->have_maps = s->dtype == KVX_BF16;
+  for (int gi = 0; gi < G && c->have_maps; ++gi)
+    c->have_maps = encode_map(&c->k_maps[gi], c, d.grp[gi].k, d.grp[gi]) &&
+                   encode_map(&c->v_maps[gi], c, d.grp[gi].v, d.grp[gi]);
   *out = c;
   return KVX_OK;
 }
@@ -224,7 +257,13 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.words = (max_q + 31) / 32;
   const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
   p.scale_log2 = (float)((double)sc * 1.4426950408889634);
-  const cudaError_t e = launch_tree_simt(p, c->shape.dtype, blocks, (cudaStream_t)stream);
+  cudaError_t e;
+  if (c->shape.dtype == KVX_F32)
+    e = launch_tree_simt(p, blocks, (cudaStream_t)stream);
+  else if (c->have_maps)
+    e = launch_tree_mma(p, c->k_maps, c->v_maps, blocks, (cudaStream_t)stream);
+  else
+    e = cudaErrorInvalidValue;
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
 }
 

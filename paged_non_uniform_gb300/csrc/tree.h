@@ -94,14 +94,21 @@ struct TreeWs {
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t st);
-cudaError_t launch_tree_simt(const TreeParams &p, int dtype, int blocks, cudaStream_t st);
+// fp32 caches: CUDA cores; bf16 caches: tensor cores, one block per SM.
+cudaError_t launch_tree_simt(const TreeParams &p, int blocks, cudaStream_t st);
 int tree_simt_rows();           // query rows of a row group
 int tree_simt_blocks_per_sm();  // resident blocks
+cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
+                            const CUtensorMap *v_maps, int blocks, cudaStream_t st);
+int tree_mma_rows(int query_rows);  // query rows of a row group, of a head's largest number
 
 }  // namespace kvx
 
 struct kvx_cache {
   kvx_shape shape;
   kvx::CacheDev dev;
-  int32_t sms;  // of the device current at the first attention call; 0: not asked yet
+  // bf16 caches: maps of each group's pools (absent where no driver is loaded)
+  CUtensorMap k_maps[KVX_MAX_GROUPS];
+  CUtensorMap v_maps[KVX_MAX_GROUPS];
+  bool have_maps;
 };

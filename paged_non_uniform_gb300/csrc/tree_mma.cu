@@ -1,0 +1,614 @@
+// tree_mma.cu -- attention for a tree of drafted tokens, bf16 cache, on the
+// 5th-generation tensor cores (tcgen05).
+//
+// out[row] = sum_t softmax(scale * <q_row, k_t>)_t v_t over the cached tokens
+// of the row's KV head and the drafts its mask shows. The T_b * g query rows of
+// a KV head share its keys, so both products are dense: S [128 rows][128 keys]
+// = Q K^T and O [128 rows][D] += P V, with S, P and O in tensor memory. One
+// pass over the keys with a running maximum and sum per row. One block per SM
+// walks its items (tree_split.cuh) in tiles of 128 keys:
+//  * warps 8 and 9 load K and V tiles from their pages into two rings (bulk
+//    tensor loads, one box of min(P, 128) rows x 64 dims per lane, landing as
+//    [half][128 rows][128 bytes], 128-byte swizzled);
+//  * warp 10 issues the MMAs: S(j), then O += P V of job j - 1, so that one warp
+//    group's softmax runs under the other's products;
+//  * warps 0-3 and 4-7 are two softmax groups, one query row per thread. Up to
+//    128 query rows, both hold all rows and take the tiles in turn (their (m, l, O) are
+//    merged at the item's end); above, each holds half the rows and takes
+//    every tile. A job is one tile for one group;
+//  * warp 11 cleans the V tiles that hold drafts or the head's end: rows past
+//    the end are zeroed (stale or padding data), and non-finite values of drafts
+//    are replaced by zero and noted, because a weight of 0 does not silence them
+//    for rows that do not see the draft; the epilogue adds them to the rows that do.
+// P is kept as a bf16 high part and a bf16 residual (two products): with the
+// high part alone the weights would be off by 2^-9, with both by 2^-18, below
+// the fp32 output's other errors. They overwrite the scores they came from, column
+// block by column block.
+// The output is rescaled only when a row's maximum has grown by more than 2^8 since
+// its reference (the weights are then at most 2^8, exact in scale), which
+// after a row's first tile is rare; a row's sum and output share one reference.
+// Every mbarrier wait gives up after two seconds, sets KVX_DEV_TIMEOUT and lets
+// all roles run to their end without waiting, loading or multiplying.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <string.h>
+
+#include "tcgen05.cuh"
+#include "tree_split.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kTile = 128;       // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kSoft = 256;       // threads of the softmax groups
+constexpr int kMinUnits = 2;     // tiles a block takes at least
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kGrow = 8.f;     // log2 growth of the maximum that triggers a rescale
+constexpr int kNotes = 8;        // items in flight between cleaning and epilogue, rounded up
+
+// kTwo: launches with more than 128 query rows a head (two Q tiles).
+template <int D, bool kTwo>
+struct Cfg {
+  static constexpr int kRows = kTwo ? 256 : 128;  // query rows of an item
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kTile * 128;            // bytes of 64 dims of a tile
+  static constexpr int kTileBytes = kHalves * kHalf;   // a K, V or Q tile
+  static constexpr int kSlots = 7 * 2 / kHalves - (kTwo ? 2 : 1);  // of 224 KB, after Q
+  static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
+  static_assert(kV < kNotes, "notes of items in flight");
+  static constexpr int kBars = 2 * kK + 3 * kV + 7;
+  static constexpr int kQ = 0, kKs = (kTwo ? 2 : 1) * kTileBytes;
+  static constexpr int kVs = kKs + kK * kTileBytes, kCtl = kVs + kV * kTileBytes;
+  static constexpr int kSmem = 1024 + kCtl + kBars * 8 + 1024;
+};
+
+struct Ctl {  // small shared state behind the barriers
+  uint32_t tmem;
+  int flag;
+  int abort;
+  int pad;
+  int64_t warp_sum[kThreads / 32];
+  TreeRange range;
+  uint32_t notes[kNotes][4];  // drafts of an item whose V is not finite
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+struct alignas(128) MmaParams {
+  CUtensorMap tmK[KVX_MAX_GROUPS];
+  CUtensorMap tmV[KVX_MAX_GROUPS];
+  TreeParams t;
+};
+
+// Bounded wait for the phase of `bar` with the given parity. When it runs out, or
+// another role's has, waits end at once and the block runs down.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                     uint32_t *status) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return;
+    if (*abort) return;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      atomicOr(status, KVX_DEV_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// How an item is worked: two groups over all rows (tiles in turn), or a half of
+// the rows each (every tile).
+struct Jobs {
+  int rows, tiles, jobs;
+  bool halves;
+  __device__ __forceinline__ Jobs(const TreeItem &it, int g, int max_rows) {
+    rows = min(max_rows, it.head.T * g - it.group * max_rows);
+    tiles = it.t1 - it.t0;
+    halves = rows > 128;
+    jobs = halves ? 2 * tiles : tiles;
+  }
+  __device__ __forceinline__ int tile(int j) const { return halves ? j >> 1 : j; }
+  __device__ __forceinline__ bool opens(int j) const { return !halves || (j & 1) == 0; }
+  __device__ __forceinline__ bool closes(int j) const { return !halves || (j & 1) == 1; }
+};
+
+// Visible keys of word c (32 keys) of the tile whose first key is draft `u0`
+// (negative: that many cached tokens first), for a row with mask words m.
+__device__ __forceinline__ uint32_t seen_word(int u0, const uint32_t (&m)[4]) {
+  if (u0 <= -32) return 0xffffffffu;
+  if (u0 < 0) return ((1u << -u0) - 1u) | (m[0] << -u0);
+  const int w = u0 >> 5, s = u0 & 31;
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i == w) lo = m[i];
+    if (i == w + 1) hi = m[i];
+  }
+  return s ? (lo >> s) | (hi << (32 - s)) : lo;
+}
+
+// One warp's part of one role's loads: all K (or V) tiles of the block.
+template <int D, bool kTwo, bool kIsV>
+__device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &range,
+                                        uint32_t ring, uint32_t full0, uint32_t empty0,
+                                        volatile int *abort, int lane) {
+  using C = Cfg<D, kTwo>;
+  constexpr int kN = kIsV ? C::kV : C::kK;
+  const TreeParams &p = mp.t;
+  const uint64_t pol = policy_evict_first();
+  const int P = p.c.P, box = min(P, kTile);
+  const int per = kTile / box;  // boxes of a tile and half
+  TreeCursor<kTile, C::kRows> cur(p, range);
+  TreeItem it;
+  int n = 0;
+  while (cur.next(p, it)) {
+    const CacheGroup &grp = p.c.grp[p.c.head_grp[it.head.h]];
+    const int rank = p.c.head_row[it.head.h], len = it.head.n + it.head.T;
+    const int32_t *table = grp.table + (size_t)it.head.b * grp.stride;
+    const void *map = kIsV ? &mp.tmV[p.c.head_grp[it.head.h]] : &mp.tmK[p.c.head_grp[it.head.h]];
+    // lane -> (box, half); a tile has at most 16 * 2 of them
+    const int bx = lane % per, half = lane / per;
+    auto page_of = [&](int tile) {
+      const int tok = tile * kTile + bx * box;
+      return half < C::kHalves && tok < len ? __ldg(table + (tok >> p.c.lgP)) : 0;
+    };
+    int page = page_of(it.t0);
+    for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
+      const int slot = n % kN, valid = min(kTile, len - tile * kTile);
+      const int boxes = (valid + box - 1) / box;
+      const int next = tile + 1 < it.t1 ? page_of(tile + 1) : 0;
+      if (n >= kN) wait(empty0 + 8 * slot, ((n / kN) - 1) & 1, abort, p.status);
+      if (__any_sync(0xffffffffu, *abort)) return;
+      const uint32_t full = full0 + 8 * slot;
+      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * box * 128 * C::kHalves));
+      __syncwarp();
+      if (half < C::kHalves && bx < boxes) {
+        int pg = page;
+        if (page < 0 || (int64_t)page >= grp.pages) {
+          atomicOr(p.status, KVX_DEV_BAD_PAGE);
+          pg = (int)grp.pages;  // past the last page: loads zeros
+        }
+        const int tok = tile * kTile + bx * box;
+        tma_load_5d(ring + slot * C::kTileBytes + half * C::kHalf + bx * box * 128, map, 0,
+                    tok & (P - 1), half, rank, pg, full, pol);
+      }
+      page = next;
+    }
+  }
+}
+
+template <int D, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_constant__ MmaParams mp) {
+  using C = Cfg<D, kTwo>;
+  const TreeParams &p = mp.t;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem);
+  uint64_t *bars = (uint64_t *)(smem + C::kCtl);
+  Ctl &ctl = *(Ctl *)(bars + C::kBars);
+  volatile int *abort = &ctl.abort;
+  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 8 * C::kK;
+  const uint32_t v_full = k_empty + 8 * C::kK, v_empty = v_full + 8 * C::kV;
+  const uint32_t v_ready = v_empty + 8 * C::kV;  // loaded, and cleaned where it has to be
+  const uint32_t s_full = v_ready + 8 * C::kV;   // [2] scores of a group are ready
+  const uint32_t p_ready = s_full + 16;         // [2] weights of a group are ready
+  const uint32_t o_full = p_ready + 16;         // [2] a group's output of the item is complete
+  const uint32_t q_ready = o_full + 16;         // Q of the item is loaded, O may be overwritten
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < C::kK; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(v_ready + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, 4);
+      mbar_init(o_full + 8 * i, 1);
+    }
+    mbar_init(q_ready, kSoft / 32);
+    ctl.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 10) tmem_alloc(smem_u32(&ctl.tmem), 512);
+  if (warp >= 8 && warp < 10 && lane < p.c.G)
+    prefetch_tensormap(warp == 8 ? &mp.tmK[lane] : &mp.tmV[lane]);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  // columns: S of both groups, O of both groups
+  const uint32_t tS = tmem, tO = tmem + 2 * kTile;
+  pdl_wait();
+  const TreeRange range =
+      tree_range<kThreads, kTile, C::kRows>(p, kMinUnits, ctl.warp_sum, &ctl.range);
+  const int g = p.c.g;
+
+  if (warp == 8) {
+    produce<D, kTwo, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
+  } else if (warp == 9) {
+    produce<D, kTwo, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
+  } else if (warp == 10) {
+    if (lane == 0) {
+      constexpr uint32_t kS = mma_desc(128, kTile, false), kO = mma_desc(128, D, true);
+      TreeCursor<kTile, C::kRows> cur(p, range);
+      TreeItem it;
+      int items = 0, nk = 0, nv = 0;
+      int np[2] = {0, 0};
+      while (cur.next(p, it)) {
+        const Jobs jb(it, g, C::kRows);
+        wait(q_ready, items & 1, abort, p.status);
+        tc_fence_after();
+        auto weigh = [&](int j) {  // O += P V of job j
+          const int w = j & 1, slot = nv % C::kV;
+          if (jb.opens(j)) wait(v_ready + 8 * slot, (nv / C::kV) & 1, abort, p.status);
+          wait(p_ready + 8 * w, np[w]++ & 1, abort, p.status);
+          tc_fence_after();
+          if (!*abort) {
+            const bool first = j < 2;  // of its group: overwrites O
+            const uint32_t v = base + C::kVs + slot * C::kTileBytes;
+            const uint32_t a = tS + w * kTile, d = tO + w * 128;
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i) {
+              const uint64_t b = smem_desc(v + i * 16 * 128, C::kHalf);
+              const uint32_t hi = a + 32 * (i >> 1) + 8 * (i & 1);
+              mma_ts(d, hi, b, kO, !(first && i == 0));
+              mma_ts(d, hi + 16, b, kO, true);
+            }
+          }
+          if (jb.closes(j)) {
+            mma_commit(v_empty + 8 * slot);
+            ++nv;
+          }
+          if (j + 2 >= jb.jobs) mma_commit(o_full + 8 * w);
+        };
+        for (int j = 0; j < jb.jobs; ++j) {
+          const int w = j & 1, slot = nk % C::kK;
+          if (jb.opens(j)) wait(k_full + 8 * slot, (nk / C::kK) & 1, abort, p.status);
+          if (!*abort) {
+            // S of this group was last read by the products of job j - 2, issued before:
+            // MMAs of one thread run in the order of issue
+            const uint32_t q = base + C::kQ + (jb.halves ? w * C::kTileBytes : 0);
+            const uint32_t k = base + C::kKs + slot * C::kTileBytes;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = (i >> 2) * C::kHalf + (i & 3) * 32;
+              mma_ss(tS + w * kTile, smem_desc(q + off, 16), smem_desc(k + off, 16), kS, i > 0);
+            }
+          }
+          mma_commit(s_full + 8 * w);
+          if (jb.closes(j)) {
+            mma_commit(k_empty + 8 * slot);
+            ++nk;
+          }
+          if (j > 0) weigh(j - 1);
+        }
+        weigh(jb.jobs - 1);
+        ++items;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    TreeCursor<kTile, C::kRows> cur(p, range);
+    TreeItem it;
+    int items = 0, n = 0;
+    while (cur.next(p, it)) {
+      const int len = it.head.n + it.head.T;
+      uint32_t notes[4] = {0, 0, 0, 0};
+      for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
+        const int slot = n % C::kV, t0 = tile * kTile;
+        wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p.status);
+        if (t0 + kTile > it.head.n) {
+          const int first = max(0, it.head.n - t0), valid = min(kTile, len - t0);
+          uint8_t *v = smem + C::kVs + slot * C::kTileBytes;
+          for (int row = first; row < kTile; ++row) {
+            // a row is 8 chunks of 16 bytes in each half: lanes 0-7 and 8-15
+            uint4 *at = (uint4 *)(v + (lane >> 3) * C::kHalf + row * 128 + (lane & 7) * 16);
+            if (row >= valid) {
+              if (lane < 8 * C::kHalves) *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            bool odd = false;
+            if (lane < 8 * C::kHalves) {
+              uint4 x = *at;
+              uint32_t *e = &x.x;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = (e[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+                const uint32_t hi = (e[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+                odd |= (lo | hi) != 0;
+                e[i] &= ~(lo | hi);
+              }
+              if (odd) *at = x;
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+              const int u = t0 + row - it.head.n;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i == (u >> 5)) notes[i] |= 1u << (u & 31);
+            }
+          }
+          if (lane < 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i == lane) ctl.notes[items % kNotes][i] = notes[i];
+          }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_ready + 8 * slot);
+      }
+      ++items;
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int w = warp >> 2;                       // group
+    const int lr = (warp & 3) * 32 + lane;         // TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tS + w * kTile + lanes;
+    TreeCursor<kTile, C::kRows> cur(p, range);
+    TreeItem it;
+    int ns = 0, items = 0;
+    int no[2] = {0, 0};
+    while (cur.next(p, it)) {
+      const TreeHead &hd = it.head;
+      const Jobs jb(it, g, C::kRows);
+      const int r0 = it.group * C::kRows;
+      // ---- Q rows into shared memory
+      {
+        constexpr int CPR = D / 8;  // 16-byte chunks of a row
+        for (int i = tid; i < jb.rows * CPR; i += kSoft) {
+          const int r = i / CPR, c = i - r * CPR;
+          const int nr = (r0 + r) / g, j = (r0 + r) - nr * g;
+          const uint4 x = __ldg((const uint4 *)(p.q + (size_t)(hd.q0 + nr) * p.q_stride +
+                                                ((size_t)hd.h * g + j) * (D * 2) + c * 16));
+          *(uint4 *)(smem + C::kQ + (r >> 7) * C::kTileBytes + (c >> 3) * C::kHalf +
+                     (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+      }
+      const int row = jb.halves ? 128 * w + lr : lr;
+      const bool live = (jb.halves ? 128 * w : 0) + (warp & 3) * 32 < jb.rows;  // of the warp
+      float m = -INFINITY, l = 0.f;  // reference of the weights (log2 units), sum
+      for (int j = w; j < jb.jobs; j += 2) {
+        const int tile = it.t0 + jb.tile(j), t0 = tile * kTile;
+        wait(s_full + 8 * w, ns++ & 1, abort, p.status);
+        tc_fence_after();
+        if (live) {
+          const bool edge = t0 + kTile > hd.n;
+          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+          if (edge) {
+            uint32_t mw[4] = {0, 0, 0, 0};
+            if (row < jb.rows) {
+              const int nr = (r0 + row) / g;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mw[i] = tree_mask_word(p, hd, nr, i);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) seen[c] = seen_word(t0 + 32 * c - hd.n, mw);
+          }
+          float mx = -INFINITY;
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(s_at + 32 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float s = __uint_as_float(x[e]);
+              if (edge) s = (seen[c] >> e) & 1u ? s : -INFINITY;
+              mx = fmaxf(mx, s);
+            }
+          }
+          mx *= p.scale_log2;
+          // a new reference for rows that have seen nothing before, or whose
+          // maximum has grown by more than kGrow
+          const bool move = mx > m + kGrow || (m == -INFINITY && mx != -INFINITY);
+          const float mn = move ? mx : m;
+          if (j >= 2 && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+            const float f = move ? tree_weight(m, mn) : 1.f;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t at = tO + w * 128 + lanes + 32 * c;
+              tmem_ld32(at, x);
+              tmem_wait_ld(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+              tmem_st32(at, x);
+            }
+          }
+          m = mn;
+          const float ref = m == -INFINITY ? 0.f : m;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(s_at + 32 * c, x);
+            tmem_wait_ld(x);
+            uint32_t y[32];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float a = ex2(fmaf(__uint_as_float(x[e]), p.scale_log2, -ref));
+              float b = ex2(fmaf(__uint_as_float(x[e + 1]), p.scale_log2, -ref));
+              if (edge) {
+                a = (seen[c] >> e) & 1u ? a : 0.f;
+                b = (seen[c] >> (e + 1)) & 1u ? b : 0.f;
+              }
+              sum0 += a;
+              sum1 += b;
+              const uint32_t hi = pack_bf16(a, b);
+              y[e >> 1] = hi;
+              y[16 + (e >> 1)] = pack_bf16(a - __uint_as_float(hi << 16),
+                                           b - __uint_as_float(hi & 0xffff0000u));
+            }
+            tmem_st32(s_at + 32 * c, y);
+          }
+          l += sum0 + sum1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + 8 * w);
+      }
+      // ---- epilogue
+      // (a half waits for its own output alone; the barrier before the next item
+      // makes the other's phase known)
+      if (!jb.halves || w == 0) wait(o_full, no[0] & 1, abort, p.status);
+      if (jb.halves ? w == 1 : jb.jobs > 1) wait(o_full + 8, no[1] & 1, abort, p.status);
+      ++no[0];
+      no[1] += jb.jobs > 1;
+      tc_fence_after();
+      const bool whole = tree_whole(it);
+      uint32_t any = 0;
+      if (it.t1 * kTile > hd.n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= ctl.notes[items % kNotes][i];
+      }
+      float f0 = 1.f, f1 = 0.f, M = m, L = l;
+      if (!jb.halves) {
+        // both groups hold partial states of the same rows; Q is no longer read
+        float2 *ml = (float2 *)(smem + C::kQ);
+        ml[w * 128 + lr] = make_float2(m, l);
+        named_sync(1, kSoft);
+        const float2 a = ml[lr], b = ml[128 + lr];
+        M = fmaxf(a.x, b.x);
+        f0 = tree_weight(a.x, M);
+        f1 = tree_weight(b.x, M);
+        L = f0 * a.y + f1 * b.y;
+      }
+      if (live) {
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        const size_t part = (size_t)tree_slot(range, it) * C::kRows + row;
+        float *dst = nullptr;
+        if (row < jb.rows) {
+          dst = whole ? tree_out(p, hd, r0 + row) : p.part_o + part * D;
+          if (!whole && (jb.halves || w == 0)) p.part_ml[part] = make_float2(M, L);
+        }
+        if (jb.halves) {
+          f0 = w == 0 ? 1.f : 0.f;
+          f1 = 1.f - f0;
+        }
+        const int c0 = jb.halves ? 0 : w * (D / 64), c1 = jb.halves ? D / 32 : c0 + D / 64;
+        for (int c = c0; c < c1; ++c) {
+          uint32_t x[32];
+          float o[32];
+          const bool use0 = !jb.halves || w == 0, use1 = jb.halves ? w == 1 : jb.jobs > 1;
+          if (use0) {
+            tmem_ld32(tO + lanes + 32 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = f0 * __uint_as_float(x[e]);
+          }
+          if (use1) {
+            tmem_ld32(tO + 128 + lanes + 32 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = use0 ? fmaf(f1, __uint_as_float(x[e]), o[e]) : f1 * __uint_as_float(x[e]);
+          }
+          if (any && row < jb.rows) {
+            // non-finite values of drafts this row sees (their weight is positive)
+            const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
+#pragma unroll 1
+            for (int u = 0; u < hd.T; ++u) {
+              const uint32_t bit = 1u << (u & 31);
+              if (!(ctl.notes[items % kNotes][u >> 5] & bit) ||
+                  !(tree_mask_word(p, hd, (r0 + row) / g, u >> 5) & bit))
+                continue;
+              const int tok = hd.n + u;
+              const int64_t pg = grp.table[(size_t)hd.b * grp.stride + (tok >> p.c.lgP)];
+              if (pg < 0 || pg >= grp.pages) continue;
+              const char *v = grp.v + pool_row(p.c, grp, pg, p.c.head_row[hd.h],
+                                               tok & (p.c.P - 1)) * (D * 2);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float b = __uint_as_float(
+                    (uint32_t)__ldg((const uint16_t *)v + 32 * c + e) << 16);
+                if (!isfinite(b)) o[e] += b;
+              }
+            }
+          }
+          if (dst) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *(float4 *)(dst + 32 * c + e) =
+                  make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          }
+        }
+      }
+      tc_fence_before();
+      if (!whole) {
+        tree_publish<D, kSoft, kTile, C::kRows>(p, range, it, tid, &ctl.flag,
+                                                [] { named_sync(1, kSoft); });
+      } else {
+        named_sync(1, kSoft);  // (m, l) in Q's place are read
+      }
+      ++items;
+    }
+  }
+  __syncthreads();
+  // Run-down: nothing of this block may still be landing when it leaves. The
+  // roles above end with every load consumed and every product waited for,
+  // unless a wait ran out.
+  if (*abort) {
+    if (tid == 0) {
+      // bounded: bulk loads land within microseconds of their issue
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 20000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 10) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <int D, bool kTwo>
+cudaError_t launch_dt(const MmaParams &mp, int blocks, cudaStream_t st) {
+  using C = Cfg<D, kTwo>;
+  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, kTwo>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, kTwo>, mp);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+int tree_mma_rows(int query_rows) { return query_rows > 128 ? 256 : 128; }
+
+cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
+                            const CUtensorMap *v_maps, int blocks, cudaStream_t st) {
+  MmaParams mp;
+  memcpy(mp.tmK, k_maps, sizeof(mp.tmK));
+  memcpy(mp.tmV, v_maps, sizeof(mp.tmV));
+  mp.t = p;
+  const bool two = p.max_q * p.c.g > 128;
+  if (p.c.D == 128)
+    return two ? launch_dt<128, true>(mp, blocks, st) : launch_dt<128, false>(mp, blocks, st);
+  return two ? launch_dt<64, true>(mp, blocks, st) : launch_dt<64, false>(mp, blocks, st);
+}
+
+}  // namespace kvx

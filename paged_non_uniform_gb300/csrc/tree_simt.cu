@@ -1,17 +1,16 @@
-// tree_simt.cu -- attention for a tree of drafted tokens on the CUDA cores,
-// fp32 arithmetic.
+// tree_simt.cu -- attention for a tree of drafted tokens, fp32 cache, on the
+// CUDA cores.
 //
 // out[row] = sum_t softmax(scale * <q_row, k_t>)_t v_t over the cached tokens
 // of the row's KV head and the drafts its mask shows, with one pass over the
 // keys per group of 32 query rows (running maximum and sum in fp32). A block
 // walks its items (tree_split.cuh) in tiles of 64 keys: K and V tiles are
-// gathered from their pages into shared memory as fp32, each thread computes a
+// gathered from their pages into shared memory, each thread computes a
 // 4 x 4 block of scores, the row maxima and sums meet in half-warp shuffles,
 // and each thread accumulates 4 rows x D/16 dims of the output.
 // A tile that holds drafts or the head's end takes a separate path that skips
 // what a row does not see instead of multiplying it by zero, so that NaN and
 // infinities in unseen rows, and padding, have no influence.
-#include <cuda_bf16.h>
 #include <math.h>
 
 #include "tree_split.cuh"
@@ -36,29 +35,11 @@ struct Smem {
   int flag;
 };
 
-template <typename T>
-__device__ __forceinline__ void load16(const char *src, float *dst);
-template <>
-__device__ __forceinline__ void load16<float>(const char *src, float *dst) {
-  *(float4 *)dst = *(const float4 *)src;
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const char *src, float *dst) {
-  const uint4 v = *(const uint4 *)src;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    dst[2 * i] = __uint_as_float(w[i] << 16);
-    dst[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ float4 smem_raw[];
   Smem<D> &sm = *(Smem<D> *)smem_raw;
-  constexpr int E = 16 / sizeof(T);  // elements of a 16-byte chunk
-  constexpr int CPR = D / E;         // chunks of a row
+  constexpr int CPR = D / 4;  // 16-byte chunks of a row
   constexpr int ND = D / 64;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_launch_dependents();
@@ -76,15 +57,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
     __syncthreads();  // the item before is done with shared memory
     for (int i = tid; i < kRows * CPR; i += kThreads) {
       const int r = i / CPR, c = i - r * CPR;
-      float *dst = &sm.q[r][c * E];
+      float *dst = &sm.q[r][c * 4];
       if (r < rows) {
         const int nr = (r0 + r) / g, j = (r0 + r) - nr * g;
-        load16<T>(p.q + (size_t)(hd.q0 + nr) * p.q_stride +
-                      ((size_t)hd.h * g + j) * p.c.row_bytes + c * 16,
-                  dst);
+        *(float4 *)dst = __ldg((const float4 *)(p.q + (size_t)(hd.q0 + nr) * p.q_stride +
+                                               ((size_t)hd.h * g + j) * (D * 4) + c * 16));
       } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[e] = 0.f;
+        *(float4 *)dst = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
     float m[4], l[4], o[4][ND][4];
@@ -101,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
       __syncthreads();                      // the tile before is consumed
       for (int i = tid; i < kTile * CPR; i += kThreads) {
         const int t = i / CPR, c = i - t * CPR;
-        float *dk = &sm.k[t][c * E], *dv = &sm.v[t][c * E];
+        float *dk = &sm.k[t][c * 4], *dv = &sm.v[t][c * 4];
         bool have = t < valid;
         if (have) {
           const int tok = t0 + t;
@@ -110,16 +89,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
           if (!have) {
             if (c == 0) atomicOr(p.status, KVX_DEV_BAD_PAGE);
           } else {
-            const int64_t at =
-                pool_row(p.c, grp, page, rank, tok & (P - 1)) * p.c.row_bytes + c * 16;
-            load16<T>(grp.k + at, dk);
-            load16<T>(grp.v + at, dv);
+            const int64_t at = pool_row(p.c, grp, page, rank, tok & (P - 1)) * (D * 4) + c * 16;
+            *(float4 *)dk = *(const float4 *)(grp.k + at);
+            *(float4 *)dv = *(const float4 *)(grp.v + at);
           }
         }
-        if (!have) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) dk[e] = dv[e] = 0.f;
-        }
+        if (!have) *(float4 *)dk = *(float4 *)dv = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       if (edge && tid < 2 * kRows) {
         // visible keys of row r, word w: bits [32w, 32w + 32) of the tile
@@ -265,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_td(const TreeParams &p, int blocks, cudaStream_t st) {
+template <int D>
+cudaError_t launch_d(const TreeParams &p, int blocks, cudaStream_t st) {
   const int bytes = (int)sizeof(Smem<D>);
-  cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<T, D>,
+  cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -281,7 +256,7 @@ cudaError_t launch_td(const TreeParams &p, int blocks, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_simt_kernel<T, D>, p);
+  e = cudaLaunchKernelEx(&cfg, tree_simt_kernel<D>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -290,11 +265,8 @@ cudaError_t launch_td(const TreeParams &p, int blocks, cudaStream_t st) {
 int tree_simt_rows() { return kRows; }
 int tree_simt_blocks_per_sm() { return 2; }
 
-cudaError_t launch_tree_simt(const TreeParams &p, int dtype, int blocks, cudaStream_t st) {
-  if (dtype == KVX_F32)
-    return p.c.D == 128 ? launch_td<float, 128>(p, blocks, st) : launch_td<float, 64>(p, blocks, st);
-  return p.c.D == 128 ? launch_td<__nv_bfloat16, 128>(p, blocks, st)
-                      : launch_td<__nv_bfloat16, 64>(p, blocks, st);
+cudaError_t launch_tree_simt(const TreeParams &p, int blocks, cudaStream_t st) {
+  return p.c.D == 128 ? launch_d<128>(p, blocks, st) : launch_d<64>(p, blocks, st);
 }
 
 }  // namespace kvx
