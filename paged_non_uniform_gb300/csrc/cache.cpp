@@ -77,7 +77,10 @@ TreeWs tree_ws_layout(const kvx_cache *c, int max_q, int blocks, int *row_groups
   w.counters = KVX_WS_HEADER_BYTES;
   w.part_ml = w.counters + up(heads * groups * sizeof(int32_t));
   w.part_o = w.part_ml + up((size_t)2 * blocks * rows * sizeof(float2));
-  w.total = w.part_o + up((size_t)2 * blocks * rows * c->shape.D * sizeof(float));
+  w.fold = w.part_o + up((size_t)2 * blocks * rows * c->shape.D * sizeof(float));
+  w.total = w.fold;
+  if (c->shape.dtype == KVX_BF16)
+    w.total += up((size_t)2 * blocks * 128 * c->shape.D * sizeof(float));
   if (row_groups) *row_groups = groups;
   return w;
 }
@@ -252,6 +255,7 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.counters = (int32_t *)(ws + w.counters);
   p.part_ml = (float2 *)(ws + w.part_ml);
   p.part_o = (float *)(ws + w.part_o);
+  p.fold = (float *)(ws + w.fold);
   p.max_rows = max_rows;
   p.max_q = max_q;
   p.words = (max_q + 31) / 32;

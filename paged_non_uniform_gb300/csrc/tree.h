@@ -81,14 +81,15 @@ struct TreeParams {
   int32_t *counters;  // [B * Hkv][row groups] finished pieces, back to 0 after the merge
   float2 *part_ml;    // [2 * blocks][rows of a group] = (max in log2 units, sum)
   float *part_o;      // [2 * blocks][rows of a group][D]
+  float *fold;        // tensor-core kernel: fp32 output sums of long items, [2 * blocks][D / 4][128][4]
   int32_t max_rows, max_q, words;  // words: uint32 words of a mask row
   int32_t row_groups;              // most row groups of a head
   float scale_log2;                // scale * log2(e)
 };
 
-// Workspace of tree attention: header | counters | partial (m, l) | partial o.
+// Workspace of tree attention: header | counters | partial (m, l) | partial o | folded o.
 struct TreeWs {
-  size_t counters, part_ml, part_o, total;
+  size_t counters, part_ml, part_o, fold, total;
 };
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st);

@@ -45,6 +45,11 @@ constexpr int kSoft = 256;       // threads of the softmax groups
 constexpr int kMinUnits = 2;     // tiles a block takes at least
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.f;     // log2 growth of the maximum that triggers a rescale
+// Tiles of a group after which its output leaves tensor memory for an fp32 sum: the
+// tensor cores truncate each of the 16 additions a tile makes to every output
+// element, which over 200 tiles was measured as 5e-5 of the output, growing
+// linearly; over 16 tiles it stays below 5e-6.
+constexpr int kFold = 16;
 constexpr int kNotes = 8;        // items in flight between cleaning and epilogue, rounded up
 
 // kTwo: launches with more than 128 query rows a head (two Q tiles).
@@ -128,6 +133,68 @@ __device__ __forceinline__ uint32_t seen_word(int u0, const uint32_t (&m)[4]) {
     if (i == w + 1) hi = m[i];
   }
   return s ? (lo >> s) | (hi << (32 - s)) : lo;
+}
+
+// One row's softmax of one tile: scores (TMEM) to weights (TMEM, in place), the
+// running reference m and sum l. All 128 scores stay in registers between the
+// maximum and the exponentials. kEdge: keys of clear `seen` bits are left out.
+// have: O holds products of earlier tiles, which a new reference rescales.
+template <int D, bool kEdge>
+__device__ __forceinline__ void soft_tile(uint32_t s_at, uint32_t o_at, const uint32_t (&seen)[4],
+                                          float scale, bool have, float &m, float &l) {
+  uint32_t x[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_wait_ld(x[c]);
+    mx[c] = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      if (kEdge && !((seen[c] >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+      mx[c] = fmaxf(mx[c], __uint_as_float(x[c][e]));
+    }
+  }
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+  // a new reference for rows that have seen nothing before, or whose maximum
+  // has grown by more than kGrow
+  const bool move = top > m + kGrow;
+  const float mn = move ? top : m;
+  const float f = move ? tree_weight(m, mn) : 1.f;
+  l *= f;
+  if (have && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t y[16];
+      tmem_ld16(o_at + 16 * c, y);
+      tmem_wait_ld(y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+      tmem_st16(o_at + 16 * c, y);
+    }
+  }
+  m = mn;
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[32];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float a = ex2(fmaf(__uint_as_float(x[c][e]), scale, -ref));
+      const float b = ex2(fmaf(__uint_as_float(x[c][e + 1]), scale, -ref));
+      sum[e & 2] += a;
+      sum[(e & 2) + 1] += b;
+      const uint32_t hi = pack_bf16(a, b);
+      y[e >> 1] = hi;
+      y[16 + (e >> 1)] = pack_bf16(a - __uint_as_float(hi << 16),
+                                   b - __uint_as_float(hi & 0xffff0000u));
+    }
+    tmem_st32(s_at + 32 * c, y);
+  }
+  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  tmem_wait_st();
 }
 
 // One warp's part of one role's loads: all K (or V) tiles of the block.
@@ -232,6 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
       tree_range<kThreads, kTile, C::kRows>(p, kMinUnits, ctl.warp_sum, &ctl.range);
   const int g = p.c.g;
 
+  // the softmax groups take registers from the other roles: 256 * 208 + 128 * 88
+  // = 384 * 168, the launch's
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 8) {
     produce<D, kTwo, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
   } else if (warp == 9) {
@@ -253,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
           wait(p_ready + 8 * w, np[w]++ & 1, abort, p.status);
           tc_fence_after();
           if (!*abort) {
-            const bool first = j < 2;  // of its group: overwrites O
+            const bool first = ((j >> 1) % kFold) == 0;  // overwrites O
             const uint32_t v = base + C::kVs + slot * C::kTileBytes;
             const uint32_t a = tS + w * kTile, d = tO + w * 128;
 #pragma unroll
@@ -296,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else {
     TreeCursor<kTile, C::kRows> cur(p, range);
     TreeItem it;
     int items = 0, n = 0;
@@ -348,12 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
       }
       ++items;
     }
+  }
   } else {
     // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int w = warp >> 2;                       // group
     const int lr = (warp & 3) * 32 + lane;         // TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tS + w * kTile + lanes;
+    const uint32_t s_at = tS + w * kTile + lanes, o_at = tO + w * 128 + lanes;
+    auto fold_at = [&](int grp, int r) {  // float4 index: a thread's are 128 apart
+      return ((size_t)blockIdx.x * 2 + grp) * (D / 4) * 128 + r;
+    };
     TreeCursor<kTile, C::kRows> cur(p, range);
     TreeItem it;
     int ns = 0, items = 0;
@@ -380,15 +456,39 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
       const int row = jb.halves ? 128 * w + lr : lr;
       const bool live = (jb.halves ? 128 * w : 0) + (warp & 3) * 32 < jb.rows;  // of the warp
       float m = -INFINITY, l = 0.f;  // reference of the weights (log2 units), sum
+      float m_acc = -INFINITY;       // reference of the folded output
+      bool folded = false;           // (of the group: every thread folds at the same tiles)
       for (int j = w; j < jb.jobs; j += 2) {
         const int tile = it.t0 + jb.tile(j), t0 = tile * kTile;
         wait(s_full + 8 * w, ns++ & 1, abort, p.status);
         tc_fence_after();
         if (live) {
-          const bool edge = t0 + kTile > hd.n;
-          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-          if (edge) {
-            uint32_t mw[4] = {0, 0, 0, 0};
+          const bool turn = j >= 2 && ((j >> 1) % kFold) == 0;  // O starts afresh
+          if (turn) {
+            // fold the tensor cores' sum of the last kFold tiles into fp32 (see kFold)
+            const float f = tree_weight(m_acc, m);
+            float4 *acc = (float4 *)p.fold + fold_at(w, lr);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(o_at + 32 * c, x);
+              tmem_wait_ld(x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (folded) v = __ldcg(acc + (8 * c + e) * 128);
+                v.x = fmaf(v.x, f, __uint_as_float(x[4 * e]));
+                v.y = fmaf(v.y, f, __uint_as_float(x[4 * e + 1]));
+                v.z = fmaf(v.z, f, __uint_as_float(x[4 * e + 2]));
+                v.w = fmaf(v.w, f, __uint_as_float(x[4 * e + 3]));
+                __stcg(acc + (8 * c + e) * 128, v);
+              }
+            }
+            m_acc = m;
+            folded = true;
+          }
+          if (t0 + kTile > hd.n) {
+            uint32_t mw[4] = {0, 0, 0, 0}, seen[4];
             if (row < jb.rows) {
               const int nr = (r0 + row) / g;
 #pragma unroll
@@ -396,65 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) seen[c] = seen_word(t0 + 32 * c - hd.n, mw);
+            soft_tile<D, true>(s_at, o_at, seen, p.scale_log2, j >= 2 && !turn, m, l);
+          } else {
+            const uint32_t all[4] = {~0u, ~0u, ~0u, ~0u};
+            soft_tile<D, false>(s_at, o_at, all, p.scale_log2, j >= 2 && !turn, m, l);
           }
-          float mx = -INFINITY;
-          uint32_t x[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_at + 32 * c, x);
-            tmem_wait_ld(x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float s = __uint_as_float(x[e]);
-              if (edge) s = (seen[c] >> e) & 1u ? s : -INFINITY;
-              mx = fmaxf(mx, s);
-            }
-          }
-          mx *= p.scale_log2;
-          // a new reference for rows that have seen nothing before, or whose
-          // maximum has grown by more than kGrow
-          const bool move = mx > m + kGrow || (m == -INFINITY && mx != -INFINITY);
-          const float mn = move ? mx : m;
-          if (j >= 2 && __any_sync(0xffffffffu, move && m != -INFINITY)) {
-            const float f = move ? tree_weight(m, mn) : 1.f;
-            l *= f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              const uint32_t at = tO + w * 128 + lanes + 32 * c;
-              tmem_ld32(at, x);
-              tmem_wait_ld(x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-              tmem_st32(at, x);
-            }
-          }
-          m = mn;
-          const float ref = m == -INFINITY ? 0.f : m;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_at + 32 * c, x);
-            tmem_wait_ld(x);
-            uint32_t y[32];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float a = ex2(fmaf(__uint_as_float(x[e]), p.scale_log2, -ref));
-              float b = ex2(fmaf(__uint_as_float(x[e + 1]), p.scale_log2, -ref));
-              if (edge) {
-                a = (seen[c] >> e) & 1u ? a : 0.f;
-                b = (seen[c] >> (e + 1)) & 1u ? b : 0.f;
-              }
-              sum0 += a;
-              sum1 += b;
-              const uint32_t hi = pack_bf16(a, b);
-              y[e >> 1] = hi;
-              y[16 + (e >> 1)] = pack_bf16(a - __uint_as_float(hi << 16),
-                                           b - __uint_as_float(hi & 0xffff0000u));
-            }
-            tmem_st32(s_at + 32 * c, y);
-          }
-          l += sum0 + sum1;
-          tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
@@ -474,17 +520,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) any |= ctl.notes[items % kNotes][i];
       }
-      float f0 = 1.f, f1 = 0.f, M = m, L = l;
+      float M = m, L = l;
+      float f[2] = {1.f, 1.f};                      // weights of the groups' outputs
+      float fa[2] = {0.f, 0.f};                     // and of their folded parts
+      bool use[2] = {w == 0, w == 1};               // groups this thread's output comes from
+      const bool folds[2] = {jb.jobs > 2 * kFold, jb.jobs > 2 * kFold + 1};
+      fa[w] = tree_weight(m_acc, m);
       if (!jb.halves) {
         // both groups hold partial states of the same rows; Q is no longer read
-        float2 *ml = (float2 *)(smem + C::kQ);
-        ml[w * 128 + lr] = make_float2(m, l);
+        float4 *st = (float4 *)(smem + C::kQ);
+        st[w * 128 + lr] = make_float4(m, l, fa[w], 0.f);
         named_sync(1, kSoft);
-        const float2 a = ml[lr], b = ml[128 + lr];
+        const float4 a = st[lr], b = st[128 + lr];
         M = fmaxf(a.x, b.x);
-        f0 = tree_weight(a.x, M);
-        f1 = tree_weight(b.x, M);
-        L = f0 * a.y + f1 * b.y;
+        f[0] = tree_weight(a.x, M);
+        f[1] = tree_weight(b.x, M);
+        L = f[0] * a.y + f[1] * b.y;
+        fa[0] = a.z;
+        fa[1] = b.z;
+        use[0] = true;
+        use[1] = jb.jobs > 1;
       }
       if (live) {
         const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
@@ -494,27 +549,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
           dst = whole ? tree_out(p, hd, r0 + row) : p.part_o + part * D;
           if (!whole && (jb.halves || w == 0)) p.part_ml[part] = make_float2(M, L);
         }
-        if (jb.halves) {
-          f0 = w == 0 ? 1.f : 0.f;
-          f1 = 1.f - f0;
-        }
         const int c0 = jb.halves ? 0 : w * (D / 64), c1 = jb.halves ? D / 32 : c0 + D / 64;
+#pragma unroll 1
         for (int c = c0; c < c1; ++c) {
-          uint32_t x[32];
           float o[32];
-          const bool use0 = !jb.halves || w == 0, use1 = jb.halves ? w == 1 : jb.jobs > 1;
-          if (use0) {
-            tmem_ld32(tO + lanes + 32 * c, x);
-            tmem_wait_ld(x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = f0 * __uint_as_float(x[e]);
-          }
-          if (use1) {
-            tmem_ld32(tO + 128 + lanes + 32 * c, x);
-            tmem_wait_ld(x);
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = use0 ? fmaf(f1, __uint_as_float(x[e]), o[e]) : f1 * __uint_as_float(x[e]);
+          for (int i = 0; i < 2; ++i) {
+            if (!use[i]) continue;
+            uint32_t x[32];
+            tmem_ld32(tO + i * 128 + lanes + 32 * c, x);
+            tmem_wait_ld(x);
+            if (folds[i]) {
+              const float4 *acc = (const float4 *)p.fold + fold_at(i, lr);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 v = __ldcg(acc + (8 * c + e) * 128);
+                x[4 * e] = __float_as_uint(fmaf(v.x, fa[i], __uint_as_float(x[4 * e])));
+                x[4 * e + 1] = __float_as_uint(fmaf(v.y, fa[i], __uint_as_float(x[4 * e + 1])));
+                x[4 * e + 2] = __float_as_uint(fmaf(v.z, fa[i], __uint_as_float(x[4 * e + 2])));
+                x[4 * e + 3] = __float_as_uint(fmaf(v.w, fa[i], __uint_as_float(x[4 * e + 3])));
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(f[i], __uint_as_float(x[e]), o[e]);
           }
           if (any && row < jb.rows) {
             // non-finite values of drafts this row sees (their weight is positive)

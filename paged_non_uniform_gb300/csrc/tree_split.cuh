@@ -196,28 +196,61 @@ __device__ __forceinline__ void tree_publish(const TreeParams &p, const TreeRang
   if (*flag) {
     const int rows = min(kRows, it.head.T * p.c.g - it.group * kRows);
     const int first = 2 * c0 + (it.seg > tree_bound(r.units, r.blocks, c0) ? 1 : 0);
-    for (int q = tid; q < rows * (D / 4); q += NT) {
-      const int row = q / (D / 4), d4 = q - row * (D / 4);
-      float M = -INFINITY, L = 0.f;
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = c0; c <= c1; ++c) {
-        const size_t at = (size_t)(c == c0 ? first : 2 * c) * kRows + row;
-        const float2 ml = __ldcg(p.part_ml + at);
-        const float4 o = __ldcg((const float4 *)(p.part_o + at * D) + d4);
-        const float m = fmaxf(M, ml.x);
-        const float a = tree_weight(M, m), f = tree_weight(ml.x, m);
-        L = L * a + f * ml.y;
-        // a partial that saw nothing has weight 0 and zeros; one with an
-        // infinity keeps it
-        O.x = O.x * a + f * o.x;
-        O.y = O.y * a + f * o.y;
-        O.z = O.z * a + f * o.z;
-        O.w = O.w * a + f * o.w;
-        M = m;
+    // Each thread owns float4 groups q = tid, tid + NT, ...; kQ of them and
+    // kC partials of each load before any is folded, so that the fold is not a chain
+    // of L2 round trips.
+    constexpr int kQ = 4, kC = 4;
+    const int n4 = rows * (D / 4);
+    for (int q0 = tid; q0 < n4; q0 += kQ * NT) {
+      float M[kQ], L[kQ];
+      float4 O[kQ];
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) {
+        M[k] = -INFINITY;
+        L[k] = 0.f;
+        O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const float s = L == 0.f ? 0.f : 1.f / L;
-      float *out = tree_out(p, it.head, it.group * kRows + row);
-      *((float4 *)out + d4) = make_float4(O.x * s, O.y * s, O.z * s, O.w * s);
+      for (int c = c0; c <= c1; c += kC) {
+        float2 ml[kC][kQ];
+        float4 o[kC][kQ];
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int k = 0; k < kQ; ++k) {
+            const int q = q0 + k * NT;
+            ml[i][k] = make_float2(-INFINITY, 0.f);
+            o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + i <= c1 && q < n4) {
+              const size_t at =
+                  (size_t)(c + i == c0 ? first : 2 * (c + i)) * kRows + q / (D / 4);
+              ml[i][k] = __ldcg(p.part_ml + at);
+              o[i][k] = __ldcg((const float4 *)(p.part_o + at * D) + q % (D / 4));
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int k = 0; k < kQ; ++k) {
+            // (a partial that saw nothing is (-inf, 0, 0): weight 0)
+            const float m = fmaxf(M[k], ml[i][k].x);
+            const float a = tree_weight(M[k], m), f = tree_weight(ml[i][k].x, m);
+            L[k] = L[k] * a + f * ml[i][k].y;
+            O[k].x = O[k].x * a + f * o[i][k].x;
+            O[k].y = O[k].y * a + f * o[i][k].y;
+            O[k].z = O[k].z * a + f * o[i][k].z;
+            O[k].w = O[k].w * a + f * o[i][k].w;
+            M[k] = m;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) {
+        const int q = q0 + k * NT;
+        if (q >= n4) continue;
+        const float s = L[k] == 0.f ? 0.f : 1.f / L[k];
+        float *out = tree_out(p, it.head, it.group * kRows + q / (D / 4));
+        *((float4 *)out + q % (D / 4)) =
+            make_float4(O[k].x * s, O[k].y * s, O[k].z * s, O[k].w * s);
+      }
     }
     if (tid == 0) *counter = 0;
   }

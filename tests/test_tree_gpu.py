@@ -309,3 +309,45 @@ def test_guard_bands():
     for w in (out_w, ws_w):
         w = w.cpu().numpy()
         assert np.all(w[:band] == 0xA5) and np.all(w[-band:] == 0xA5)
+
+
+@pytest.mark.parametrize("T,D", [(3, 64), (40, 64), (40, 128)])
+def test_long_items_leave_tensor_memory_in_time(T, D):
+    """One head of 1.4 M keys: every block works on 72 tiles of it, so that its output is folded
+    into the fp32 sum several times (twice with the tiles taken in turn, four times with 160 rows). The
+    tensor cores truncate what they add: 16 additions to an output element a tile, each off by at most
+    2^-23 of the sum so far, over the 16 tiles between folds; the folds and the merge round like fp32."""
+    n, g = 1_400_000, 4
+    P, len_ = 128, 1_400_000 + T
+    pages = -(-len_ // P)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    k = torch.empty(pages * P, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    v = torch.empty(pages * P, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    v += 0.5  # sums that grow
+    q = torch.empty(T, g, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    table = torch.randperm(pages, generator=gen, device="cuda").int().view(1, -1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = kvx.Cache(1, g, 1, D, P, 1, kvx.KVX_BF16, [0], [k], [v], [pages], [table], [pages])
+    ws = torch.zeros(kvx.kvx_tree_attn_workspace_bytes(cache, T) // 4, **i32)
+    out = torch.zeros(T, g, D, device="cuda")
+    for _ in range(2):
+        kvx.kvx_tree_attn(cache, q, torch.tensor([0, T], **i32), T, T, torch.tensor([[n]], **i32), None, 0.0,
+                          out, ws)
+    torch.cuda.synchronize()
+    at = (table.long().view(-1, 1) * P + torch.arange(P, device="cuda")).view(-1)[:len_]
+    kd, vd = k[at].double(), v[at].double()
+    x = q.view(T * g, D).double() @ kd.T / D ** 0.5
+    row = torch.arange(T * g, device="cuda") // g
+    x[:, n:] = x[:, n:].masked_fill(torch.arange(T, device="cuda") > row[:, None], -float("inf"))
+    p = torch.softmax(x, 1)
+    want, mag = p @ vd, p @ vd.abs()
+    far = float((x.amax(1) - x[:, :n].amin(1)).max()) + float(x[:, :n].abs().max())
+    s_abs = float((q.view(T * g, D).double().abs() @ kd.abs().T).max()) / D ** 0.5
+    u = 2.0 ** -24
+    weight = 2 * u * (D + 2) * s_abs + 3 * u * far + 2.0 ** -22
+    # truncation between folds 2u * 16 * 16; a sum of l over 128 keys of a tile by four chains, tiles and
+    # pieces: (32 + 72 + 152) u; folds and merge (5 + 152) u of output and sum
+    tol = (2 * weight + 2.0 ** -18 + 2 * u * 256 + (256 + 2 * 157) * u) * mag
+    err = (out.view(T * g, D).double() - want).abs()
+    assert bool((err <= tol).all()), (float(err.max()), float((err / tol).max()))
+    assert kvx.kvx_workspace_status(ws) == 0
