@@ -63,7 +63,8 @@ int tree_blocks(const kvx_cache *c, int *blocks) {
   int32_t sms = 0;
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
-  *blocks = sms * (c->shape.dtype == KVX_F32 ? tree_simt_blocks_per_sm() : 1);
+  *blocks = c->shape.dtype == KVX_F32 ? sms * tree_simt_blocks_per_sm()
+                                      : std::min(sms, kTreeMmaBlocks);
   return KVX_OK;
 }
 
@@ -259,6 +260,7 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.max_rows = max_rows;
   p.max_q = max_q;
   p.words = (max_q + 31) / 32;
+  p.recip_g = (65536 + c->dev.g - 1) / c->dev.g;
   const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
   p.scale_log2 = (float)((double)sc * 1.4426950408889634);
   cudaError_t e;

@@ -84,6 +84,7 @@ struct TreeParams {
   float *fold;        // tensor-core kernel: fp32 output sums of long items, [2 * blocks][D / 4][128][4]
   int32_t max_rows, max_q, words;  // words: uint32 words of a mask row
   int32_t row_groups;              // most row groups of a head
+  int32_t recip_g;                 // ceil(2^16 / g): r * recip_g >> 16 = r / g for r <= 1024
   float scale_log2;                // scale * log2(e)
 };
 
@@ -101,6 +102,7 @@ int tree_simt_rows();           // query rows of a row group
 int tree_simt_blocks_per_sm();  // resident blocks
 cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
                             const CUtensorMap *v_maps, int blocks, cudaStream_t st);
+constexpr int kTreeMmaBlocks = 152;  // most blocks of the tensor-core kernel: GB300's SMs
 int tree_mma_rows(int query_rows);  // query rows of a row group, of a head's largest number
 
 }  // namespace kvx

@@ -234,9 +234,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
         *(float4 *)(dst + tx * 4 + 64 * d) =
             make_float4(o[a][d][0] * f, o[a][d][1] * f, o[a][d][2] * f, o[a][d][3] * f);
     }
-    if (!whole)
-      tree_publish<D, kThreads, kTile, kRows>(p, range, it, tid, &sm.flag,
-                                              [] { __syncthreads(); });
+    if (!whole) {
+      __syncthreads();
+      if (tid == 0) sm.flag = tree_ticket(p, range, it);
+      __syncthreads();
+      if (sm.flag) tree_merge<D, kThreads, kRows>(p, range, it, tid);
+    }
   }
 }
 

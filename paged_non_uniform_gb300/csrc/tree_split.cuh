@@ -30,20 +30,35 @@ struct TreeHead {
   int tiles, groups;
 };
 
-// Reads the lengths of head `hd`; lengths that do not fit their arrays give
-// T = 0 and set KVX_DEV_BAD_LENGTH (in the one block that reports).
+// The lengths of a head as they are in memory: loaded ahead of their use.
+struct TreeRaw {
+  int q0, q1, n;
+};
+__device__ __forceinline__ TreeRaw tree_raw(const TreeParams &p, int hd) {
+  TreeRaw r = {0, 0, 0};
+  if (hd < p.c.B * p.c.Hkv) {
+    const int b = hd / p.c.Hkv;
+    r.q0 = __ldg(p.q_start + b);
+    r.q1 = __ldg(p.q_start + b + 1);
+    r.n = __ldg(p.kv_len + hd);
+  }
+  return r;
+}
+
+// Head `hd` from its lengths; lengths that do not fit their arrays give T = 0
+// and set KVX_DEV_BAD_LENGTH (in the one block that reports).
 template <int kTile, int kRows>
-__device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, bool report) {
+__device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const TreeRaw &r,
+                                              bool report) {
   TreeHead t;
   t.b = hd / p.c.Hkv;
   t.h = hd - t.b * p.c.Hkv;
-  t.q0 = __ldg(p.q_start + t.b);
-  const int q1 = __ldg(p.q_start + t.b + 1);
-  t.n = __ldg(p.kv_len + hd);
-  t.T = q1 - t.q0;
+  t.q0 = r.q0;
+  t.n = r.n;
+  t.T = r.q1 - r.q0;
   const CacheGroup &g = p.c.grp[p.c.head_grp[t.h]];
-  const bool ok = t.q0 >= 0 && q1 >= t.q0 && q1 <= p.max_rows && t.T <= p.max_q && t.n >= 0 &&
-                  (int64_t)t.n + t.T <= ((int64_t)g.stride << p.c.lgP);
+  const bool ok = r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.max_rows && t.T <= p.max_q && r.n >= 0 &&
+                  (int64_t)r.n + t.T <= ((int64_t)g.stride << p.c.lgP);
   if (!ok) {
     if (report) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     t.T = t.n = 0;
@@ -54,20 +69,21 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, bool 
 }
 
 struct TreeRange {
-  int64_t units;    // of all heads
-  int blocks;       // blocks with work
-  int64_t begin, end;  // this block's units
-  int head;         // the head that holds `begin`
-  int64_t base;     // first unit of that head
+  int units;       // of all heads
+  int blocks;      // blocks with work
+  int begin, end;  // this block's units
+  int head;        // the head that holds `begin`
+  int base;        // first unit of that head
 };
 
-// First unit of block c.
-__device__ __forceinline__ int64_t tree_bound(int64_t units, int blocks, int c) {
-  return (int64_t)c * units / blocks;
+// First unit of block c: floor(c * units / blocks) without 64 bits.
+__device__ __forceinline__ int tree_bound(int units, int blocks, int c) {
+  const int q = units / blocks, r = units - q * blocks;
+  return c * q + c * r / blocks;  // blocks is at most a few hundred
 }
 // The block that holds unit u.
-__device__ __forceinline__ int tree_block_of(int64_t units, int blocks, int64_t u) {
-  return (int)(((u + 1) * blocks - 1) / units);
+__device__ __forceinline__ int tree_block_of(int units, int blocks, int u) {
+  return (int)((((int64_t)u + 1) * blocks - 1) / units);
 }
 
 // Sums the units of all heads over the block's NT threads and finds this block's range.
@@ -82,7 +98,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
   const int lo = min(heads, tid * per), hi = min(heads, lo + per);
   int64_t s = 0;
   for (int i = lo; i < hi; ++i) {
-    const TreeHead t = tree_head<kTile, kRows>(p, i, blockIdx.x == 0);
+    const TreeHead t = tree_head<kTile, kRows>(p, i, tree_raw(p, i), blockIdx.x == 0);
     s += (int64_t)t.tiles * t.groups;
   }
   int64_t x = s;
@@ -99,21 +115,27 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
-  const int64_t want = all / min_units;
-  const int blocks = (int)(want < 1 ? 1 : want < (int64_t)gridDim.x ? want : (int64_t)gridDim.x);
-  const bool work = (int)blockIdx.x < blocks && all > 0;
-  const int64_t begin = work ? tree_bound(all, blocks, blockIdx.x) : 0;
-  const int64_t end = work ? tree_bound(all, blocks, blockIdx.x + 1) : 0;
+  // (more units than an int holds would be hundreds of times the device's memory,
+  // reachable only through aliased pages: refused whole)
+  if (all > INT32_MAX) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
+    all = 0;
+  }
+  const int units = (int)all, want = units / min_units;
+  const int blocks = want < 1 ? 1 : min(want, (int)gridDim.x);
+  const bool work = (int)blockIdx.x < blocks && units > 0;
+  const int begin = work ? tree_bound(units, blocks, blockIdx.x) : 0;
+  const int end = work ? tree_bound(units, blocks, blockIdx.x + 1) : 0;
   const int64_t mine = before + x - s;
   if (!work) {
-    if (tid == 0) *shared = {all, blocks, 0, 0, 0, 0};
+    if (tid == 0) *shared = {units, blocks, 0, 0, 0, 0};
   } else if (begin >= mine && begin < mine + s) {
-    int64_t base = mine;
+    int base = (int)mine;
     for (int i = lo; i < hi; ++i) {
-      const TreeHead t = tree_head<kTile, kRows>(p, i, false);
-      const int64_t u = (int64_t)t.tiles * t.groups;
+      const TreeHead t = tree_head<kTile, kRows>(p, i, tree_raw(p, i), false);
+      const int u = t.tiles * t.groups;
       if (begin < base + u) {
-        *shared = {all, blocks, begin, end, i, base};
+        *shared = {units, blocks, begin, end, i, base};
         break;
       }
       base += u;
@@ -127,32 +149,41 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
 struct TreeItem {
   TreeHead head;
   int hd, group, t0, t1;
-  int64_t seg;  // first unit of the row group
+  int seg;  // first unit of the row group
 };
 
+// Walks a block's items. The lengths of the two heads after the current one are
+// already in flight, so that short heads do not wait for them.
 template <int kTile, int kRows>
 struct TreeCursor {
-  int64_t at, end, base;
-  int hd;
+  int at, end, base, hd;
   TreeHead head;
+  TreeRaw raw1, raw2;
   __device__ __forceinline__ TreeCursor(const TreeParams &p, const TreeRange &r)
       : at(r.begin), end(r.end), base(r.base), hd(r.head) {
-    if (at < end) head = tree_head<kTile, kRows>(p, hd, false);
+    if (at < end) {
+      const TreeRaw raw = tree_raw(p, hd);
+      raw1 = tree_raw(p, hd + 1);
+      raw2 = tree_raw(p, hd + 2);
+      head = tree_head<kTile, kRows>(p, hd, raw, false);
+    }
   }
   __device__ __forceinline__ bool next(const TreeParams &p, TreeItem &it) {
     if (at >= end) return false;
-    while (at - base >= (int64_t)head.tiles * head.groups) {
-      base += (int64_t)head.tiles * head.groups;
-      head = tree_head<kTile, kRows>(p, ++hd, false);
+    while (at - base >= head.tiles * head.groups) {
+      base += head.tiles * head.groups;
+      ++hd;
+      head = tree_head<kTile, kRows>(p, hd, raw1, false);
+      raw1 = raw2;
+      raw2 = tree_raw(p, hd + 2);
     }
-    const int v = (int)(at - base);
+    const int v = at - base;
     it.head = head;
     it.hd = hd;
-    it.group = v / head.tiles;
+    it.group = head.groups == 1 ? 0 : v / head.tiles;
     it.t0 = v - it.group * head.tiles;
     it.seg = at - it.t0;
-    const int64_t left = end - at;
-    it.t1 = left < head.tiles - it.t0 ? it.t0 + (int)left : head.tiles;
+    it.t1 = it.t0 + min(end - at, head.tiles - it.t0);
     at += it.t1 - it.t0;
     return true;
   }
@@ -177,84 +208,64 @@ __device__ __forceinline__ float *tree_out(const TreeParams &p, const TreeHead &
   return p.out + ((size_t)(t.q0 + i) * p.c.Hq + (size_t)t.h * p.c.g + j) * p.c.D;
 }
 
-// Publishes this block's partial of a split row group, written by the NT
-// threads, and merges the row group in the block that published last. All NT
-// threads call it; sync() is a barrier over them, *flag a shared int.
-template <int D, int NT, int kTile, int kRows, typename Sync>
-__device__ __forceinline__ void tree_publish(const TreeParams &p, const TreeRange &r,
-                                             const TreeItem &it, int tid, int *flag, Sync sync) {
-  const int64_t seg_end = it.seg + it.head.tiles;
+// Ticket of this block's partial of a split row group: true in the block that
+// took the last one. One thread calls it, after a barrier behind which all
+// of the partial's writes lie: the release publishes them, and in the last block the
+// acquire, passed on by a second barrier, makes the other partials visible.
+__device__ __forceinline__ bool tree_ticket(const TreeParams &p, const TreeRange &r,
+                                            const TreeItem &it) {
   const int c0 = tree_block_of(r.units, r.blocks, it.seg);
-  const int c1 = tree_block_of(r.units, r.blocks, seg_end - 1);
+  const int c1 = tree_block_of(r.units, r.blocks, it.seg + it.head.tiles - 1);
   int *counter = p.counters + (size_t)it.hd * p.row_groups + it.group;
-  // the barrier orders the partial's writes before the ticket, whose release
-  // publishes them; in the last block its acquire, passed on by the second
-  // barrier, makes the other partials visible
-  sync();
-  if (tid == 0) *flag = ticket_acq_rel(counter) == c1 - c0;
-  sync();
-  if (*flag) {
-    const int rows = min(kRows, it.head.T * p.c.g - it.group * kRows);
-    const int first = 2 * c0 + (it.seg > tree_bound(r.units, r.blocks, c0) ? 1 : 0);
-    // Each thread owns float4 groups q = tid, tid + NT, ...; kQ of them and
-    // kC partials of each load before any is folded, so that the fold is not a chain
-    // of L2 round trips.
-    constexpr int kQ = 4, kC = 4;
-    const int n4 = rows * (D / 4);
-    for (int q0 = tid; q0 < n4; q0 += kQ * NT) {
-      float M[kQ], L[kQ];
-      float4 O[kQ];
+  if (ticket_acq_rel(counter) != c1 - c0) return false;
+  *counter = 0;  // for the next call
+  return true;
+}
+
+// Folds the partials of a row group, in block order, into its output rows (NT
+// threads, after the last ticket).
+template <int D, int NT, int kRows>
+__device__ __forceinline__ void tree_merge(const TreeParams &p, const TreeRange &r,
+                                           const TreeItem &it, int tid) {
+  const int c0 = tree_block_of(r.units, r.blocks, it.seg);
+  const int c1 = tree_block_of(r.units, r.blocks, it.seg + it.head.tiles - 1);
+  const int rows = min(kRows, it.head.T * p.c.g - it.group * kRows);
+  const int first = 2 * c0 + (it.seg > tree_bound(r.units, r.blocks, c0) ? 1 : 0);
+  // four partials' loads at a time, so that the fold is not a chain of L2 round trips
+  for (int q = tid; q < rows * (D / 4); q += NT) {
+    const int row = q / (D / 4), d4 = q % (D / 4);
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += 4) {
+      float2 ml[4];
+      float4 o[4];
 #pragma unroll
-      for (int k = 0; k < kQ; ++k) {
-        M[k] = -INFINITY;
-        L[k] = 0.f;
-        O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      for (int c = c0; c <= c1; c += kC) {
-        float2 ml[kC][kQ];
-        float4 o[kC][kQ];
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-#pragma unroll
-          for (int k = 0; k < kQ; ++k) {
-            const int q = q0 + k * NT;
-            ml[i][k] = make_float2(-INFINITY, 0.f);
-            o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + i <= c1 && q < n4) {
-              const size_t at =
-                  (size_t)(c + i == c0 ? first : 2 * (c + i)) * kRows + q / (D / 4);
-              ml[i][k] = __ldcg(p.part_ml + at);
-              o[i][k] = __ldcg((const float4 *)(p.part_o + at * D) + q % (D / 4));
-            }
-          }
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-#pragma unroll
-          for (int k = 0; k < kQ; ++k) {
-            // (a partial that saw nothing is (-inf, 0, 0): weight 0)
-            const float m = fmaxf(M[k], ml[i][k].x);
-            const float a = tree_weight(M[k], m), f = tree_weight(ml[i][k].x, m);
-            L[k] = L[k] * a + f * ml[i][k].y;
-            O[k].x = O[k].x * a + f * o[i][k].x;
-            O[k].y = O[k].y * a + f * o[i][k].y;
-            O[k].z = O[k].z * a + f * o[i][k].z;
-            O[k].w = O[k].w * a + f * o[i][k].w;
-            M[k] = m;
-          }
+      for (int i = 0; i < 4; ++i) {
+        // (a partial that saw nothing is (-inf, 0, 0): weight 0)
+        ml[i] = make_float2(-INFINITY, 0.f);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + i <= c1) {
+          const size_t at = (size_t)(c + i == c0 ? first : 2 * (c + i)) * kRows + row;
+          ml[i] = __ldcg(p.part_ml + at);
+          o[i] = __ldcg((const float4 *)(p.part_o + at * D) + d4);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < kQ; ++k) {
-        const int q = q0 + k * NT;
-        if (q >= n4) continue;
-        const float s = L[k] == 0.f ? 0.f : 1.f / L[k];
-        float *out = tree_out(p, it.head, it.group * kRows + q / (D / 4));
-        *((float4 *)out + q % (D / 4)) =
-            make_float4(O[k].x * s, O[k].y * s, O[k].z * s, O[k].w * s);
+      for (int i = 0; i < 4; ++i) {
+        const float m = fmaxf(M, ml[i].x);
+        const float a = tree_weight(M, m), f = tree_weight(ml[i].x, m);
+        L = L * a + f * ml[i].y;
+        O.x = O.x * a + f * o[i].x;
+        O.y = O.y * a + f * o[i].y;
+        O.z = O.z * a + f * o[i].z;
+        O.w = O.w * a + f * o[i].w;
+        M = m;
       }
     }
-    if (tid == 0) *counter = 0;
+    const float s = L == 0.f ? 0.f : 1.f / L;
+    *((float4 *)tree_out(p, it.head, it.group * kRows + row) + d4) =
+        make_float4(O.x * s, O.y * s, O.z * s, O.w * s);
   }
-  sync();
 }
 
 // Word `w` of the visibility mask of new row i of a sequence of T rows (bits
