@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvx.so")
 SOURCES = ["plan.cpp", "abi.cpp", "attn_mma.cu", "attn_simt.cu", "gather.cu", "select.cu",
            "frame.cu", "cache.cpp", "tables.cu", "rows.cu", "tree_simt.cu",
-           "tree_mma.cu"]
+           "tree_mma.cu", "tree_merge.cu"]
 HEADERS = [os.path.join(CSRC, "kvx_internal.h"), os.path.join(CSRC, "ptx.cuh"),
            os.path.join(CSRC, "split_merge.cuh"), os.path.join(CSRC, "tree.h"),
            os.path.join(CSRC, "tree_split.cuh"), os.path.join(CSRC, "tcgen05.cuh"),

@@ -30,60 +30,77 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need) {
   return ws && aligned(ws, 256) && bytes >= need;
 }
 
-// A 5-D bf16 tensor map over one head group's pool, dims (innermost first)
-// {64 elements, P slots, D/64 halves, |G| heads, pages}; one box {64, P, 1, 1,
-// 1} is a page's rows of one head and half, 128-byte swizzled, zeros outside.
-bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g) {
+bool encode(CUtensorMap *tm, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
   typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  void *f = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                       &found) != cudaSuccess ||
-      found != cudaDriverEntryPointSuccess || !f) {
-    cudaGetLastError();
-    return false;
-  }
+  static const Encode fn = []() -> Encode {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return (Encode)f;
+  }();
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn && fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A 5-D bf16 tensor map over one head group's pool, dims (innermost first)
+// {64 elements, P slots, D/64 halves, |G| heads, pages}; one box {64, P, 1, 1,
+// 1} is a page's rows of one head and half, 128-byte swizzled, zeros outside.
+bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g) {
   const cuuint64_t row = (cuuint64_t)c->dev.row_bytes, P = (cuuint64_t)c->dev.P;
   const cuuint64_t n = (cuuint64_t)g.size;
   const cuuint64_t dims[5] = {64, P, row / 128, n, (cuuint64_t)g.pages};
   const cuuint64_t strides[4] = {c->dev.token_major ? row * n : row, 128,
                                  c->dev.token_major ? row : row * P, row * P * n};
-  const cuuint32_t box[5] = {64, (cuuint32_t)P, 1, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
-  return ((Encode)f)(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims,
-                     strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[5] = {64, (cuuint32_t)P, 1, 1, 1};
+  return encode(tm, pool, dims, strides, box);
 }
 
-// Blocks of the attention kernel on the current device.
-int tree_blocks(const kvx_cache *c, int *blocks) {
+// 5-D map over the query rows, dims {64 elements, D/64 halves, Hq heads, rows, 1}; one
+// box {64, 1, g, 8, 1} is the g query heads of one KV head of 8 rows, one half.
+bool encode_q_map(CUtensorMap *tm, const kvx_cache *c, const void *q, int64_t stride_bytes,
+                  int max_rows) {
+  const cuuint64_t row = (cuuint64_t)c->dev.row_bytes;
+  const cuuint64_t dims[5] = {64, row / 128, (cuuint64_t)c->dev.Hq, (cuuint64_t)max_rows, 1};
+  const cuuint64_t strides[4] = {128, row, (cuuint64_t)stride_bytes, (cuuint64_t)stride_bytes};
+  const cuuint32_t box[5] = {64, 1, (cuuint32_t)c->dev.g, kTreeBox, 1};
+  return encode(tm, q, dims, strides, box);
+}
+
+// What a call's max_q fixes: row groups, blocks and the workspace.
+struct TreeShape {
+  int blocks, tokens, rows;
+  TreeWs ws;
+};
+int tree_shape(const kvx_cache *c, int max_q, TreeShape *t) {
   int32_t sms = 0;
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
-  *blocks = c->shape.dtype == KVX_F32 ? sms * tree_simt_blocks_per_sm()
-                                      : std::min(sms, kTreeMmaBlocks);
-  return KVX_OK;
-}
-
-TreeWs tree_ws_layout(const kvx_cache *c, int max_q, int blocks, int *row_groups) {
-  const int rows =
-      c->shape.dtype == KVX_F32 ? tree_simt_rows() : tree_mma_rows(max_q * c->dev.g);
-  const size_t heads = (size_t)c->shape.B * c->shape.Hkv;
-  const int groups = (max_q * c->dev.g + rows - 1) / rows;
+  const int g = c->dev.g;
+  const bool f32 = c->shape.dtype == KVX_F32;
+  t->blocks = f32 ? sms * tree_simt_blocks_per_sm() : std::min(sms, kTreeMmaBlocks);
+  t->rows = f32 ? tree_simt_rows() : tree_mma_rows(max_q, g);
+  t->tokens = f32 ? tree_simt_tokens(g) : tree_mma_tokens(t->rows, g);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  TreeWs w;
-  w.counters = KVX_WS_HEADER_BYTES;
-  w.part_ml = w.counters + up(heads * groups * sizeof(int32_t));
-  w.part_o = w.part_ml + up((size_t)2 * blocks * rows * sizeof(float2));
-  w.fold = w.part_o + up((size_t)2 * blocks * rows * c->shape.D * sizeof(float));
-  w.total = w.fold;
-  if (c->shape.dtype == KVX_BF16)
-    w.total += up((size_t)2 * blocks * 128 * c->shape.D * sizeof(float));
-  if (row_groups) *row_groups = groups;
-  return w;
+  const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);
+  TreeWs &w = t->ws;
+  w.split = KVX_WS_HEADER_BYTES;
+  w.part_ml = w.split + up(t->blocks * sizeof(TreeSplit));
+  w.part_o = w.part_ml + up(slots * t->rows * sizeof(float2));
+  w.fold = w.part_o + up(slots * t->rows * row);
+  w.total = w.fold + (f32 ? 0 : up(slots * 128 * row));
+  return KVX_OK;
 }
 
 }  // namespace
@@ -219,11 +236,10 @@ extern "C" int kvx_append_kv(const kvx_cache *c, const void *k_new, int64_t k_st
 extern "C" int kvx_tree_attn_workspace_bytes(const kvx_cache *c, int32_t max_q, size_t *bytes) {
   if (!c || !bytes) return KVX_EINVAL;
   if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
-  int blocks = 0;
-  const int rc = tree_blocks(c, &blocks);
-  if (rc != KVX_OK) return rc;
-  *bytes = tree_ws_layout(c, max_q, blocks, nullptr).total;
-  return KVX_OK;
+  TreeShape t;
+  const int rc = tree_shape(c, max_q, &t);
+  if (rc == KVX_OK) *bytes = t.ws.total;
+  return rc;
 }
 
 extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride,
@@ -241,11 +257,12 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.q_stride = row_stride(c, q_stride, c->dev.Hq);
   if (!p.q_stride) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
-  int blocks = 0;
-  const int rc = tree_blocks(c, &blocks);
+  TreeShape t;
+  const int rc = tree_shape(c, max_q, &t);
   if (rc != KVX_OK) return rc;
-  const TreeWs w = tree_ws_layout(c, max_q, blocks, &p.row_groups);
+  const TreeWs &w = t.ws;
   if (workspace_bytes < w.total) return KVX_EINVAL;
+  if (max_rows == 0) return KVX_OK;
   char *ws = (char *)workspace;
   p.q = (const char *)q;
   p.q_start = q_start;
@@ -253,23 +270,26 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.mask = mask;
   p.out = out;
   p.status = (uint32_t *)ws;
-  p.counters = (int32_t *)(ws + w.counters);
+  p.split = (TreeSplit *)(ws + w.split);
   p.part_ml = (float2 *)(ws + w.part_ml);
   p.part_o = (float *)(ws + w.part_o);
   p.fold = (float *)(ws + w.fold);
   p.max_rows = max_rows;
   p.max_q = max_q;
   p.words = (max_q + 31) / 32;
+  p.group_tokens = t.tokens;
+  p.group_rows = t.rows;
   p.recip_g = (65536 + c->dev.g - 1) / c->dev.g;
   const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
   p.scale_log2 = (float)((double)sc * 1.4426950408889634);
-  cudaError_t e;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaErrorInvalidValue;
+  CUtensorMap q_map;
   if (c->shape.dtype == KVX_F32)
-    e = launch_tree_simt(p, blocks, (cudaStream_t)stream);
-  else if (c->have_maps)
-    e = launch_tree_mma(p, c->k_maps, c->v_maps, blocks, (cudaStream_t)stream);
-  else
-    e = cudaErrorInvalidValue;
+    e = launch_tree_simt(p, t.blocks, st);
+  else if (c->have_maps && encode_q_map(&q_map, c, q, p.q_stride, max_rows))
+    e = launch_tree_mma(p, c->k_maps, c->v_maps, q_map, t.blocks, st);
+  if (e == cudaSuccess) e = launch_tree_merge(p, t.blocks, st);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
 }
 

@@ -67,6 +67,12 @@ struct CommitParams {
   int32_t max_rows, path_stride;
 };
 
+// A row group whose tiles span blocks: `parts` partials, the first in slot
+// `first`, the others in slots 2c of the blocks that follow (0: none).
+struct TreeSplit {
+  int32_t parts, first, row0, h, rows;
+};
+
 // Tree attention. A head's keys come in tiles, its query rows (new row i and
 // query head j of the KV head: row i * g + j) in groups; tree_split.cuh
 // says how the (row group, tile) units are cut over the blocks.
@@ -78,19 +84,21 @@ struct TreeParams {
   const uint32_t *mask;
   float *out;
   uint32_t *status;
-  int32_t *counters;  // [B * Hkv][row groups] finished pieces, back to 0 after the merge
-  float2 *part_ml;    // [2 * blocks][rows of a group] = (max in log2 units, sum)
-  float *part_o;      // [2 * blocks][rows of a group][D]
+  TreeSplit *split;   // [blocks] the row group that starts in the block and runs on
+  float2 *part_ml;    // [2 * blocks][group_rows] = (max in log2 units, sum)
+  float *part_o;      // [2 * blocks][group_rows][D]
   float *fold;        // tensor-core kernel: fp32 output sums of long items, [2 * blocks][D / 4][128][4]
   int32_t max_rows, max_q, words;  // words: uint32 words of a mask row
-  int32_t row_groups;              // most row groups of a head
+  int32_t group_tokens;            // new rows of a row group
+  int32_t group_rows;              // room for its query rows
   int32_t recip_g;                 // ceil(2^16 / g): r * recip_g >> 16 = r / g for r <= 1024
   float scale_log2;                // scale * log2(e)
 };
 
-// Workspace of tree attention: header | counters | partial (m, l) | partial o | folded o.
+// Workspace of tree attention: header | split row groups | partial (m, l) | partial o |
+// folded o.
 struct TreeWs {
-  size_t counters, part_ml, part_o, fold, total;
+  size_t split, part_ml, part_o, fold, total;
 };
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st);
@@ -98,12 +106,18 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t st);
 // fp32 caches: CUDA cores; bf16 caches: tensor cores, one block per SM.
 cudaError_t launch_tree_simt(const TreeParams &p, int blocks, cudaStream_t st);
-int tree_simt_rows();           // query rows of a row group
+int tree_simt_tokens(int g);    // new rows of a row group; its query rows:
+int tree_simt_rows();
 int tree_simt_blocks_per_sm();  // resident blocks
-cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
-                            const CUtensorMap *v_maps, int blocks, cudaStream_t st);
 constexpr int kTreeMmaBlocks = 152;  // most blocks of the tensor-core kernel: GB300's SMs
-int tree_mma_rows(int query_rows);  // query rows of a row group, of a head's largest number
+constexpr int kTreeBox = 8;          // new rows of a query load
+cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
+                            const CUtensorMap *v_maps, const CUtensorMap &q_map, int blocks,
+                            cudaStream_t st);
+int tree_mma_rows(int max_q, int g);  // room for query rows (128 or 256) ...
+int tree_mma_tokens(int rows, int g);  // ... and the new rows that fill it
+// Folds the partials of split row groups (after either kernel).
+cudaError_t launch_tree_merge(const TreeParams &p, int blocks, cudaStream_t st);
 
 }  // namespace kvx
 

@@ -32,7 +32,6 @@ struct Smem {
   uint32_t seen[kRows][2];  // visible keys of the tile, by row
   int64_t warp_sum[kThreads / 32];
   TreeRange range;
-  int flag;
 };
 
 template <int D>
@@ -44,23 +43,24 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_launch_dependents();
   pdl_wait();
-  const TreeRange range =
-      tree_range<kThreads, kTile, kRows>(p, kMinUnits, sm.warp_sum, &sm.range);
-  TreeCursor<kTile, kRows> cur(p, range);
+  const TreeRange range = tree_range<kThreads, kTile>(p, kMinUnits, sm.warp_sum, &sm.range);
+  TreeCursor<kTile> cur(p, range);
   TreeItem it;
+  bool any = false;
   while (cur.next(p, it)) {
+    any = true;
     const TreeHead &hd = it.head;
     const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
     const int rank = p.c.head_row[hd.h], g = p.c.g, P = p.c.P;
     const int32_t *table = grp.table + (size_t)hd.b * grp.stride;
-    const int r0 = it.group * kRows, rows = min(kRows, hd.T * g - r0);
+    const int i0 = tree_first(p, it), rows = tree_rows(p, it);
     __syncthreads();  // the item before is done with shared memory
     for (int i = tid; i < kRows * CPR; i += kThreads) {
       const int r = i / CPR, c = i - r * CPR;
       float *dst = &sm.q[r][c * 4];
       if (r < rows) {
-        const int nr = (r0 + r) / g, j = (r0 + r) - nr * g;
-        *(float4 *)dst = __ldg((const float4 *)(p.q + (size_t)(hd.q0 + nr) * p.q_stride +
+        const int nr = tree_div_g(p, r), j = r - nr * g;
+        *(float4 *)dst = __ldg((const float4 *)(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
                                                ((size_t)hd.h * g + j) * (D * 4) + c * 16));
       } else {
         *(float4 *)dst = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
         const int r = tid >> 1, w = tid & 1;
         uint32_t bits = 0;
         if (r < rows) {
-          const int nr = (r0 + r) / g;
+          const int nr = i0 + tree_div_g(p, r);
 #pragma unroll 4
           for (int e = 0; e < 32; ++e) {
             const int u = t0 + 32 * w + e - hd.n;  // draft index, < 0: cached
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
       float *dst;
       float f = 1.f;
       if (whole) {
-        dst = tree_out(p, hd, r0 + r);
+        dst = tree_out(p, hd.q0 + i0, hd.h, r);
         f = l[a] == 0.f ? 0.f : 1.f / l[a];
       } else {
         const size_t at = (size_t)slot * kRows + r;
@@ -234,13 +234,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
         *(float4 *)(dst + tx * 4 + 64 * d) =
             make_float4(o[a][d][0] * f, o[a][d][1] * f, o[a][d][2] * f, o[a][d][3] * f);
     }
-    if (!whole) {
-      __syncthreads();
-      if (tid == 0) sm.flag = tree_ticket(p, range, it);
-      __syncthreads();
-      if (sm.flag) tree_merge<D, kThreads, kRows>(p, range, it, tid);
-    }
   }
+  if (tid == 0) tree_describe(p, range, any ? &it : nullptr);
 }
 
 template <int D>
@@ -266,6 +261,7 @@ cudaError_t launch_d(const TreeParams &p, int blocks, cudaStream_t st) {
 }  // namespace
 
 int tree_simt_rows() { return kRows; }
+int tree_simt_tokens(int g) { return kRows / g; }
 int tree_simt_blocks_per_sm() { return 2; }
 
 cudaError_t launch_tree_simt(const TreeParams &p, int blocks, cudaStream_t st) {

@@ -1,19 +1,20 @@
 // tree_split.cuh -- how tree attention is cut over the thread blocks, from
 // device lengths, and how the pieces of a head are merged.
 //
-// A head (b, h) with T_b new rows has T_b * g query rows, in groups of kRows,
-// and n[b][h] + T_b keys, in tiles of kTile. A unit is one tile for one row
-// group. All units are laid end to end -- heads in order, row groups within a
-// head, tiles within a row group -- and block c of `blocks` takes units
-// [c * U / blocks, (c + 1) * U / blocks): the flat equal cut of the
+// A head (b, h) with T_b new rows has T_b * g query rows, in groups of
+// group_tokens new rows, and n[b][h] + T_b keys, in tiles of kTile. A unit is one
+// tile for one row group. All units are laid end to end -- heads in order, row
+// groups within a head, tiles within a row group -- and block c of `blocks` takes
+// units [c * U / blocks, (c + 1) * U / blocks): the flat equal cut of the
 // ahead-of-time plan ("Tangram: Unlocking Non-Uniform KV Cache for Efficient
 // Multi-turn LLM Serving", AOT Load Balancing, Fig. 13), but found by every
 // block itself from one pass over the lengths, so that nothing is planned on
 // the host. A row group whose tiles span blocks leaves one partial (max in
-// log2 units, sum, un-normalised output) per block; the block that finishes
-// last folds them in block order. A block leaves at most two partials: of the
-// row group that its range begins in (slot 2c) and of one that begins inside
-// its range and runs past its end (slot 2c + 1).
+// log2 units, sum, un-normalised output) per block; a second, small kernel folds
+// them in block order. A block leaves at most two partials: of the row group
+// that its range begins in (slot 2c) and of one that begins inside its range and
+// runs past its end (slot 2c + 1). At most one row group starts in a block and
+// runs past its end: the block describes it for the second kernel.
 #pragma once
 
 #include <math.h>
@@ -47,7 +48,7 @@ __device__ __forceinline__ TreeRaw tree_raw(const TreeParams &p, int hd) {
 
 // Head `hd` from its lengths; lengths that do not fit their arrays give T = 0
 // and set KVX_DEV_BAD_LENGTH (in the one block that reports).
-template <int kTile, int kRows>
+template <int kTile>
 __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const TreeRaw &r,
                                               bool report) {
   TreeHead t;
@@ -64,7 +65,7 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const
     t.T = t.n = 0;
   }
   t.tiles = t.T > 0 ? (t.n + t.T + kTile - 1) / kTile : 0;
-  t.groups = (t.T * p.c.g + kRows - 1) / kRows;
+  t.groups = t.T <= p.group_tokens ? 1 : (t.T + p.group_tokens - 1) / p.group_tokens;
   return t;
 }
 
@@ -88,7 +89,7 @@ __device__ __forceinline__ int tree_block_of(int units, int blocks, int u) {
 
 // Sums the units of all heads over the block's NT threads and finds this block's range.
 // `min_units`: a block gets at least that many where there are few in all.
-template <int NT, int kTile, int kRows>
+template <int NT, int kTile>
 __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_units,
                                                 int64_t *warp_sum /* shared, NT / 32 */,
                                                 TreeRange *shared) {
@@ -98,7 +99,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
   const int lo = min(heads, tid * per), hi = min(heads, lo + per);
   int64_t s = 0;
   for (int i = lo; i < hi; ++i) {
-    const TreeHead t = tree_head<kTile, kRows>(p, i, tree_raw(p, i), blockIdx.x == 0);
+    const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), blockIdx.x == 0);
     s += (int64_t)t.tiles * t.groups;
   }
   int64_t x = s;
@@ -132,7 +133,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
   } else if (begin >= mine && begin < mine + s) {
     int base = (int)mine;
     for (int i = lo; i < hi; ++i) {
-      const TreeHead t = tree_head<kTile, kRows>(p, i, tree_raw(p, i), false);
+      const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), false);
       const int u = t.tiles * t.groups;
       if (begin < base + u) {
         *shared = {units, blocks, begin, end, i, base};
@@ -154,7 +155,7 @@ struct TreeItem {
 
 // Walks a block's items. The lengths of the two heads after the current one are
 // already in flight, so that short heads do not wait for them.
-template <int kTile, int kRows>
+template <int kTile>
 struct TreeCursor {
   int at, end, base, hd;
   TreeHead head;
@@ -165,7 +166,7 @@ struct TreeCursor {
       const TreeRaw raw = tree_raw(p, hd);
       raw1 = tree_raw(p, hd + 1);
       raw2 = tree_raw(p, hd + 2);
-      head = tree_head<kTile, kRows>(p, hd, raw, false);
+      head = tree_head<kTile>(p, hd, raw, false);
     }
   }
   __device__ __forceinline__ bool next(const TreeParams &p, TreeItem &it) {
@@ -173,7 +174,7 @@ struct TreeCursor {
     while (at - base >= head.tiles * head.groups) {
       base += head.tiles * head.groups;
       ++hd;
-      head = tree_head<kTile, kRows>(p, hd, raw1, false);
+      head = tree_head<kTile>(p, hd, raw1, false);
       raw1 = raw2;
       raw2 = tree_raw(p, hd + 2);
     }
@@ -202,70 +203,35 @@ __device__ __forceinline__ float tree_weight(float m, float M) {
   return m == -INFINITY ? 0.f : ex2(m - M);
 }
 
-// The output row of query row `r` (new row r / g, query head r % g).
-__device__ __forceinline__ float *tree_out(const TreeParams &p, const TreeHead &t, int r) {
-  const int i = r / p.c.g, j = r - i * p.c.g;
-  return p.out + ((size_t)(t.q0 + i) * p.c.Hq + (size_t)t.h * p.c.g + j) * p.c.D;
+// First new row, and query rows, of an item.
+__device__ __forceinline__ int tree_first(const TreeParams &p, const TreeItem &it) {
+  return it.group * p.group_tokens;
+}
+__device__ __forceinline__ int tree_rows(const TreeParams &p, const TreeItem &it) {
+  return min(p.group_tokens, it.head.T - it.group * p.group_tokens) * p.c.g;
+}
+// r / g for the query rows r of an item.
+__device__ __forceinline__ int tree_div_g(const TreeParams &p, int r) {
+  return (r * p.recip_g) >> 16;
+}
+// The output row of query row r of the item whose first new row is row0 of the
+// row arrays.
+__device__ __forceinline__ float *tree_out(const TreeParams &p, int row0, int h, int r) {
+  const int i = tree_div_g(p, r), j = r - i * p.c.g;
+  return p.out + ((size_t)(row0 + i) * p.c.Hq + (size_t)h * p.c.g + j) * p.c.D;
 }
 
-// Ticket of this block's partial of a split row group: true in the block that
-// took the last one. One thread calls it, after a barrier behind which all
-// of the partial's writes lie: the release publishes them, and in the last block the
-// acquire, passed on by a second barrier, makes the other partials visible.
-__device__ __forceinline__ bool tree_ticket(const TreeParams &p, const TreeRange &r,
-                                            const TreeItem &it) {
-  const int c0 = tree_block_of(r.units, r.blocks, it.seg);
-  const int c1 = tree_block_of(r.units, r.blocks, it.seg + it.head.tiles - 1);
-  int *counter = p.counters + (size_t)it.hd * p.row_groups + it.group;
-  if (ticket_acq_rel(counter) != c1 - c0) return false;
-  *counter = 0;  // for the next call
-  return true;
-}
-
-// Folds the partials of a row group, in block order, into its output rows (NT
-// threads, after the last ticket).
-template <int D, int NT, int kRows>
-__device__ __forceinline__ void tree_merge(const TreeParams &p, const TreeRange &r,
-                                           const TreeItem &it, int tid) {
-  const int c0 = tree_block_of(r.units, r.blocks, it.seg);
-  const int c1 = tree_block_of(r.units, r.blocks, it.seg + it.head.tiles - 1);
-  const int rows = min(kRows, it.head.T * p.c.g - it.group * kRows);
-  const int first = 2 * c0 + (it.seg > tree_bound(r.units, r.blocks, c0) ? 1 : 0);
-  // four partials' loads at a time, so that the fold is not a chain of L2 round trips
-  for (int q = tid; q < rows * (D / 4); q += NT) {
-    const int row = q / (D / 4), d4 = q % (D / 4);
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += 4) {
-      float2 ml[4];
-      float4 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // (a partial that saw nothing is (-inf, 0, 0): weight 0)
-        ml[i] = make_float2(-INFINITY, 0.f);
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c + i <= c1) {
-          const size_t at = (size_t)(c + i == c0 ? first : 2 * (c + i)) * kRows + row;
-          ml[i] = __ldcg(p.part_ml + at);
-          o[i] = __ldcg((const float4 *)(p.part_o + at * D) + d4);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float m = fmaxf(M, ml[i].x);
-        const float a = tree_weight(M, m), f = tree_weight(ml[i].x, m);
-        L = L * a + f * ml[i].y;
-        O.x = O.x * a + f * o[i].x;
-        O.y = O.y * a + f * o[i].y;
-        O.z = O.z * a + f * o[i].z;
-        O.w = O.w * a + f * o[i].w;
-        M = m;
-      }
-    }
-    const float s = L == 0.f ? 0.f : 1.f / L;
-    *((float4 *)tree_out(p, it.head, it.group * kRows + row) + d4) =
-        make_float4(O.x * s, O.y * s, O.z * s, O.w * s);
+// Describes the row group that starts in this block and runs past its end (one
+// thread; `it` is the block's last item, or null if it has none).
+__device__ __forceinline__ void tree_describe(const TreeParams &p, const TreeRange &r,
+                                              const TreeItem *it) {
+  TreeSplit s = {0, 0, 0, 0, 0};
+  if (it && it->t0 == 0 && !tree_whole(*it)) {
+    const int last = tree_block_of(r.units, r.blocks, it->seg + it->head.tiles - 1);
+    s = {last - (int)blockIdx.x + 1, tree_slot(r, *it), it->head.q0 + tree_first(p, *it),
+         it->head.h, tree_rows(p, *it)};
   }
+  p.split[blockIdx.x] = s;
 }
 
 // Word `w` of the visibility mask of new row i of a sequence of T rows (bits
