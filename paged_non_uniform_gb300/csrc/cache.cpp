@@ -89,7 +89,7 @@ int tree_shape(const kvx_cache *c, int max_q, TreeShape *t) {
   if (rc != KVX_OK) return rc;
   const int g = c->dev.g;
   const bool f32 = c->shape.dtype == KVX_F32;
-  t->blocks = f32 ? sms * tree_simt_blocks_per_sm() : std::min(sms, kTreeMmaBlocks);
+  t->blocks = sms * (f32 ? tree_simt_blocks_per_sm() : tree_mma_blocks_per_sm());
   t->rows = f32 ? tree_simt_rows() : tree_mma_rows(max_q, g);
   t->tokens = f32 ? tree_simt_tokens(g) : tree_mma_tokens(t->rows, g);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -99,7 +99,7 @@ int tree_shape(const kvx_cache *c, int max_q, TreeShape *t) {
   w.part_ml = w.split + up(t->blocks * sizeof(TreeSplit));
   w.part_o = w.part_ml + up(slots * t->rows * sizeof(float2));
   w.fold = w.part_o + up(slots * t->rows * row);
-  w.total = w.fold + (f32 ? 0 : up(slots * 128 * row));
+  w.total = w.fold + (f32 ? 0 : up((size_t)t->blocks * 128 * row));
   return KVX_OK;
 }
 

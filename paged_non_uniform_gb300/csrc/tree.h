@@ -87,7 +87,7 @@ struct TreeParams {
   TreeSplit *split;   // [blocks] the row group that starts in the block and runs on
   float2 *part_ml;    // [2 * blocks][group_rows] = (max in log2 units, sum)
   float *part_o;      // [2 * blocks][group_rows][D]
-  float *fold;        // tensor-core kernel: fp32 output sums of long items, [2 * blocks][D / 4][128][4]
+  float *fold;        // tensor-core kernel: fp32 output sums of long items, [blocks][D / 4][128][4]
   int32_t max_rows, max_q, words;  // words: uint32 words of a mask row
   int32_t group_tokens;            // new rows of a row group
   int32_t group_rows;              // room for its query rows
@@ -104,18 +104,18 @@ struct TreeWs {
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t st);
-// fp32 caches: CUDA cores; bf16 caches: tensor cores, one block per SM.
+// fp32 caches: CUDA cores; bf16 caches: tensor cores.
 cudaError_t launch_tree_simt(const TreeParams &p, int blocks, cudaStream_t st);
 int tree_simt_tokens(int g);    // new rows of a row group; its query rows:
 int tree_simt_rows();
 int tree_simt_blocks_per_sm();  // resident blocks
-constexpr int kTreeMmaBlocks = 152;  // most blocks of the tensor-core kernel: GB300's SMs
-constexpr int kTreeBox = 8;          // new rows of a query load
+constexpr int kTreeBox = 8;     // new rows of a query load
 cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
                             const CUtensorMap *v_maps, const CUtensorMap &q_map, int blocks,
                             cudaStream_t st);
-int tree_mma_rows(int max_q, int g);  // room for query rows (128 or 256) ...
+int tree_mma_rows(int max_q, int g);   // room for query rows (64 or 128) ...
 int tree_mma_tokens(int rows, int g);  // ... and the new rows that fill it
+int tree_mma_blocks_per_sm();
 // Folds the partials of split row groups (after either kernel).
 cudaError_t launch_tree_merge(const TreeParams &p, int blocks, cudaStream_t st);
 

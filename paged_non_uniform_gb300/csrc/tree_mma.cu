@@ -5,18 +5,16 @@
 // of the row's KV head and the drafts its mask shows. The T_b * g query rows of
 // a KV head share its keys, so both products are dense: S [128 rows][128 keys]
 // = Q K^T and O [128 rows][D] += P V, with S, P and O in tensor memory. One
-// pass over the keys with a running reference and sum per row. One block per SM
-// walks its items (tree_split.cuh) in tiles of 128 keys:
-//  * warps 8 and 9 load K and V tiles from their pages into two rings (bulk
+// pass over the keys with a running reference and sum per row. Two blocks per SM,
+// independent of each other, so that one's item changes and softmax run under the
+// other's loads and products; each walks its items (tree_split.cuh) in tiles of
+// 128 keys:
+//  * warps 4 and 5 load K and V tiles from their pages into two rings (bulk
 //    tensor loads, one box of min(P, 128) rows x 64 dims per lane, landing as
 //    [half][128 rows][128 bytes], 128-byte swizzled);
-//  * warp 10 issues the MMAs: S(j), then O += P V of job j - 1, so that one warp
-//    group's softmax runs under the other's products;
-//  * warps 0-3 and 4-7 are two softmax groups, one query row per thread. Up to
-//    128 query rows, both hold all rows and take the tiles in turn (their (m, l, O) are
-//    merged at the item's end); above, each holds half the rows and takes
-//    every tile. A job is one tile for one group;
-//  * warp 11 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
+//  * warp 6 issues the MMAs: S, then O += P V of the tile;
+//  * warps 0-3 do the softmax, one query row per thread;
+//  * warp 7 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
 //    8 new rows x the g heads) and cleans the V tiles that hold drafts or the
 //    head's end: rows past the end are zeroed (stale or padding data), and
 //    non-finite values of drafts are replaced by zero and noted, because a weight
@@ -26,9 +24,8 @@
 // high part alone the weights would be off by 2^-9, with both by 2^-18, below
 // the fp32 output's other errors. They overwrite the scores they came from, column
 // block by column block.
-// The per-item path is kept short and its loops rolled: the roles run side by side on
-// one instruction cache, and code that runs once an item costs about five
-// cycles an instruction there.
+// Loops are kept rolled and the per-item path short: the roles run side by side on
+// one instruction cache.
 // Every mbarrier wait gives up after two seconds, sets KVX_DEV_TIMEOUT and lets
 // all roles run to their end without waiting, loading or multiplying.
 #include <cuda_bf16.h>
@@ -43,48 +40,48 @@ namespace kvx {
 namespace {
 
 constexpr int kTile = 128;       // keys of a tile
-constexpr int kThreads = 384;
-constexpr int kSoft = 256;       // threads of the softmax groups
-constexpr int kMinUnits = 2;     // tiles a block takes at least
+constexpr int kThreads = 256;
+constexpr int kSoft = 128;       // threads of the softmax warps
+constexpr int kMinUnits = 1;     // tiles a block takes at least
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 16.f;    // log2 growth of the maximum that raises the reference
-// Tiles of a group after which its output leaves tensor memory for an fp32 sum: the
+// Tiles after which the output leaves tensor memory for an fp32 sum: the
 // tensor cores truncate each of the 16 additions a tile makes to every output
 // element, which over 200 tiles was measured as 5e-5 of the output, growing
 // linearly; over 16 tiles it stays below 5e-6.
 constexpr int kFold = 16;
-constexpr int kItems = 16;       // item slots: more than V tiles in flight, plus one
-constexpr int kCtlBytes = 1408;
+constexpr int kItems = 8;        // item slots: more than V tiles in flight, plus one
 
-// kTwo: launches with more than 128 query rows a head.
-template <int D, bool kTwo>
-struct Cfg {
-  static constexpr int kRows = kTwo ? 256 : 128;       // query rows of an item
-  static constexpr int kHalves = D / 64;
-  static constexpr int kHalf = kTile * 128;            // bytes of 64 dims of a K or V tile
-  static constexpr int kTileBytes = kHalves * kHalf;
-  static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
-  static constexpr int kQs = kTwo ? 1 : 2;             // query buffers
-  static constexpr int kSlots = 7 * 2 / kHalves - 2;   // of 224 KB, after the queries
-  static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
-  static_assert(kV + 1 < kItems, "items in flight");
-  static constexpr int kBars = 2 * kK + 3 * kV + 6 + 2 * kQs + 2 + kItems;
-  static constexpr int kQ = 0, kKs = kQs * kQBytes;
-  static constexpr int kVs = kKs + kK * kTileBytes, kCtl = kVs + kV * kTileBytes;
-  static constexpr int kSmem = 1024 + kCtl + kBars * 8 + 8 + kCtlBytes;
-  static_assert(kSmem <= 232448, "shared memory of a block");
-};
-
-struct alignas(16) Ctl {  // small shared state behind the barriers
+struct alignas(16) Ctl {  // small shared state
+  uint64_t bars[28];
   uint32_t tmem;
   int abort;
   int more[2];
   int64_t warp_sum[kThreads / 32];
   TreeRange range;
-  TreeItem item[kItems];      // written by warp 11, ahead of the others
+  TreeItem item[kItems];                  // written by warp 7, ahead of the others
   alignas(16) uint32_t notes[kItems][4];  // drafts of an item whose V is not finite
 };
-static_assert(sizeof(Ctl) <= kCtlBytes && offsetof(Ctl, notes) % 16 == 0, "control block");
+static_assert(offsetof(Ctl, notes) % 16 == 0, "read as vectors");
+
+// kRows: room for query rows, 64 or 128. (The products have 128 rows either way; with 64
+// the others read what lies behind Q and reach lanes that nobody looks at.)
+template <int D, int kRows>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kTile * 128;            // bytes of 64 dims of a K or V tile
+  static constexpr int kTileBytes = kHalves * kHalf;
+  static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
+  static constexpr int kSlots = (112 * 1024 - kQBytes) / kTileBytes;  // K and V tiles
+  static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
+  static_assert(kK >= 1 && kV + 1 < kItems, "ring depths");
+  static constexpr int kBars = 2 * kK + 3 * kV + 5 + kItems;
+  static constexpr int kKs = kQBytes, kVs = kKs + kK * kTileBytes;
+  static constexpr int kCtl = kVs + kV * kTileBytes;
+  // Two blocks with the 1 KB that the system keeps in each have to fit in 228 KB.
+  static constexpr int kSmem = kCtl + (int)sizeof(Ctl);
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks per SM");
+};
 
 struct alignas(128) MmaParams {
   CUtensorMap tmK[KVX_MAX_GROUPS];
@@ -111,21 +108,6 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int
     }
   }
 }
-
-// How an item is worked: two groups over all rows (tiles in turn), or a half of
-// the rows each (every tile).
-struct Jobs {
-  int rows, jobs;
-  bool halves;
-  __device__ __forceinline__ Jobs(const TreeParams &p, const TreeItem &it) {
-    rows = tree_rows(p, it);
-    halves = rows > 128;
-    jobs = (it.t1 - it.t0) << (halves ? 1 : 0);
-  }
-  __device__ __forceinline__ int tile(int j) const { return halves ? j >> 1 : j; }
-  __device__ __forceinline__ bool opens(int j) const { return !halves || (j & 1) == 0; }
-  __device__ __forceinline__ bool closes(int j) const { return !halves || (j & 1) == 1; }
-};
 
 // Visible keys among the 32 from draft `u0` on (negative: that many cached
 // tokens first) for new row i.
@@ -263,11 +245,11 @@ __device__ __forceinline__ void add_fold(uint32_t (&x)[16], const float4 *acc, f
   }
 }
 
-// Adds to an output row the non-finite values of the noted drafts that new row i sees, in
-// dims [d0, d1): their weight is positive, so the sum is what they are.
+// Adds to an output row the non-finite values of the noted drafts that new row i
+// sees: their weight is positive, so the sum is what they are.
 template <int D>
-__device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, int i, int d0,
-                                       int d1, const uint32_t *notes, float *out) {
+__device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, int i,
+                                       const uint32_t *notes, float *out) {
   const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
   for (int u = 0; u < hd.T; ++u) {
     const uint32_t bit = 1u << (u & 31);
@@ -277,7 +259,7 @@ __device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, 
     if (pg < 0 || pg >= grp.pages) continue;
     const uint16_t *v = (const uint16_t *)(grp.v + pool_row(p.c, grp, pg, p.c.head_row[hd.h],
                                                             tok & (p.c.P - 1)) * (D * 2));
-    for (int d = d0; d < d1; ++d) {
+    for (int d = 0; d < D; ++d) {
       const float b = __uint_as_float((uint32_t)__ldg(v + d) << 16);
       if (!isfinite(b)) out[d] += b;
     }
@@ -302,11 +284,11 @@ struct TileWalk {
 };
 
 // One warp's part of one role's loads: all K (or V) tiles of the block.
-template <int D, bool kTwo, bool kIsV>
+template <int D, int kRows, bool kIsV>
 __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &range,
                                         uint32_t ring, uint32_t full0, uint32_t empty0,
                                         volatile int *abort, int lane) {
-  using C = Cfg<D, kTwo>;
+  using C = Cfg<D, kRows>;
   constexpr int kN = kIsV ? C::kV : C::kK;
   const TreeParams &p = mp.t;
   const uint64_t pol = policy_evict_first();
@@ -360,28 +342,30 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
   }
 }
 
-template <int D, bool kTwo>
-__global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_constant__ MmaParams mp) {
-  using C = Cfg<D, kTwo>;
+template <int D, int kRows>
+__global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_constant__ MmaParams mp) {
+  using C = Cfg<D, kRows>;
   const TreeParams &p = mp.t;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // tiles start on 1024 bytes
+  Ctl &ctl = *(Ctl *)(smem + C::kCtl);
+  static_assert(C::kBars <= sizeof(ctl.bars) / 8, "barriers");
   const uint32_t base = smem_u32(smem);
-  uint64_t *bars = (uint64_t *)(smem + C::kCtl);
-  Ctl &ctl = *(Ctl *)(bars + (C::kBars + 1) / 2 * 2);
   volatile int *abort = &ctl.abort;
-  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 8 * C::kK;
+  const uint32_t k_full = smem_u32(ctl.bars), k_empty = k_full + 8 * C::kK;
   const uint32_t v_full = k_empty + 8 * C::kK, v_empty = v_full + 8 * C::kV;
   const uint32_t v_ready = v_empty + 8 * C::kV;  // loaded, and cleaned where it has to be
-  const uint32_t s_full = v_ready + 8 * C::kV;   // [2] scores of a group are ready
-  const uint32_t p_ready = s_full + 16;          // [2] weights of a group are ready
-  const uint32_t o_full = p_ready + 16;          // [2] a group's output of the item is complete
-  const uint32_t q_full = o_full + 16;           // [kQs] queries of an item are loaded
-  const uint32_t i_done = q_full + 8 * C::kQs;   // [2] items 0, 2, .. and 1, 3, .. : the
-                                                 // softmax groups are done with Q and O
-  const uint32_t i_full = i_done + 16;           // [kItems] an item is written
+  const uint32_t s_full = v_ready + 8 * C::kV;   // scores of a tile are ready
+  const uint32_t p_ready = s_full + 8;           // weights of a tile are ready
+  const uint32_t o_full = p_ready + 8;           // the output of an item is complete
+  const uint32_t q_full = o_full + 8;            // queries of an item are loaded
+  const uint32_t i_done = q_full + 8;            // the softmax warps are done with an item
+  const uint32_t i_full = i_done + 8;            // [kItems] an item is written
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
+  if (base & 1023u) {  // no toolchain places it so; nothing below would hold
+    if (tid == 0) atomicOr(p.status, KVX_DEV_TIMEOUT);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(k_full + 8 * i, 1);
@@ -392,27 +376,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(v_ready + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_ready + 8 * i, 4);
-      mbar_init(o_full + 8 * i, 1);
-      mbar_init(i_done + 8 * i, kSoft / 32);
-    }
-    for (int i = 0; i < C::kQs; ++i) mbar_init(q_full + 8 * i, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_ready, kSoft / 32);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, 1);
+    mbar_init(i_done, kSoft / 32);
     for (int i = 0; i < kItems; ++i) mbar_init(i_full + 8 * i, 1);
     ctl.abort = 0;
     fence_barrier_init();
   }
-  if (warp == 10) tmem_alloc(smem_u32(&ctl.tmem), 512);
-  if (warp >= 8 && warp < 10 && lane < p.c.G)
-    prefetch_tensormap(warp == 8 ? &mp.tmK[lane] : &mp.tmV[lane]);
-  if (warp == 11 && lane == 0) prefetch_tensormap(&mp.tmQ);
+  if (warp == 6) tmem_alloc(smem_u32(&ctl.tmem), 256);
+  if (warp >= 4 && warp < 6 && lane < p.c.G)
+    prefetch_tensormap(warp == 4 ? &mp.tmK[lane] : &mp.tmV[lane]);
+  if (warp == 7 && lane == 0) prefetch_tensormap(&mp.tmQ);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
-  // columns: S of both groups, O of both groups
-  const uint32_t tS = tmem, tO = tmem + 2 * kTile;
+  const uint32_t tS = ctl.tmem, tO = tS + kTile;  // TMEM columns of S and O
   pdl_wait();
   const TreeRange range = tree_range<kThreads, kTile>(p, kMinUnits, ctl.warp_sum, &ctl.range);
   // Item i of the block (the last is followed by one without tiles).
@@ -421,190 +401,160 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     return ctl.item[i % kItems];
   };
 
-  // the softmax groups take registers from the other roles: 256 * 208 + 128 * 88
-  // = 384 * 168, the launch's
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-      produce<D, kTwo, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
-    } else if (warp == 9) {
-      produce<D, kTwo, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
-    } else if (warp == 10) {
-      if (lane == 0) {
-        constexpr uint32_t kS = mma_desc(128, kTile, false), kO = mma_desc(128, D, true);
-        int nk = 0, nv = 0;
-        int np[2] = {0, 0};
-        for (int i = 0;; ++i) {
-          const TreeItem it = item_at(i);
-          if (*abort || it.t0 >= it.t1) break;
-          const Jobs jb(p, it);
-          const int qb = i % C::kQs;
-          wait(q_full + 8 * qb, (i / C::kQs) & 1, abort, p.status);
-          if (i > 0) wait(i_done + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, abort, p.status);
+  if (warp == 4) {
+    produce<D, kRows, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
+  } else if (warp == 5) {
+    produce<D, kRows, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
+  } else if (warp == 6) {
+    if (lane == 0) {
+      constexpr uint32_t kS = mma_desc(128, kTile, false), kO = mma_desc(128, D, true);
+      int n = 0;
+      for (int i = 0;; ++i) {
+        const TreeItem &it = item_at(i);
+        const int tiles = it.t1 - it.t0;
+        if (*abort || tiles <= 0) break;
+        // (the queries are loaded once the item before is done with Q and O)
+        wait(q_full, i & 1, abort, p.status);
+        for (int j = 0; j < tiles; ++j, ++n) {
+          const int ks = n % C::kK, vs = n % C::kV;
+          wait(k_full + 8 * ks, (n / C::kK) & 1, abort, p.status);
           tc_fence_after();
-          const uint32_t q0 = base + C::kQ + qb * C::kQBytes;
-          auto weigh = [&](int j) {  // O += P V of job j
-            const int w = j & 1, slot = nv % C::kV;
-            if (jb.opens(j)) wait(v_ready + 8 * slot, (nv / C::kV) & 1, abort, p.status);
-            wait(p_ready + 8 * w, np[w]++ & 1, abort, p.status);
-            tc_fence_after();
-            if (!*abort) {
-              const bool first = ((j >> 1) % kFold) == 0;  // overwrites O
-              const uint32_t v = base + C::kVs + slot * C::kTileBytes;
-              const uint32_t a = tS + w * kTile, d = tO + w * 128;
+          if (!*abort) {
+            // (P of the tile before was read by products issued before: MMAs of one
+            // thread run in the order of issue)
+            const uint32_t k = base + C::kKs + ks * C::kTileBytes;
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k) {
-                const uint64_t b = smem_desc(v + k * 16 * 128, C::kHalf);
-                mma_ts(d, a + 16 * k, b, kO, !(first && k == 0));
-                mma_ts(d, a + 16 * k + 8, b, kO, true);
-              }
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = (e & 3) * 32;
+              mma_ss(tS, smem_desc(base + (e >> 2) * C::kQHalf + off, 16),
+                     smem_desc(k + (e >> 2) * C::kHalf + off, 16), kS, e > 0);
             }
-            if (jb.closes(j)) {
-              mma_commit(v_empty + 8 * slot);
-              ++nv;
-            }
-            if (j + 2 >= jb.jobs) mma_commit(o_full + 8 * w);
-          };
-          for (int j = 0; j < jb.jobs; ++j) {
-            const int w = j & 1, slot = nk % C::kK;
-            if (jb.opens(j)) wait(k_full + 8 * slot, (nk / C::kK) & 1, abort, p.status);
-            if (!*abort) {
-              // S of this group was last read by the products of job j - 2, issued before:
-              // MMAs of one thread run in the order of issue
-              const uint32_t q = q0 + (jb.halves ? w * (128 * 128) : 0);
-              const uint32_t k = base + C::kKs + slot * C::kTileBytes;
-#pragma unroll
-              for (int e = 0; e < D / 16; ++e) {
-                const uint32_t off = (e & 3) * 32;
-                mma_ss(tS + w * kTile, smem_desc(q + (e >> 2) * C::kQHalf + off, 16),
-                       smem_desc(k + (e >> 2) * C::kHalf + off, 16), kS, e > 0);
-              }
-            }
-            mma_commit(s_full + 8 * w);
-            if (jb.closes(j)) {
-              mma_commit(k_empty + 8 * slot);
-              ++nk;
-            }
-            if (j > 0) weigh(j - 1);
           }
-          weigh(jb.jobs - 1);
+          mma_commit(s_full);
+          mma_commit(k_empty + 8 * ks);
+          wait(v_ready + 8 * vs, (n / C::kV) & 1, abort, p.status);
+          wait(p_ready, n & 1, abort, p.status);
+          tc_fence_after();
+          if (!*abort) {
+            const bool first = j % kFold == 0;  // overwrites O
+            const uint32_t v = base + C::kVs + vs * C::kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) {
+              const uint64_t b = smem_desc(v + k * 16 * 128, C::kHalf);
+              mma_ts(tO, tS + 16 * k, b, kO, !(first && k == 0));
+              mma_ts(tO, tS + 16 * k + 8, b, kO, true);
+            }
+          }
+          mma_commit(v_empty + 8 * vs);
         }
+        mma_commit(o_full);
       }
-      __syncwarp();
-    } else {
-      // items and queries for the other roles, and the V tiles that have to be cleaned
-      TreeCursor<kTile> cur(p, range);
-      TreeItem it;
-      bool more = true, any_item = false;
-      for (int i = 0, n = 0; more; ++i) {
-        more = cur.next(p, it) && !__any_sync(0xffffffffu, *abort);
-        if (!more) {
-          if (lane == 0) tree_describe(p, range, any_item ? &it : nullptr);
-          it.t0 = it.t1 = 0;
-        }
-        any_item = more;
-        if (lane == 0) {
-          ctl.item[i % kItems] = it;
-          mbar_arrive(i_full + 8 * (i % kItems));
-        }
-        if (!more) break;
-        const int qb = i % C::kQs;
-        if (i >= C::kQs) {  // the item that had this buffer is done with it
-          const int b = i - C::kQs;
-          wait(i_done + 8 * (b & 1), (b >> 1) & 1, abort, p.status);
-        }
-        if (!__any_sync(0xffffffffu, *abort)) {
-          // lane -> (box of 8 new rows, half): at most 16 * 2 of them
-          const int i0 = tree_first(p, it), boxes = (tree_rows(p, it) + kTreeBox * p.c.g - 1) /
-                                                    (kTreeBox * p.c.g);
-          const uint32_t bytes = kTreeBox * p.c.g * 128;
-          if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * qb, boxes * bytes * C::kHalves);
-          __syncwarp();
-          const int bx = lane / C::kHalves, half = lane % C::kHalves;
-          if (bx < boxes)
-            tma_load_5d(base + C::kQ + qb * C::kQBytes + half * C::kQHalf + bx * bytes, &mp.tmQ, 0,
-                        half, it.head.h * p.c.g, it.head.q0 + i0 + bx * kTreeBox, 0,
-                        q_full + 8 * qb, policy_evict_first());
-        }
-        const int len = it.head.n + it.head.T;
-        uint32_t notes[4] = {0, 0, 0, 0};
-        for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
-          const int slot = n % C::kV, t0 = tile * kTile;
-          wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p.status);
-          if (t0 + kTile > it.head.n) {
-            const int first = max(0, it.head.n - t0), valid = min(kTile, len - t0);
-            // chunk (16 bytes) x of a row: half x >> 3, place x & 7
-            constexpr int CPR = D / 8, RPW = 32 / CPR;  // rows a warp covers at once
-            const int x = lane % CPR;
-            uint8_t *v = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * C::kHalf + (x & 7) * 16;
+    }
+    __syncwarp();
+  } else if (warp == 7) {
+    // items and queries for the other roles, and the V tiles that have to be cleaned
+    TreeCursor<kTile> cur(p, range);
+    TreeItem it;
+    bool more = true, any_item = false;
+    for (int i = 0, n = 0; more; ++i) {
+      more = cur.next(p, it) && !__any_sync(0xffffffffu, *abort);
+      if (!more) {
+        if (lane == 0) tree_describe(p, range, any_item ? &it : nullptr);
+        it.t0 = it.t1 = 0;
+      }
+      any_item = more;
+      if (lane == 0) {
+        ctl.item[i % kItems] = it;
+        mbar_arrive(i_full + 8 * (i % kItems));
+      }
+      if (!more) break;
+      if (i > 0) wait(i_done, (i - 1) & 1, abort, p.status);
+      if (!__any_sync(0xffffffffu, *abort)) {
+        // lane -> (box of 8 new rows, half): at most 16 * 2 of them
+        const int boxes = (tree_rows(p, it) + kTreeBox * p.c.g - 1) / (kTreeBox * p.c.g);
+        const uint32_t bytes = kTreeBox * p.c.g * 128;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, boxes * bytes * C::kHalves);
+        __syncwarp();
+        const int bx = lane / C::kHalves, half = lane % C::kHalves;
+        if (bx < boxes)
+          tma_load_5d(base + half * C::kQHalf + bx * bytes, &mp.tmQ, 0, half, it.head.h * p.c.g,
+                      it.head.q0 + tree_first(p, it) + bx * kTreeBox, 0, q_full,
+                      policy_evict_first());
+      }
+      const int len = it.head.n + it.head.T;
+      uint32_t notes[4] = {0, 0, 0, 0};
+      for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
+        const int slot = n % C::kV, t0 = tile * kTile;
+        wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p.status);
+        if (t0 + kTile > it.head.n) {
+          const int first = max(0, it.head.n - t0), valid = min(kTile, len - t0);
+          // chunk (16 bytes) x of a row: half x >> 3, place x & 7
+          constexpr int CPR = D / 8, RPW = 32 / CPR;  // rows a warp covers at once
+          const int x = lane % CPR;
+          uint8_t *v = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * C::kHalf + (x & 7) * 16;
 #pragma unroll 4
-            for (int row = valid + lane / CPR; row < kTile; row += RPW)
-              *(uint4 *)(v + row * 128) = make_uint4(0, 0, 0, 0);
-            for (int r0 = first; r0 < valid; r0 += 4 * RPW) {
-              uint4 y[4];
+          for (int row = valid + lane / CPR; row < kTile; row += RPW)
+            *(uint4 *)(v + row * 128) = make_uint4(0, 0, 0, 0);
+          for (int r0 = first; r0 < valid; r0 += 4 * RPW) {
+            uint4 y[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int row = r0 + k * RPW + lane / CPR;
-                y[k] = row < valid ? *(const uint4 *)(v + row * 128) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 4; ++k) {
+              const int row = r0 + k * RPW + lane / CPR;
+              y[k] = row < valid ? *(const uint4 *)(v + row * 128) : make_uint4(0, 0, 0, 0);
+            }
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t e[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                odd |= (e[i] & 0x7f80u) == 0x7f80u || (e[i] & 0x7f800000u) == 0x7f800000u;
+            }
+            if (!__any_sync(0xffffffffu, odd)) continue;
+            // rare: zero the elements and note their drafts
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const int row = r0 + k * RPW + lane / CPR;
+              bool hit = false;
+              if (row < valid) {
+                uint32_t *at = (uint32_t *)(v + row * 128);
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t e = at[i];
+                  const uint32_t bad = ((e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+                                       ((e & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+                  if (bad) at[i] = e & ~bad;
+                  hit |= bad != 0;
+                }
               }
-              bool odd = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t e[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+              const uint32_t who = __ballot_sync(0xffffffffu, hit);
+              for (int rr = 0; rr < RPW; ++rr) {
+                const int u = t0 + r0 + k * RPW + rr - it.head.n;
+                const uint32_t part = CPR == 32 ? ~0u : (1u << (CPR % 32)) - 1u;
+                if (!(who & (part << (rr * CPR)))) continue;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  odd |= (e[i] & 0x7f80u) == 0x7f80u || (e[i] & 0x7f800000u) == 0x7f800000u;
+                  if (i == (u >> 5)) notes[i] |= 1u << (u & 31);
               }
-              if (!__any_sync(0xffffffffu, odd)) continue;
-              // rare: zero the elements and note their drafts
-#pragma unroll 1
-              for (int k = 0; k < 4; ++k) {
-                const int row = r0 + k * RPW + lane / CPR;
-                bool hit = false;
-                if (row < valid) {
-                  uint32_t *at = (uint32_t *)(v + row * 128);
-                  for (int i = 0; i < 4; ++i) {
-                    const uint32_t e = at[i];
-                    const uint32_t bad = ((e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
-                                         ((e & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-                    if (bad) at[i] = e & ~bad;
-                    hit |= bad != 0;
-                  }
-                }
-                const uint32_t who = __ballot_sync(0xffffffffu, hit);
-                for (int rr = 0; rr < RPW; ++rr) {
-                  const int u = t0 + r0 + k * RPW + rr - it.head.n;
-                  const uint32_t part = CPR == 32 ? ~0u : (1u << (CPR % 32)) - 1u;
-                  if (!(who & (part << (rr * CPR)))) continue;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (i == (u >> 5)) notes[i] |= 1u << (u & 31);
-                }
-              }
-            }
-            if (lane < 4) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (e == lane) ctl.notes[i % kItems][e] = notes[e];
             }
           }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_ready + 8 * slot);
+          if (lane < 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e == lane) ctl.notes[i % kItems][e] = notes[e];
+          }
         }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_ready + 8 * slot);
       }
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int w = warp >> 2;                       // group
-    const int lr = (warp & 3) * 32 + lane;         // TMEM lane
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tS + w * kTile + lanes, o_at = tO + w * 128 + lanes;
-    auto fold_at = [&](int grp) {  // this lane's float4s of a group, 128 apart
-      return (float4 *)p.fold + ((size_t)blockIdx.x * 2 + grp) * (D / 4) * 128 + lr;
-    };
-    int ns = 0, no0 = 0, no1 = 0;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t s_at = tS + lanes, o_at = tO + lanes;
+    // this lane's folded float4s, 128 apart
+    float4 *acc = (float4 *)p.fold + (size_t)blockIdx.x * (D / 4) * 128 + tid;
+    int n = 0;
     // One thread says whether item i is worked on, so that all agree even while
     // a wait runs out; a barrier follows.
     auto decide = [&](int i) {
@@ -616,123 +566,79 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     named_sync(1, kSoft);
     for (int i = 0; ctl.more[i & 1]; ++i) {
       const TreeItem &it = ctl.item[i % kItems];  // in shared memory: not worth registers
-      const Jobs jb(p, it);
-      const int row = jb.halves ? 128 * w + lr : lr;
-      const bool live = row - lane < jb.rows;  // of the warp
+      const int rows = tree_rows(p, it), tiles = it.t1 - it.t0;
+      const bool live = warp * 32 < rows;
       float m = -INFINITY, l = 0.f;  // reference of the weights (log2 units), sum
       float m_acc = -INFINITY;       // reference of the folded output
-      for (int j = w; j < jb.jobs; j += 2) {
-        const int t0 = (it.t0 + jb.tile(j)) * kTile;
-        wait(s_full + 8 * w, ns++ & 1, abort, p.status);
+      for (int j = 0; j < tiles; ++j) {
+        const int t0 = (it.t0 + j) * kTile;
+        wait(s_full, n++ & 1, abort, p.status);
         tc_fence_after();
         if (live) {
-          const bool turn = j >= 2 && ((j >> 1) % kFold) == 0;  // O starts afresh
+          const bool turn = j > 0 && j % kFold == 0;  // O starts afresh
           if (turn) {
             // fold the tensor cores' sum of the last kFold tiles into fp32 (see kFold)
             const float f = tree_weight(m_acc, m);
-            float4 *acc = fold_at(w);
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t x[16];
               tmem_get16(o_at + 16 * c, x);
+              if (j > kFold) add_fold(x, acc + 4 * c * 128, f);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if ((j >> 1) > kFold) v = __ldcg(acc + (4 * c + e) * 128);
-                v.x = fmaf(v.x, f, __uint_as_float(x[4 * e]));
-                v.y = fmaf(v.y, f, __uint_as_float(x[4 * e + 1]));
-                v.z = fmaf(v.z, f, __uint_as_float(x[4 * e + 2]));
-                v.w = fmaf(v.w, f, __uint_as_float(x[4 * e + 3]));
-                __stcg(acc + (4 * c + e) * 128, v);
-              }
+              for (int e = 0; e < 4; ++e)
+                __stcg((uint4 *)acc + (4 * c + e) * 128,
+                       make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
             }
             m_acc = m;
           }
           if (t0 + kTile > it.head.n)
-            hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, row), row < jb.rows,
+            hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, tid), tid < rows,
                       t0 - it.head.n, s_at);
-          soft_tile<D>(s_at, o_at, p.scale_log2, j >= 2 && !turn, m, l);
+          soft_tile<D>(s_at, o_at, p.scale_log2, j > 0 && !turn, m, l);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + 8 * w);
+        if (lane == 0) mbar_arrive(p_ready);
       }
-      // ---- epilogue. A half waits for its own output alone; the barrier makes the
-      // other's phase known. All products that read Q are done, so its buffer takes
-      // the groups' (m, l, weight of the folded part).
-      if (!jb.halves || w == 0) wait(o_full, no0 & 1, abort, p.status);
-      if (jb.halves ? w == 1 : jb.jobs > 1) wait(o_full + 8, no1 & 1, abort, p.status);
-      ++no0;
-      no1 += jb.jobs > 1;
+      // ---- epilogue
+      wait(o_full, i & 1, abort, p.status);
       tc_fence_after();
-      float4 *st = (float4 *)(smem + C::kQ + (i % C::kQs) * C::kQBytes);
-      float f0 = 1.f, f1 = 0.f, fa = tree_weight(m_acc, m), fb = 0.f;
-      if (!jb.halves) st[w * 128 + lr] = make_float4(m, l, fa, 0.f);
-      decide(i + 1);
-      named_sync(1, kSoft);
-      if (!jb.halves) {
-        // both groups hold partial states of the same rows
-        const float4 a = st[lr], b = st[128 + lr];
-        m = fmaxf(a.x, b.x);
-        f0 = tree_weight(a.x, m);
-        f1 = tree_weight(b.x, m);
-        l = f0 * a.y + f1 * b.y;
-        fa = a.z;
-        fb = b.z;
-      }
       if (live) {
-        const bool whole = tree_whole(it), ok = row < jb.rows;
-        const int row0 = it.head.q0 + tree_first(p, it);
-        float *dst = tree_out(p, row0, it.head.h, row);
+        const bool whole = tree_whole(it), ok = tid < rows, folded = tiles > kFold;
+        float *dst = tree_out(p, it.head.q0 + tree_first(p, it), it.head.h, tid);
+        float f = 1.f;
         if (whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          f0 *= inv;
-          f1 *= inv;
+          f = l == 0.f ? 0.f : 1.f / l;
         } else {
-          const size_t at = (size_t)tree_slot(range, it) * C::kRows + row;
+          const size_t at = (size_t)tree_slot(range, it) * p.group_rows + tid;
           dst = p.part_o + at * D;
-          if (ok && (jb.halves || w == 0)) p.part_ml[at] = make_float2(m, l);
+          if (ok) p.part_ml[at] = make_float2(m, l);
         }
-        // The first output is group 0's, or the half's own; the second, group 1's where
-        // it had a tile.
-        const int own = jb.halves ? w : 0;
-        const bool both = !jb.halves && jb.jobs > 1;
-        const bool fold0 = jb.jobs > 2 * kFold + own, fold1 = both && jb.jobs > 2 * kFold + 1;
-        bool odd = false;
-        if (it.t1 * kTile > it.head.n) {
-          const uint4 n = *(const uint4 *)ctl.notes[i % kItems];
-          odd = (n.x | n.y | n.z | n.w) != 0;
-        }
-        const int c0 = jb.halves ? 0 : w * (D / 32), c1 = jb.halves ? D / 16 : c0 + D / 32;
+        const float fa = tree_weight(m_acc, m);
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          uint32_t x[16], y[16];
-          tmem_get16(tO + own * 128 + lanes + 16 * c, x);
-          if (fold0) add_fold(x, fold_at(own) + 4 * c * 128, fa);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f0);
-          if (both) {
-            tmem_get16(tO + 128 + lanes + 16 * c, y);
-            if (fold1) add_fold(y, fold_at(1) + 4 * c * 128, fb);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f1, __uint_as_float(x[e])));
-          }
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t x[16];
+          tmem_get16(o_at + 16 * c, x);
+          if (folded) add_fold(x, acc + 4 * c * 128, fa);
           if (ok) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              *(uint4 *)(dst + 16 * c + 4 * e) =
-                  make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+              *(float4 *)(dst + 16 * c + 4 * e) =
+                  make_float4(__uint_as_float(x[4 * e]) * f, __uint_as_float(x[4 * e + 1]) * f,
+                              __uint_as_float(x[4 * e + 2]) * f, __uint_as_float(x[4 * e + 3]) * f);
           }
         }
-        if (odd && ok)
-          add_notes<D>(p, it.head, tree_first(p, it) + tree_div_g(p, row), 16 * c0, 16 * c1,
-                       ctl.notes[i % kItems], dst);
+        if (it.t1 * kTile > it.head.n) {
+          const uint4 o = *(const uint4 *)ctl.notes[i % kItems];
+          if ((o.x | o.y | o.z | o.w) && ok)
+            add_notes<D>(p, it.head, tree_first(p, it) + tree_div_g(p, tid),
+                         ctl.notes[i % kItems], dst);
+        }
       }
       tc_fence_before();
-      fence_async_shared();  // the next queries land where (m, l) were
-      __syncwarp();
-      if (lane == 0) mbar_arrive(i_done + 8 * (i & 1));
+      decide(i + 1);
+      named_sync(1, kSoft);
+      if (lane == 0) mbar_arrive(i_done);
     }
   }
   __syncthreads();
@@ -748,36 +654,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  if (warp == 10) {
+  if (warp == 6) {
     tc_fence_after();
-    tmem_free(tmem, 512);
+    tmem_free(tS, 256);
   }
 }
 
-template <int D, bool kTwo>
-cudaError_t launch_dt(const MmaParams &mp, int blocks, cudaStream_t st) {
-  using C = Cfg<D, kTwo>;
-  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, kTwo>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+template <int D, int kRows>
+cudaError_t launch_dr(const MmaParams &mp, int blocks, cudaStream_t st) {
+  using C = Cfg<D, kRows>;
+  constexpr int bytes = C::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, kRows>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, kTwo>, mp);
+  e = cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, kRows>, mp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 int tree_mma_tokens(int rows, int g) { return rows / (kTreeBox * g) * kTreeBox; }
-int tree_mma_rows(int max_q, int g) { return max_q > tree_mma_tokens(128, g) ? 256 : 128; }
+int tree_mma_rows(int max_q, int g) { return max_q > tree_mma_tokens(64, g) ? 128 : 64; }
+int tree_mma_blocks_per_sm() { return 2; }
 
 cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
                             const CUtensorMap *v_maps, const CUtensorMap &q_map, int blocks,
@@ -787,10 +695,10 @@ cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
   memcpy(mp.tmV, v_maps, sizeof(mp.tmV));
   mp.tmQ = q_map;
   mp.t = p;
-  const bool two = p.group_rows > 128;
+  const bool few = p.group_rows == 64;
   if (p.c.D == 128)
-    return two ? launch_dt<128, true>(mp, blocks, st) : launch_dt<128, false>(mp, blocks, st);
-  return two ? launch_dt<64, true>(mp, blocks, st) : launch_dt<64, false>(mp, blocks, st);
+    return few ? launch_dr<128, 64>(mp, blocks, st) : launch_dr<128, 128>(mp, blocks, st);
+  return few ? launch_dr<64, 64>(mp, blocks, st) : launch_dr<64, 128>(mp, blocks, st);
 }
 
 }  // namespace kvx
