@@ -78,20 +78,20 @@ bool encode_q_map(CUtensorMap *tm, const kvx_cache *c, const void *q, int64_t st
   return encode(tm, q, dims, strides, box);
 }
 
-// What a call's max_q fixes: row groups, blocks and the workspace.
+// Row groups, blocks and the workspace of a cache's attention calls.
 struct TreeShape {
   int blocks, tokens, rows;
   TreeWs ws;
 };
-int tree_shape(const kvx_cache *c, int max_q, TreeShape *t) {
+int tree_shape(const kvx_cache *c, TreeShape *t) {
   int32_t sms = 0;
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
   const int g = c->dev.g;
   const bool f32 = c->shape.dtype == KVX_F32;
   t->blocks = sms * (f32 ? tree_simt_blocks_per_sm() : tree_mma_blocks_per_sm());
-  t->rows = f32 ? tree_simt_rows() : tree_mma_rows(max_q, g);
-  t->tokens = f32 ? tree_simt_tokens(g) : tree_mma_tokens(t->rows, g);
+  t->rows = f32 ? tree_simt_rows() : tree_mma_rows();
+  t->tokens = f32 ? tree_simt_tokens(g) : tree_mma_tokens(g);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);
   TreeWs &w = t->ws;
@@ -237,7 +237,7 @@ extern "C" int kvx_tree_attn_workspace_bytes(const kvx_cache *c, int32_t max_q, 
   if (!c || !bytes) return KVX_EINVAL;
   if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
   TreeShape t;
-  const int rc = tree_shape(c, max_q, &t);
+  const int rc = tree_shape(c, &t);
   if (rc == KVX_OK) *bytes = t.ws.total;
   return rc;
 }
@@ -258,7 +258,7 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   if (!p.q_stride) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   TreeShape t;
-  const int rc = tree_shape(c, max_q, &t);
+  const int rc = tree_shape(c, &t);
   if (rc != KVX_OK) return rc;
   const TreeWs &w = t.ws;
   if (workspace_bytes < w.total) return KVX_EINVAL;

@@ -113,8 +113,8 @@ constexpr int kTreeBox = 8;     // new rows of a query load
 cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
                             const CUtensorMap *v_maps, const CUtensorMap &q_map, int blocks,
                             cudaStream_t st);
-int tree_mma_rows(int max_q, int g);   // room for query rows (64 or 128) ...
-int tree_mma_tokens(int rows, int g);  // ... and the new rows that fill it
+int tree_mma_tokens(int g);
+int tree_mma_rows();
 int tree_mma_blocks_per_sm();
 // Folds the partials of split row groups (after either kernel).
 cudaError_t launch_tree_merge(const TreeParams &p, int blocks, cudaStream_t st);

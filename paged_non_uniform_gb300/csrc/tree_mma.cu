@@ -9,12 +9,14 @@
 // independent of each other, so that one's item changes and softmax run under the
 // other's loads and products; each walks its items (tree_split.cuh) in tiles of
 // 128 keys:
-//  * warps 4 and 5 load K and V tiles from their pages into two rings (bulk
+//  * warps 8 and 9 load K and V tiles from their pages into two rings (bulk
 //    tensor loads, one box of min(P, 128) rows x 64 dims per lane, landing as
 //    [half][128 rows][128 bytes], 128-byte swizzled);
-//  * warp 6 issues the MMAs: S, then O += P V of the tile;
-//  * warps 0-3 do the softmax, one query row per thread;
-//  * warp 7 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
+//  * warp 10 issues the MMAs: S, then O += P V of the tile;
+//  * warps 0-3 and 4-7 do the softmax: a query row belongs to two threads, one for each
+//    half of a tile's keys (a thread can only reach one lane of TMEM). They agree on
+//    the row's reference in one barrier with an OR a tile, and keep sums of their own;
+//  * warp 11 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
 //    8 new rows x the g heads) and cleans the V tiles that hold drafts or the
 //    head's end: rows past the end are zeroed (stale or padding data), and
 //    non-finite values of drafts are replaced by zero and noted, because a weight
@@ -40,8 +42,8 @@ namespace kvx {
 namespace {
 
 constexpr int kTile = 128;       // keys of a tile
-constexpr int kThreads = 256;
-constexpr int kSoft = 128;       // threads of the softmax warps
+constexpr int kThreads = 384;
+constexpr int kSoft = 256;       // threads of the softmax warps
 constexpr int kMinUnits = 1;     // tiles a block takes at least
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 16.f;    // log2 growth of the maximum that raises the reference
@@ -59,24 +61,22 @@ struct alignas(16) Ctl {  // small shared state
   int more[2];
   int64_t warp_sum[kThreads / 32];
   TreeRange range;
-  TreeItem item[kItems];                  // written by warp 7, ahead of the others
+  TreeItem item[kItems];                  // written by warp 11, ahead of the others
   alignas(16) uint32_t notes[kItems][4];  // drafts of an item whose V is not finite
+  float swap[2][128];                     // between the two threads of a row
 };
 static_assert(offsetof(Ctl, notes) % 16 == 0, "read as vectors");
 
-// kRows: room for query rows, 64 or 128. (The products have 128 rows either way; with 64
-// the others read what lies behind Q and reach lanes that nobody looks at.)
-template <int D, int kRows>
+template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalf = kTile * 128;            // bytes of 64 dims of a K or V tile
-  static constexpr int kTileBytes = kHalves * kHalf;
-  static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
-  static constexpr int kSlots = (112 * 1024 - kQBytes) / kTileBytes;  // K and V tiles
+  static constexpr int kHalf = 128 * 128;              // bytes of 64 dims of 128 rows
+  static constexpr int kTileBytes = kHalves * kHalf;   // a Q, K or V tile
+  static constexpr int kSlots = (111 * 1024 - kTileBytes) / kTileBytes;  // K and V tiles
   static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
   static_assert(kK >= 1 && kV + 1 < kItems, "ring depths");
   static constexpr int kBars = 2 * kK + 3 * kV + 5 + kItems;
-  static constexpr int kKs = kQBytes, kVs = kKs + kK * kTileBytes;
+  static constexpr int kKs = kTileBytes, kVs = kKs + kK * kTileBytes;
   static constexpr int kCtl = kVs + kV * kTileBytes;
   // Two blocks with the 1 KB that the system keeps in each have to fit in 228 KB.
   static constexpr int kSmem = kCtl + (int)sizeof(Ctl);
@@ -119,118 +119,84 @@ __device__ __forceinline__ uint32_t seen_word(const TreeParams &p, const TreeHea
   return s ? __funnelshift_r(lo, tree_mask_word(p, t, i, w + 1), s) : lo;
 }
 
-// Scores of keys that the row does not see become -inf (a tile with drafts or
-// the head's end).
+// Scores of keys that the row does not see become -inf, in 64 columns whose first key is
+// draft u0 (a tile with drafts or the head's end).
 __device__ __forceinline__ void hide_keys(const TreeParams &p, const TreeHead &t, int row_i,
                                           bool row_ok, int u0, uint32_t s_at) {
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 64; c += 32) {
     uint32_t x[32];
-    const uint32_t seen = row_ok ? seen_word(p, t, row_i, u0 + 32 * c) : 0u;
-    tmem_get32(s_at + 32 * c, x);
+    const uint32_t seen = row_ok ? seen_word(p, t, row_i, u0 + c) : 0u;
+    tmem_get32(s_at + c, x);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (!((seen >> e) & 1u)) x[e] = __float_as_uint(-INFINITY);
-    tmem_st32(s_at + 32 * c, x);
+    tmem_st32(s_at + c, x);
   }
   tmem_wait_st();
 }
 
-// Weights of 32 keys from their scores: per 16 keys, 8 columns of high parts and 8
-// of residuals (two keys a column), the A operands of two products.
-__device__ __forceinline__ void weigh32(uint32_t (&x)[32], uint64_t scale2, uint64_t ref2,
-                                        uint64_t (&sum)[2]) {
-  uint32_t y[32];
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float a, b;
-    unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, ref2), a, b);
-    a = ex2(a);
-    b = ex2(b);
-    const uint64_t ab = pack2(a, b);
-    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], ab);
-    const uint32_t hi = pack_bf16(a, b);
-    float ra, rb;
-    unpack2(add2(ab, pack2(__uint_as_float((hi << 16) ^ 0x80000000u),
-                           __uint_as_float((hi & 0xffff0000u) ^ 0x80000000u))),
-            ra, rb);
-    const int at = (e & 16) + ((e & 15) >> 1);
-    y[at] = hi;
-    y[at + 8] = pack_bf16(ra, rb);
-  }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = y[e];
-}
-
-// A row's reference m has to rise: by a whole number of log2 units, so that what was
-// weighed before -- O, and the first `done` blocks of 32 keys of this tile -- is
-// rescaled exactly. Rare after a row's first keys.
-template <int D>
-__device__ __noinline__ float raise_ref(uint32_t s_at, uint32_t o_at, bool have, int done,
-                                        float top, float m) {
-  const bool move = top > m + kGrow;
-  if (!__any_sync(0xffffffffu, move && m != -INFINITY)) return move ? top : m;
-  const float mn = !move ? m : m == -INFINITY ? top : m + ceilf(top - m);
-  const float f = mn == m ? 1.f : tree_weight(m, mn);
-  for (int c = 0; c < done * 32; c += 16) {
-    uint32_t y[16];
-    tmem_get16(s_at + c, y);
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      y[e] = pack_bf16(__uint_as_float(y[e] << 16) * f, __uint_as_float(y[e] & 0xffff0000u) * f);
-    tmem_st16(s_at + c, y);
-  }
-  if (have) {
-    for (int c = 0; c < D; c += 16) {
-      uint32_t y[16];
-      tmem_get16(o_at + c, y);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-      tmem_st16(o_at + c, y);
-    }
-  }
-  return mn;
-}
-
-// One row's softmax of one tile, in one pass: scores (TMEM) to weights (TMEM, in
-// place), the running reference m and sum l. The reference is the maximum of a row's
-// first keys and rises only when a score passes it by more than kGrow; weights and
-// sums are then at most 2^kGrow times larger than with the running maximum, which
-// fp32 and bf16 hold as exactly. have: O holds products of earlier tiles.
-template <int D>
-__device__ __forceinline__ void soft_tile(uint32_t s_at, uint32_t o_at, float scale, bool have,
-                                          float &m, float &l) {
-  const uint64_t scale2 = pack2(scale, scale);
-  uint64_t sum[2] = {0, 0};
+// The largest of 64 scores of a row.
+__device__ __forceinline__ float top_score(uint32_t s_at) {
+  float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 64; c += 32) {
     uint32_t x[32];
-    tmem_get32(s_at + 32 * c, x);
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    tmem_get32(s_at + c, x);
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       mx0 = max3(mx0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
       mx1 = max3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
     }
-    const float top = fmaxf(mx0, mx1) * scale;
-    if (__any_sync(0xffffffffu, top > m + kGrow)) {
-      const float mn = raise_ref<D>(s_at, o_at, have, c, top, m);
-      const float f = mn == m ? 1.f : tree_weight(m, mn);
-      const uint64_t f2 = pack2(f, f);
-      l *= f;
-      sum[0] = mul2(sum[0], f2);
-      sum[1] = mul2(sum[1], f2);
-      m = mn;
+  }
+  return fmaxf(mx0, mx1);
+}
+
+// x *= f over `cols` TMEM columns.
+__device__ __noinline__ void rescale(uint32_t at, int cols, float f) {
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t y[16];
+    tmem_get16(at + c, y);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+    tmem_st16(at + c, y);
+  }
+  tmem_wait_st();
+}
+
+// Weights of 64 keys of a row from their scores, in place: per 16 keys, 8 columns of
+// high parts and 8 of residuals (two keys a column), the A operands of two products.
+// Returns their sum.
+__device__ __forceinline__ float weigh(uint32_t s_at, float scale, float ref) {
+  const uint64_t scale2 = pack2(scale, scale), ref2 = pack2(-ref, -ref);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t x[16], y[16];
+    tmem_get16(s_at + c, x);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float a, b;
+      unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, ref2), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      const uint64_t ab = pack2(a, b);
+      sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], ab);
+      const uint32_t hi = pack_bf16(a, b);
+      float ra, rb;
+      unpack2(add2(ab, pack2(__uint_as_float((hi << 16) ^ 0x80000000u),
+                             __uint_as_float((hi & 0xffff0000u) ^ 0x80000000u))),
+              ra, rb);
+      y[e >> 1] = hi;
+      y[8 + (e >> 1)] = pack_bf16(ra, rb);
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    weigh32(x, scale2, pack2(-ref, -ref), sum);
-    tmem_st32(s_at + 32 * c, x);
+    tmem_st16(s_at + c, y);
   }
   float s0, s1, s2, s3;
   unpack2(sum[0], s0, s1);
   unpack2(sum[1], s2, s3);
-  l += (s0 + s1) + (s2 + s3);
   tmem_wait_st();
+  return (s0 + s1) + (s2 + s3);
 }
 
 // x += f * (16 folded output elements), from an acc whose float4s are 128 apart.
@@ -245,10 +211,10 @@ __device__ __forceinline__ void add_fold(uint32_t (&x)[16], const float4 *acc, f
   }
 }
 
-// Adds to an output row the non-finite values of the noted drafts that new row i
-// sees: their weight is positive, so the sum is what they are.
+// Adds to half an output row (from dim d0 on) the non-finite values of the noted drafts
+// that new row i sees: their weight is positive, so the sum is what they are.
 template <int D>
-__device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, int i,
+__device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, int i, int d0,
                                        const uint32_t *notes, float *out) {
   const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
   for (int u = 0; u < hd.T; ++u) {
@@ -259,8 +225,8 @@ __device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, 
     if (pg < 0 || pg >= grp.pages) continue;
     const uint16_t *v = (const uint16_t *)(grp.v + pool_row(p.c, grp, pg, p.c.head_row[hd.h],
                                                             tok & (p.c.P - 1)) * (D * 2));
-    for (int d = 0; d < D; ++d) {
-      const float b = __uint_as_float((uint32_t)__ldg(v + d) << 16);
+    for (int d = 0; d < D / 2; ++d) {
+      const float b = __uint_as_float((uint32_t)__ldg(v + d0 + d) << 16);
       if (!isfinite(b)) out[d] += b;
     }
   }
@@ -284,11 +250,11 @@ struct TileWalk {
 };
 
 // One warp's part of one role's loads: all K (or V) tiles of the block.
-template <int D, int kRows, bool kIsV>
+template <int D, bool kIsV>
 __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &range,
                                         uint32_t ring, uint32_t full0, uint32_t empty0,
                                         volatile int *abort, int lane) {
-  using C = Cfg<D, kRows>;
+  using C = Cfg<D>;
   constexpr int kN = kIsV ? C::kV : C::kK;
   const TreeParams &p = mp.t;
   const uint64_t pol = policy_evict_first();
@@ -342,9 +308,10 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
   }
 }
 
-template <int D, int kRows>
-__global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_constant__ MmaParams mp) {
-  using C = Cfg<D, kRows>;
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    tree_mma_kernel(const __grid_constant__ MmaParams mp) {
+  using C = Cfg<D>;
   const TreeParams &p = mp.t;
   extern __shared__ __align__(1024) uint8_t smem[];  // tiles start on 1024 bytes
   Ctl &ctl = *(Ctl *)(smem + C::kCtl);
@@ -385,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
     ctl.abort = 0;
     fence_barrier_init();
   }
-  if (warp == 6) tmem_alloc(smem_u32(&ctl.tmem), 256);
-  if (warp >= 4 && warp < 6 && lane < p.c.G)
-    prefetch_tensormap(warp == 4 ? &mp.tmK[lane] : &mp.tmV[lane]);
-  if (warp == 7 && lane == 0) prefetch_tensormap(&mp.tmQ);
+  if (warp == 10) tmem_alloc(smem_u32(&ctl.tmem), 256);
+  if (warp >= 8 && warp < 10 && lane < p.c.G)
+    prefetch_tensormap(warp == 8 ? &mp.tmK[lane] : &mp.tmV[lane]);
+  if (warp == 11 && lane == 0) prefetch_tensormap(&mp.tmQ);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -401,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
     return ctl.item[i % kItems];
   };
 
-  if (warp == 4) {
-    produce<D, kRows, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
-  } else if (warp == 5) {
-    produce<D, kRows, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
-  } else if (warp == 6) {
+  if (warp == 8) {
+    produce<D, false>(mp, range, base + C::kKs, k_full, k_empty, abort, lane);
+  } else if (warp == 9) {
+    produce<D, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
+  } else if (warp == 10) {
     if (lane == 0) {
       constexpr uint32_t kS = mma_desc(128, kTile, false), kO = mma_desc(128, D, true);
       int n = 0;
@@ -426,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
               const uint32_t off = (e & 3) * 32;
-              mma_ss(tS, smem_desc(base + (e >> 2) * C::kQHalf + off, 16),
+              mma_ss(tS, smem_desc(base + (e >> 2) * C::kHalf + off, 16),
                      smem_desc(k + (e >> 2) * C::kHalf + off, 16), kS, e > 0);
             }
           }
@@ -451,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
       }
     }
     __syncwarp();
-  } else if (warp == 7) {
+  } else if (warp == 11) {
     // items and queries for the other roles, and the V tiles that have to be cleaned
     TreeCursor<kTile> cur(p, range);
     TreeItem it;
@@ -477,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
         __syncwarp();
         const int bx = lane / C::kHalves, half = lane % C::kHalves;
         if (bx < boxes)
-          tma_load_5d(base + half * C::kQHalf + bx * bytes, &mp.tmQ, 0, half, it.head.h * p.c.g,
+          tma_load_5d(base + half * C::kHalf + bx * bytes, &mp.tmQ, 0, half, it.head.h * p.c.g,
                       it.head.q0 + tree_first(p, it) + bx * kTreeBox, 0, q_full,
                       policy_evict_first());
       }
@@ -550,10 +517,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
     }
   } else {
     // ------------------------------------------------------------- softmax
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t s_at = tS + lanes, o_at = tO + lanes;
-    // this lane's folded float4s, 128 apart
-    float4 *acc = (float4 *)p.fold + (size_t)blockIdx.x * (D / 4) * 128 + tid;
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // keys' half; TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tS + lanes + half * 64, o_at = tO + lanes + half * (D / 2);
+    // this thread's half of the folded row: float4s, 128 apart
+    float4 *acc = (float4 *)p.fold + ((size_t)blockIdx.x * 2 + half) * (D / 8) * 128 + row;
     int n = 0;
     // One thread says whether item i is worked on, so that all agree even while
     // a wait runs out; a barrier follows.
@@ -567,20 +535,21 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
     for (int i = 0; ctl.more[i & 1]; ++i) {
       const TreeItem &it = ctl.item[i % kItems];  // in shared memory: not worth registers
       const int rows = tree_rows(p, it), tiles = it.t1 - it.t0;
-      const bool live = warp * 32 < rows;
+      const bool live = (warp & 3) * 32 < rows;
       float m = -INFINITY, l = 0.f;  // reference of the weights (log2 units), sum
       float m_acc = -INFINITY;       // reference of the folded output
       for (int j = 0; j < tiles; ++j) {
-        const int t0 = (it.t0 + j) * kTile;
+        const int u0 = (it.t0 + j) * kTile - it.head.n;  // the tile's first key as a draft
         wait(s_full, n++ & 1, abort, p.status);
         tc_fence_after();
+        const bool turn = j > 0 && j % kFold == 0;  // O starts afresh
+        float top = -INFINITY;
         if (live) {
-          const bool turn = j > 0 && j % kFold == 0;  // O starts afresh
           if (turn) {
             // fold the tensor cores' sum of the last kFold tiles into fp32 (see kFold)
             const float f = tree_weight(m_acc, m);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t x[16];
               tmem_get16(o_at + 16 * c, x);
               if (j > kFold) add_fold(x, acc + 4 * c * 128, f);
@@ -591,32 +560,52 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
             }
             m_acc = m;
           }
-          if (t0 + kTile > it.head.n)
-            hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, tid), tid < rows,
-                      t0 - it.head.n, s_at);
-          soft_tile<D>(s_at, o_at, p.scale_log2, j > 0 && !turn, m, l);
+          if (u0 + kTile > 0)
+            hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, row), row < rows,
+                      u0 + half * 64, s_at);
+          top = top_score(s_at) * p.scale_log2;
         }
+        // The reference is the maximum of a row's first tile and rises only when a score
+        // passes it by more than kGrow: weights and sums are then at most 2^kGrow times
+        // larger than with the running maximum, which fp32 and bf16 hold as exactly.
+        if (named_or(1, kSoft, top > m + kGrow)) {
+          ctl.swap[half][row] = top;
+          named_sync(1, kSoft);
+          top = fmaxf(top, ctl.swap[half ^ 1][row]);
+          const float mn = top > m + kGrow ? top : m;
+          const float f = mn == m ? 1.f : tree_weight(m, mn);
+          l *= f;
+          if (live && j > 0 && !turn && __any_sync(0xffffffffu, f != 1.f))
+            rescale(o_at, D / 2, f);
+          m = mn;
+        }
+        if (live) l += weigh(s_at, p.scale_log2, m == -INFINITY ? 0.f : m);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready);
       }
       // ---- epilogue
-      wait(o_full, i & 1, abort, p.status);
+      decide(i + 1);
+      wait(o_full, i & 1, abort, p.status);  // (all have left the last tile)
       tc_fence_after();
+      ctl.swap[half][row] = l;
+      named_sync(1, kSoft);
       if (live) {
-        const bool whole = tree_whole(it), ok = tid < rows, folded = tiles > kFold;
-        float *dst = tree_out(p, it.head.q0 + tree_first(p, it), it.head.h, tid);
+        l += ctl.swap[half ^ 1][row];
+        const bool whole = tree_whole(it), ok = row < rows, folded = tiles > kFold;
+        float *dst = tree_out(p, it.head.q0 + tree_first(p, it), it.head.h, row);
         float f = 1.f;
         if (whole) {
           f = l == 0.f ? 0.f : 1.f / l;
         } else {
-          const size_t at = (size_t)tree_slot(range, it) * p.group_rows + tid;
+          const size_t at = (size_t)tree_slot(range, it) * p.group_rows + row;
           dst = p.part_o + at * D;
-          if (ok) p.part_ml[at] = make_float2(m, l);
+          if (ok && half == 0) p.part_ml[at] = make_float2(m, l);
         }
+        dst += half * (D / 2);
         const float fa = tree_weight(m_acc, m);
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t x[16];
           tmem_get16(o_at + 16 * c, x);
           if (folded) add_fold(x, acc + 4 * c * 128, fa);
@@ -631,13 +620,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
         if (it.t1 * kTile > it.head.n) {
           const uint4 o = *(const uint4 *)ctl.notes[i % kItems];
           if ((o.x | o.y | o.z | o.w) && ok)
-            add_notes<D>(p, it.head, tree_first(p, it) + tree_div_g(p, tid),
+            add_notes<D>(p, it.head, tree_first(p, it) + tree_div_g(p, row), half * (D / 2),
                          ctl.notes[i % kItems], dst);
         }
       }
       tc_fence_before();
-      decide(i + 1);
-      named_sync(1, kSoft);
+      __syncwarp();
       if (lane == 0) mbar_arrive(i_done);
     }
   }
@@ -654,17 +642,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  if (warp == 6) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_free(tS, 256);
   }
 }
 
-template <int D, int kRows>
-cudaError_t launch_dr(const MmaParams &mp, int blocks, cudaStream_t st) {
-  using C = Cfg<D, kRows>;
+template <int D>
+cudaError_t launch_d(const MmaParams &mp, int blocks, cudaStream_t st) {
+  using C = Cfg<D>;
   constexpr int bytes = C::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, kRows>,
+  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -677,14 +665,14 @@ cudaError_t launch_dr(const MmaParams &mp, int blocks, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, kRows>, mp);
+  e = cudaLaunchKernelEx(&cfg, tree_mma_kernel<D>, mp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-int tree_mma_tokens(int rows, int g) { return rows / (kTreeBox * g) * kTreeBox; }
-int tree_mma_rows(int max_q, int g) { return max_q > tree_mma_tokens(64, g) ? 128 : 64; }
+int tree_mma_rows() { return 128; }
+int tree_mma_tokens(int g) { return 128 / (kTreeBox * g) * kTreeBox; }
 int tree_mma_blocks_per_sm() { return 2; }
 
 cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
@@ -695,10 +683,7 @@ cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
   memcpy(mp.tmV, v_maps, sizeof(mp.tmV));
   mp.tmQ = q_map;
   mp.t = p;
-  const bool few = p.group_rows == 64;
-  if (p.c.D == 128)
-    return few ? launch_dr<128, 64>(mp, blocks, st) : launch_dr<128, 128>(mp, blocks, st);
-  return few ? launch_dr<64, 64>(mp, blocks, st) : launch_dr<64, 128>(mp, blocks, st);
+  return p.c.D == 128 ? launch_d<128>(mp, blocks, st) : launch_d<64>(mp, blocks, st);
 }
 
 }  // namespace kvx
