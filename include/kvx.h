@@ -686,7 +686,8 @@ typedef struct kvx_cache kvx_cache;
  *               [num_groups], as for kvx_decode_attn; pools and tables are
  *               written by kvx_append_kv, kvx_tree_commit and kvx_build_tables.
  * Errors: KVX_EINVAL, KVX_EUNSUPPORTED, KVX_ERANGE (pool_pages >= 2^31 - 1;
- * page_table_stride * page_size past int32), KVX_ENOMEM. */
+ * page_table_stride * page_size past int32; bf16: pool_pages times the larger of
+ * |G| and page_size / 8 past int32), KVX_ENOMEM. */
 int kvx_cache_create(const kvx_shape *shape, const int32_t *head_group,
                      void *const *k_pools, void *const *v_pools, const int64_t *pool_pages,
                      int32_t *const *page_tables, const int32_t *page_table_stride,

@@ -54,16 +54,23 @@ bool encode(CUtensorMap *tm, const void *base, const cuuint64_t *dims, const cuu
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A 5-D bf16 tensor map over one head group's pool, dims (innermost first)
-// {64 elements, P slots, D/64 halves, |G| heads, pages}; one box {64, P, 1, 1,
-// 1} is a page's rows of one head and half, 128-byte swizzled, zeros outside.
+// A 5-D bf16 tensor map over one head group's pool, whose box is one head's rows of a
+// page and lands as [8-row group][64-dim half][8 rows][128 bytes], 128-byte swizzled,
+// zeros outside: the same distance between all 8-row groups of a tile, which one
+// operand descriptor can express. Dims (innermost first):
+//   head-major pages:  {64 elements, 8 rows, D/64 halves, P/8 groups, pages * |G|}
+//   token-major pages: {64 elements, 8 rows, D/64 halves, pages * P/8 groups, |G|}
 bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g) {
   const cuuint64_t row = (cuuint64_t)c->dev.row_bytes, P = (cuuint64_t)c->dev.P;
-  const cuuint64_t n = (cuuint64_t)g.size;
-  const cuuint64_t dims[5] = {64, P, row / 128, n, (cuuint64_t)g.pages};
-  const cuuint64_t strides[4] = {c->dev.token_major ? row * n : row, 128,
-                                 c->dev.token_major ? row : row * P, row * P * n};
-  const cuuint32_t box[5] = {64, (cuuint32_t)P, 1, 1, 1};
+  const cuuint64_t n = (cuuint64_t)g.size, pages = (cuuint64_t)g.pages, halves = row / 128;
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)P / 8, 1};
+  if (c->dev.token_major) {
+    const cuuint64_t dims[5] = {64, 8, halves, pages * P / 8, n};
+    const cuuint64_t strides[4] = {row * n, 128, 8 * row * n, row};
+    return encode(tm, pool, dims, strides, box);
+  }
+  const cuuint64_t dims[5] = {64, 8, halves, P / 8, pages * n};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, P * row};
   return encode(tm, pool, dims, strides, box);
 }
 
@@ -142,6 +149,10 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
     if (pool_pages[gi] < 1 || page_table_stride[gi] < 1) return KVX_EINVAL;
     if (pool_pages[gi] >= ((int64_t)1 << 31) - 1 ||
         (int64_t)page_table_stride[gi] * s->page_size > INT32_MAX)
+      return KVX_ERANGE;
+    // (coordinates of the tensor maps)
+    if (s->dtype == KVX_BF16 &&
+        (pool_pages[gi] + 1) * std::max(size[gi], s->page_size / 8) > INT32_MAX)
       return KVX_ERANGE;
   }
   kvx_cache *c = new (std::nothrow) kvx_cache();

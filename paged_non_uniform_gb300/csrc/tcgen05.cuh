@@ -118,14 +118,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // ---- matrix instructions -----------------------------------------------------
 // Shared-memory operand, 128-byte swizzle, rows of 64 16-bit elements (128
-// bytes) in groups of 8 (1024 bytes, base 1024-byte aligned).
-//   K-major (a row holds 64 consecutive k): groups along m/n are 1024 bytes
-//   apart; `lead` is not used.
-//   MN-major (a row holds 64 consecutive m/n, rows are k): groups along k are
-//   1024 bytes apart, blocks of 64 along m/n `lead` bytes.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+// bytes) in groups of 8 (1024 bytes, 1024-byte aligned), the groups `stride` bytes
+// apart.
+//   K-major (a row holds 64 consecutive k): the groups run along m/n; `lead` is
+//   not used.
+//   MN-major (a row holds 64 consecutive m/n, rows are k): the groups run along k,
+//   blocks of 64 along m/n are `lead` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
   return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-         ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+         ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, B K-major or MN-major.

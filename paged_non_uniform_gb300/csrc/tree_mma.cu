@@ -10,8 +10,8 @@
 // other's loads and products; each walks its items (tree_split.cuh) in tiles of
 // 128 keys:
 //  * warps 8 and 9 load K and V tiles from their pages into two rings (bulk
-//    tensor loads, one box of min(P, 128) rows x 64 dims per lane, landing as
-//    [half][128 rows][128 bytes], 128-byte swizzled);
+//    tensor loads, one box a page of at most 128 rows, landing as [8-row group][half
+//    of the dims][8 rows][128 bytes], 128-byte swizzled);
 //  * warp 10 issues the MMAs: S, then O += P V of the tile;
 //  * warps 0-3 and 4-7 do the softmax: a query row belongs to two threads, one for each
 //    half of a tile's keys (a thread can only reach one lane of TMEM). They agree on
@@ -70,8 +70,9 @@ static_assert(offsetof(Ctl, notes) % 16 == 0, "read as vectors");
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalf = 128 * 128;              // bytes of 64 dims of 128 rows
-  static constexpr int kTileBytes = kHalves * kHalf;   // a Q, K or V tile
+  static constexpr int kTileBytes = D * 2 * 128;       // a Q, K or V tile
+  static constexpr int kQHalf = 128 * 128;             // Q: 64 dims of all rows together
+  static constexpr int kGroup = 1024 * kHalves;        // K, V: all dims of 8 rows together
   static constexpr int kSlots = (111 * 1024 - kTileBytes) / kTileBytes;  // K and V tiles
   static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
   static_assert(kK >= 1 && kV + 1 < kItems, "ring depths");
@@ -259,9 +260,7 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
   const TreeParams &p = mp.t;
   const uint64_t pol = policy_evict_first();
   const int P = p.c.P, box = min(P, kTile);
-  const int per = kTile / box;  // boxes of a tile and half
-  // lane -> (box, half); a tile has at most 16 * 2 of them
-  const int bx = lane % per, half = lane / per;
+  const int per = kTile / box;  // boxes of a tile: lane i loads box i
   // Two walks over the tiles: `ahead` runs kAhead tiles before `now` and reads
   // the page ids, so that neither the lengths nor the page table hold up a load.
   constexpr int kAhead = 3;
@@ -270,8 +269,8 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
     if (!ahead.more) return 0;
     const TreeHead &h = ahead.it.head;
     const CacheGroup &grp = p.c.grp[p.c.head_grp[h.h]];
-    const int tok = ahead.tile * kTile + bx * box;
-    const int page = half < C::kHalves && tok < h.n + h.T
+    const int tok = ahead.tile * kTile + lane * box;
+    const int page = lane < per && tok < h.n + h.T
                          ? __ldg(grp.table + (size_t)h.b * grp.stride + (tok >> p.c.lgP))
                          : 0;
     ahead.step(p);
@@ -294,15 +293,17 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
     const uint32_t full = full0 + 8 * slot;
     if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * box * 128 * C::kHalves));
     __syncwarp();
-    if (half < C::kHalves && bx < boxes) {
-      const int64_t have = p.c.grp[gi].pages;
-      if (page < 0 || (int64_t)page >= have) {
+    if (lane < boxes) {
+      if (page < 0 || (int64_t)page >= p.c.grp[gi].pages) {
         atomicOr(p.status, KVX_DEV_BAD_PAGE);
-        page = (int)have;  // past the last page: loads zeros
+        page = (int)p.c.grp[gi].pages;  // past the last page: loads zeros
       }
-      const int tok = now.tile * kTile + bx * box;
-      tma_load_5d(ring + slot * C::kTileBytes + half * C::kHalf + bx * box * 128,
-                  kIsV ? &mp.tmV[gi] : &mp.tmK[gi], 0, tok & (P - 1), half, rank, page, full, pol);
+      // the box's first 8-row group in the map's last two dims
+      const int off = ((now.tile * kTile + lane * box) & (P - 1)) >> 3;
+      const int c3 = p.c.token_major ? page * (P >> 3) + off : off;
+      const int c4 = p.c.token_major ? rank : page * p.c.grp[gi].size + rank;
+      tma_load_5d(ring + slot * C::kTileBytes + lane * box * (D * 2),
+                  kIsV ? &mp.tmV[gi] : &mp.tmK[gi], 0, 0, 0, c3, c4, full, pol);
     }
     now.step(p);
   }
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
               const uint32_t off = (e & 3) * 32;
-              mma_ss(tS, smem_desc(base + (e >> 2) * C::kHalf + off, 16),
-                     smem_desc(k + (e >> 2) * C::kHalf + off, 16), kS, e > 0);
+              mma_ss(tS, smem_desc(base + (e >> 2) * C::kQHalf + off, 0, 1024),
+                     smem_desc(k + (e >> 2) * 1024 + off, 0, C::kGroup), kS, e > 0);
             }
           }
           mma_commit(s_full);
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t v = base + C::kVs + vs * C::kTileBytes;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
-              const uint64_t b = smem_desc(v + k * 16 * 128, C::kHalf);
+              const uint64_t b = smem_desc(v + k * 2 * C::kGroup, 1024, C::kGroup);
               mma_ts(tO, tS + 16 * k, b, kO, !(first && k == 0));
               mma_ts(tO, tS + 16 * k + 8, b, kO, true);
             }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         const int bx = lane / C::kHalves, half = lane % C::kHalves;
         if (bx < boxes)
-          tma_load_5d(base + half * C::kHalf + bx * bytes, &mp.tmQ, 0, half, it.head.h * p.c.g,
+          tma_load_5d(base + half * C::kQHalf + bx * bytes, &mp.tmQ, 0, half, it.head.h * p.c.g,
                       it.head.q0 + tree_first(p, it) + bx * kTreeBox, 0, q_full,
                       policy_evict_first());
       }
@@ -458,16 +459,17 @@ __global__ void __launch_bounds__(kThreads, 2)
           // chunk (16 bytes) x of a row: half x >> 3, place x & 7
           constexpr int CPR = D / 8, RPW = 32 / CPR;  // rows a warp covers at once
           const int x = lane % CPR;
-          uint8_t *v = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * C::kHalf + (x & 7) * 16;
+          uint8_t *v0 = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * 1024 + (x & 7) * 16;
+          auto v = [&](int row) { return v0 + (row >> 3) * C::kGroup + (row & 7) * 128; };
 #pragma unroll 4
           for (int row = valid + lane / CPR; row < kTile; row += RPW)
-            *(uint4 *)(v + row * 128) = make_uint4(0, 0, 0, 0);
+            *(uint4 *)v(row) = make_uint4(0, 0, 0, 0);
           for (int r0 = first; r0 < valid; r0 += 4 * RPW) {
             uint4 y[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int row = r0 + k * RPW + lane / CPR;
-              y[k] = row < valid ? *(const uint4 *)(v + row * 128) : make_uint4(0, 0, 0, 0);
+              y[k] = row < valid ? *(const uint4 *)v(row) : make_uint4(0, 0, 0, 0);
             }
             bool odd = false;
 #pragma unroll
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int row = r0 + k * RPW + lane / CPR;
               bool hit = false;
               if (row < valid) {
-                uint32_t *at = (uint32_t *)(v + row * 128);
+                uint32_t *at = (uint32_t *)v(row);
                 for (int i = 0; i < 4; ++i) {
                   const uint32_t e = at[i];
                   const uint32_t bad = ((e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
