@@ -67,10 +67,10 @@ struct CommitParams {
   int32_t max_rows, path_stride;
 };
 
-// A row group whose tiles span blocks: `parts` partials, the first in slot
-// `first`, the others in slots 2c of the blocks that follow (0: none).
+// A row group that starts in block c and runs on: `parts` partials, the first in slot
+// 2c + 1, the others in slots 2c of the blocks that follow (0: none).
 struct TreeSplit {
-  int32_t parts, first, row0, h, rows;
+  int32_t parts, row0, h, rows;
 };
 
 // Tree attention. A head's keys come in tiles, its query rows (new row i and

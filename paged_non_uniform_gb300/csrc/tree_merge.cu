@@ -27,10 +27,10 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_const
   const int lane = threadIdx.x & 31;
   const int r_end = min(s.rows, ((int)blockIdx.x + 1) * kRowsPerBlock);
   for (int r = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5); r < r_end; r += kThreads / 32) {
-    // row r of partial c: the first in its slot, the others at the start of their
-    // blocks' ranges
+    // row r of partial c: the first is its block's last piece, the others are their
+    // blocks' first
     auto at = [&](int c) {
-      return (size_t)(c == 0 ? s.first : 2 * ((int)blockIdx.y + c)) * p.group_rows + r;
+      return (size_t)(2 * ((int)blockIdx.y + c) + (c == 0 ? 1 : 0)) * p.group_rows + r;
     };
     float M = -INFINITY;
     for (int c = lane; c < s.parts; c += 32) M = fmaxf(M, __ldcg(p.part_ml + at(c)).x);

@@ -44,7 +44,7 @@ namespace {
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kSoft = 256;       // threads of the softmax warps
-constexpr int kMinUnits = 1;     // tiles a block takes at least
+constexpr int kMinTiles = 1;     // tiles a block takes at least
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 16.f;    // log2 growth of the maximum that raises the reference
 // Tiles after which the output leaves tensor memory for an fp32 sum: the
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tS = ctl.tmem, tO = tS + kTile;  // TMEM columns of S and O
   pdl_wait();
-  const TreeRange range = tree_range<kThreads, kTile>(p, kMinUnits, ctl.warp_sum, &ctl.range);
+  const TreeRange range = tree_range<kThreads, kTile>(p, kMinTiles, ctl.warp_sum, &ctl.range);
   // Item i of the block (the last is followed by one without tiles).
   auto item_at = [&](int i) -> const TreeItem & {
     wait(i_full + 8 * (i % kItems), (i / kItems) & 1, abort, p.status);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (whole) {
           f = l == 0.f ? 0.f : 1.f / l;
         } else {
-          const size_t at = (size_t)tree_slot(range, it) * p.group_rows + row;
+          const size_t at = (size_t)tree_slot(it) * p.group_rows + row;
           dst = p.part_o + at * D;
           if (ok && half == 0) p.part_ml[at] = make_float2(m, l);
         }

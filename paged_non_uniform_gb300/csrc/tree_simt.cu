@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTile = 64;
 constexpr int kRows = 32;
-constexpr int kMinUnits = 2;
+constexpr int kMinTiles = 2;
 
 template <int D>
 struct Smem {
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_launch_dependents();
   pdl_wait();
-  const TreeRange range = tree_range<kThreads, kTile>(p, kMinUnits, sm.warp_sum, &sm.range);
+  const TreeRange range = tree_range<kThreads, kTile>(p, kMinTiles, sm.warp_sum, &sm.range);
   TreeCursor<kTile> cur(p, range);
   TreeItem it;
   bool any = false;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
       }
     }
     const bool whole = tree_whole(it);
-    const int slot = whole ? 0 : tree_slot(range, it);
+    const int slot = whole ? 0 : tree_slot(it);
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = ty * 4 + a;

@@ -2,19 +2,19 @@
 // device lengths, and how the pieces of a head are merged.
 //
 // A head (b, h) with T_b new rows has T_b * g query rows, in groups of
-// group_tokens new rows, and n[b][h] + T_b keys, in tiles of kTile. A unit is one
-// tile for one row group. All units are laid end to end -- heads in order, row
-// groups within a head, tiles within a row group -- and block c of `blocks` takes
-// units [c * U / blocks, (c + 1) * U / blocks): the flat equal cut of the
+// group_tokens new rows, and n[b][h] + T_b keys, in tiles of kTile. A row group costs
+// kItemCost for being worked on at all (queries, pipeline fill, epilogue) and kTileCost
+// a tile. All costs are laid end to end -- heads in order, row groups within a head,
+// tiles within a row group -- and block c of `blocks` takes the tiles that start in
+// [c * U / blocks, (c + 1) * U / blocks): the flat cut with a charge per item of the
 // ahead-of-time plan ("Tangram: Unlocking Non-Uniform KV Cache for Efficient
 // Multi-turn LLM Serving", AOT Load Balancing, Fig. 13), but found by every
 // block itself from one pass over the lengths, so that nothing is planned on
 // the host. A row group whose tiles span blocks leaves one partial (max in
 // log2 units, sum, un-normalised output) per block; a second, small kernel folds
 // them in block order. A block leaves at most two partials: of the row group
-// that its range begins in (slot 2c) and of one that begins inside its range and
-// runs past its end (slot 2c + 1). At most one row group starts in a block and
-// runs past its end: the block describes it for the second kernel.
+// that runs into it (slot 2c) and of one that begins in it and runs on (slot 2c +
+// 1), which it also describes for the second kernel.
 #pragma once
 
 #include <math.h>
@@ -24,11 +24,20 @@
 
 namespace kvx {
 
+// Measured on 256 sequences of 100 to 1000 tokens: an item costs a block of the
+// tensor-core kernel 3.3 us and a tile 2.4 us; with the charge the slowest block ended
+// after TODO us instead of 136.
+constexpr int kTileCost = 5;
+constexpr int kItemCost = 7;
+
 struct TreeHead {
   int b, h;      // sequence, KV head
   int q0, T;     // first new row, new rows (0: nothing to do)
   int n;         // cached tokens
   int tiles, groups;
+  // cost of a row group, and of the head
+  __device__ __forceinline__ int seg() const { return tiles ? kItemCost + kTileCost * tiles : 0; }
+  __device__ __forceinline__ int64_t cost() const { return (int64_t)seg() * groups; }
 };
 
 // The lengths of a head as they are in memory: loaded ahead of their use.
@@ -70,27 +79,29 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const
 }
 
 struct TreeRange {
-  int units;       // of all heads
+  int units;       // cost of all heads
   int blocks;      // blocks with work
-  int begin, end;  // this block's units
+  int begin, end;  // this block's part of it
   int head;        // the head that holds `begin`
-  int base;        // first unit of that head
+  int base;        // where that head starts
+  TreeHead first;  // that head
 };
 
-// First unit of block c: floor(c * units / blocks) without 64 bits.
+// Where block c begins: floor(c * units / blocks) without 64 bits.
 __device__ __forceinline__ int tree_bound(int units, int blocks, int c) {
   const int q = units / blocks, r = units - q * blocks;
   return c * q + c * r / blocks;  // blocks is at most a few hundred
 }
-// The block that holds unit u.
+// The block that holds position u.
 __device__ __forceinline__ int tree_block_of(int units, int blocks, int u) {
   return (int)((((int64_t)u + 1) * blocks - 1) / units);
 }
 
-// Sums the units of all heads over the block's NT threads and finds this block's range.
-// `min_units`: a block gets at least that many where there are few in all.
+// Sums the costs of all heads over the block's NT threads and finds this block's range.
+// `min_tiles`: a block gets at least the cost of that many (one at least, so that every
+// block between a row group's first and last has a tile of it).
 template <int NT, int kTile>
-__device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_units,
+__device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_tiles,
                                                 int64_t *warp_sum /* shared, NT / 32 */,
                                                 TreeRange *shared) {
   const int heads = p.c.B * p.c.Hkv;
@@ -100,7 +111,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
   int64_t s = 0;
   for (int i = lo; i < hi; ++i) {
     const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), blockIdx.x == 0);
-    s += (int64_t)t.tiles * t.groups;
+    s += t.cost();
   }
   int64_t x = s;
 #pragma unroll
@@ -122,21 +133,21 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
     if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     all = 0;
   }
-  const int units = (int)all, want = units / min_units;
+  const int units = (int)all, want = units / (min_tiles * kTileCost);
   const int blocks = want < 1 ? 1 : min(want, (int)gridDim.x);
   const bool work = (int)blockIdx.x < blocks && units > 0;
   const int begin = work ? tree_bound(units, blocks, blockIdx.x) : 0;
   const int end = work ? tree_bound(units, blocks, blockIdx.x + 1) : 0;
   const int64_t mine = before + x - s;
   if (!work) {
-    if (tid == 0) *shared = {units, blocks, 0, 0, 0, 0};
+    if (tid == 0) *shared = {units, blocks, 0, 0, 0, 0, {}};
   } else if (begin >= mine && begin < mine + s) {
     int base = (int)mine;
     for (int i = lo; i < hi; ++i) {
       const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), false);
-      const int u = t.tiles * t.groups;
+      const int u = (int)t.cost();
       if (begin < base + u) {
-        *shared = {units, blocks, begin, end, i, base};
+        *shared = {units, blocks, begin, end, i, base, t};
         break;
       }
       base += u;
@@ -150,7 +161,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_uni
 struct TreeItem {
   TreeHead head;
   int hd, group, t0, t1;
-  int seg;  // first unit of the row group
+  int seg;  // where the row group starts
 };
 
 // Walks a block's items. The lengths of the two heads after the current one are
@@ -161,40 +172,46 @@ struct TreeCursor {
   TreeHead head;
   TreeRaw raw1, raw2;
   __device__ __forceinline__ TreeCursor(const TreeParams &p, const TreeRange &r)
-      : at(r.begin), end(r.end), base(r.base), hd(r.head) {
+      : at(r.begin), end(r.end), base(r.base), hd(r.head), head(r.first) {
     if (at < end) {
-      const TreeRaw raw = tree_raw(p, hd);
       raw1 = tree_raw(p, hd + 1);
       raw2 = tree_raw(p, hd + 2);
-      head = tree_head<kTile>(p, hd, raw, false);
     }
   }
   __device__ __forceinline__ bool next(const TreeParams &p, TreeItem &it) {
-    if (at >= end) return false;
-    while (at - base >= head.tiles * head.groups) {
-      base += head.tiles * head.groups;
-      ++hd;
-      head = tree_head<kTile>(p, hd, raw1, false);
-      raw1 = raw2;
-      raw2 = tree_raw(p, hd + 2);
+    while (at < end) {
+      const int seg = head.seg();
+      if (at - base >= seg * head.groups) {
+        base += seg * head.groups;
+        ++hd;
+        head = tree_head<kTile>(p, hd, raw1, false);
+        raw1 = raw2;
+        raw2 = tree_raw(p, hd + 2);
+        continue;
+      }
+      const int group = head.groups == 1 ? 0 : (at - base) / seg;
+      const int start = base + group * seg, first = start + kItemCost;  // of its tile 0
+      const int t0 = max(0, at - first + kTileCost - 1) / kTileCost;
+      const int t1 = min(head.tiles, (max(0, end - first) + kTileCost - 1) / kTileCost);
+      at = start + seg;  // (past `end` where the row group runs on)
+      if (t0 >= t1) continue;
+      it.head = head;
+      it.hd = hd;
+      it.group = group;
+      it.t0 = t0;
+      it.t1 = t1;
+      it.seg = start;
+      return true;
     }
-    const int v = at - base;
-    it.head = head;
-    it.hd = hd;
-    it.group = head.groups == 1 ? 0 : v / head.tiles;
-    it.t0 = v - it.group * head.tiles;
-    it.seg = at - it.t0;
-    it.t1 = it.t0 + min(end - at, head.tiles - it.t0);
-    at += it.t1 - it.t0;
-    return true;
+    return false;
   }
 };
 
 __device__ __forceinline__ bool tree_whole(const TreeItem &it) {
   return it.t0 == 0 && it.t1 == it.head.tiles;
 }
-__device__ __forceinline__ int tree_slot(const TreeRange &r, const TreeItem &it) {
-  return 2 * (int)blockIdx.x + (it.seg > r.begin ? 1 : 0);
+__device__ __forceinline__ int tree_slot(const TreeItem &it) {
+  return 2 * (int)blockIdx.x + (it.t0 == 0 ? 1 : 0);
 }
 
 // Scale of a partial with maximum m when the merged maximum is M (a partial
@@ -225,11 +242,12 @@ __device__ __forceinline__ float *tree_out(const TreeParams &p, int row0, int h,
 // thread; `it` is the block's last item, or null if it has none).
 __device__ __forceinline__ void tree_describe(const TreeParams &p, const TreeRange &r,
                                               const TreeItem *it) {
-  TreeSplit s = {0, 0, 0, 0, 0};
+  TreeSplit s = {0, 0, 0, 0};
   if (it && it->t0 == 0 && !tree_whole(*it)) {
-    const int last = tree_block_of(r.units, r.blocks, it->seg + it->head.tiles - 1);
-    s = {last - (int)blockIdx.x + 1, tree_slot(r, *it), it->head.q0 + tree_first(p, *it),
-         it->head.h, tree_rows(p, *it)};
+    const int last = tree_block_of(
+        r.units, r.blocks, it->seg + kItemCost + kTileCost * (it->head.tiles - 1));
+    s = {last - (int)blockIdx.x + 1, it->head.q0 + tree_first(p, *it), it->head.h,
+         tree_rows(p, *it)};
   }
   p.split[blockIdx.x] = s;
 }
