@@ -113,6 +113,19 @@ int tree_shape(const kvx_cache *c, TreeShape *t) {
 }  // namespace
 }  // namespace kvx
 
+namespace kvx {
+
+cudaError_t raise_smem_limit(int8_t (&done)[64], const void *kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev] = 1;
+  return e;
+}
+
+}  // namespace kvx
+
 using namespace kvx;
 
 extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,

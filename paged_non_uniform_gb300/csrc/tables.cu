@@ -23,36 +23,46 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Exclusive sums of a[0..n), in place; a[n] becomes the total. n ints in
-// shared memory, all threads take part. Sums that pass int32 are caught by the
-// caller's 64-bit totals.
-__device__ void exclusive_scan(int *a, int n, int *warp_sum) {
+// Exclusive sums of three arrays a[0..n), stride n + 1 apart, in place; a[n] becomes
+// the total. Shared memory, all threads take part. Sums that pass int32 are caught by
+// the caller's 64-bit totals.
+__device__ void exclusive_scans(int *a, int n, int (*warp_sum)[kWarps]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + kThreads - 1) / kThreads;
   const int lo = min(n, tid * per), hi = min(n, lo + per);
-  int s = 0;
-  for (int i = lo; i < hi; ++i) s += a[i];
-  int x = s;
+  int s[3], x[3];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
+  for (int k = 0; k < 3; ++k) {
+    s[k] = 0;
+    for (int i = lo; i < hi; ++i) s[k] += a[k * (n + 1) + i];
+    x[k] = s[k];
   }
-  if (lane == 31) warp_sum[warp] = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], d);
+      if (lane >= d) x[k] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) warp_sum[k][warp] = x[k];
   __syncthreads();
-  int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sum[w];
-    all += warp_sum[w];
+  for (int k = 0; k < 3; ++k) {
+    int run = x[k] - s[k], all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) run += warp_sum[k][w];
+      all += warp_sum[k][w];
+    }
+    for (int i = lo; i < hi; ++i) {
+      const int v = a[k * (n + 1) + i];
+      a[k * (n + 1) + i] = run;
+      run += v;
+    }
+    if (tid == 0) a[k * (n + 1) + n] = all;
   }
-  int run = before + x - s;
-  for (int i = lo; i < hi; ++i) {
-    const int v = a[i];
-    a[i] = run;
-    run += v;
-  }
-  if (tid == 0) a[n] = all;
   __syncthreads();
 }
 
@@ -73,7 +83,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   extern __shared__ int sm[];
   __shared__ unsigned long long total[2][KVX_MAX_GROUPS];  // alloc, release
   __shared__ unsigned long long rows_total;
-  __shared__ int warp_sum[kWarps];
+  __shared__ int warp_sum[3][kWarps];
+  __shared__ int free_in[KVX_MAX_GROUPS];
   __shared__ int8_t heads[KVX_MAX_KV_HEADS];  // heads by group
   __shared__ int head_off[KVX_MAX_GROUPS + 1];
   pdl_launch_dependents();
@@ -94,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   }
   __syncthreads();
   pdl_wait();
+  if (tid < G) free_in[tid] = __ldg(p.free_in + tid);
 
   // ---- lengths of every (group, sequence); sums of this block's group
   int bad = 0;
@@ -125,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   if (!bad) {
     bad = rows_total > (unsigned long long)p.max_rows;
     for (int g = 0; g < G; ++g) {
-      const int64_t f = __ldg(p.free_in + g);
+      const int64_t f = free_in[g];
       const int64_t a = (int64_t)total[0][g], r = (int64_t)total[1][g];
       bad |= f < 0 || f + r > c.grp[g].pages;
       short_list |= a > f + r;
@@ -136,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     if (first) {
       for (int b = tid; b < B; b += kThreads)
         p.pages_out[(size_t)own * B + b] = __ldg(p.pages_in + (size_t)own * B + b);
-      if (tid == 0) p.free_out[own] = __ldg(p.free_in + own);
+      if (tid == 0) p.free_out[own] = free_in[own];
       if (own == 0) {
         for (int b = tid; b <= B; b += kThreads) p.q_start[b] = 0;
         if (tid == 0) atomicOr(p.status, bad ? KVX_DEV_BAD_LENGTH : KVX_DEV_NO_PAGES);
@@ -149,12 +161,10 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     for (int b = tid; b < B; b += kThreads)
       p.pages_out[(size_t)own * B + b] = __ldg(pages_in + b) + a_start[b] - r_start[b];
   __syncthreads();
-  exclusive_scan(a_start, B, warp_sum);
-  exclusive_scan(r_start, B, warp_sum);
-  exclusive_scan(q_start, B, warp_sum);
+  exclusive_scans(sm, B, warp_sum);
   const CacheGroup &grp = c.grp[own];
   int32_t *list = p.free_pages[own];
-  const int F = __ldg(p.free_in + own), A = a_start[B], R = r_start[B], N = q_start[B];
+  const int F = free_in[own], A = a_start[B], R = r_start[B], N = q_start[B];
   if (first) {
     if (tid == 0) p.free_out[own] = F + R - A;
     if (own == 0)
@@ -178,12 +188,16 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     const int j = __ldg(pages_in + b) + ((int)k - a_start[b]);
     grp.table[(size_t)b * grp.stride + j] = popped((int)k);
   }
-  // ---- slots of this group's heads
+  // ---- slots of this group's heads, rows [r0, r1) of this block: consecutive threads
+  // take consecutive heads, then rows, so that a thread mostly stays in one
+  // sequence and a page id is read once for its neighbours
   const int nh = grp.size;
-  const int64_t total_slots = (int64_t)N * nh;
+  const int r0 = (int)((int64_t)blockIdx.x * N / gridDim.x);
+  const int r1 = (int)((int64_t)(blockIdx.x + 1) * N / gridDim.x);
+  const unsigned total_slots = (unsigned)(r1 - r0) * nh;
   int b = 0, b_end = 0;  // q_start[b + 1] of the sequence of the last row
-  for (int64_t i = at0; i < total_slots; i += step) {
-    const int row = (int)(i / nh), rank = (int)(i - (int64_t)row * nh);
+  for (unsigned i = tid; i < total_slots; i += kThreads) {
+    const int row = r0 + (int)(i / (unsigned)nh), rank = (int)(i % (unsigned)nh);
     if (row >= b_end) {
       b = owner(q_start, B, row);
       b_end = q_start[b + 1];
@@ -206,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st) {
   const int64_t slots = (int64_t)p.max_rows * p.c.Hkv;
-  const int64_t want = (slots / p.c.G + 4 * kThreads - 1) / (4 * kThreads);
-  const int most = 608 / p.c.G > 1 ? 608 / p.c.G : 1;
+  const int64_t want = (slots / p.c.G + 8 * kThreads - 1) / (8 * kThreads);
+  const int most = 1216 / p.c.G;  // eight blocks per SM over all groups
   const unsigned blocks = (unsigned)(want < 1 ? 1 : want > most ? most : want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, (unsigned)p.c.G);

@@ -116,6 +116,9 @@ cudaError_t launch_tree_mma(const TreeParams &p, const CUtensorMap *k_maps,
 int tree_mma_tokens(int g);
 int tree_mma_rows();
 int tree_mma_blocks_per_sm();
+// Raises a kernel's shared-memory limit on the current device, once (`done`: one flag per
+// device, of that kernel).
+cudaError_t raise_smem_limit(int8_t (&done)[64], const void *kernel, int bytes);
 // Folds the partials of split row groups (after either kernel).
 cudaError_t launch_tree_merge(const TreeParams &p, int blocks, cudaStream_t st);
 

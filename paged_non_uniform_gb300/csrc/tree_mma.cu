@@ -654,8 +654,8 @@ template <int D>
 cudaError_t launch_d(const MmaParams &mp, int blocks, cudaStream_t st) {
   using C = Cfg<D>;
   constexpr int bytes = C::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static int8_t done[64];
+  cudaError_t e = raise_smem_limit(done, (const void *)tree_mma_kernel<D>, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

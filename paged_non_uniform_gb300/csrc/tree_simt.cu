@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
 template <int D>
 cudaError_t launch_d(const TreeParams &p, int blocks, cudaStream_t st) {
   const int bytes = (int)sizeof(Smem<D>);
-  cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static int8_t done[64];
+  cudaError_t e = raise_smem_limit(done, (const void *)tree_simt_kernel<D>, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

@@ -184,15 +184,28 @@ def _dptr(x) -> int | None:
     return int(x.data_ptr())
 
 
+def _find_stream() -> int | None:
+    """torch's current stream; the first call settles how it is asked for."""
+    global _current_stream
+    try:
+        import torch
+    except ImportError:
+        _current_stream = lambda: None  # noqa: E731
+        return None
+    if not torch.cuda.is_available():
+        return None
+    torch.cuda.current_device()  # initialises CUDA
+    raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
+_current_stream = _find_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return int(torch.cuda.current_stream().cuda_stream)
-        except ImportError:
-            pass
-        return None
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -504,13 +517,15 @@ class Frame:
 def _dense(x, what: str, itemsize: int, count: int = 0):
     """Address of a dense device array: integer addresses pass, tensors must be
     contiguous, of the given item size and hold at least `count` items."""
-    if isinstance(x, int):
-        return x
-    if x is None or not x.is_cuda or x.element_size() != itemsize or not x.is_contiguous() \
-            or x.numel() < count:
-        raise KvxError(f"{what}: not a dense device array of {count} {itemsize}-byte items",
-                       KVX_EINVAL)
-    return x.data_ptr()
+    try:
+        if x.is_cuda and x.is_contiguous() and x.element_size() == itemsize \
+                and x.numel() >= count:
+            return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+    raise KvxError(f"{what}: not a dense device array of {count} {itemsize}-byte items",
+                   KVX_EINVAL)
 
 
 def _rows(x, what: str, itemsize: int, width: int, max_rows: int):
@@ -519,17 +534,20 @@ def _rows(x, what: str, itemsize: int, width: int, max_rows: int):
     stride apart; for an integer address, the rows are dense."""
     if isinstance(x, int):
         return x, width
-    inner = 1
-    ok = x is not None and x.is_cuda and x.element_size() == itemsize and x.dim() >= 2 \
-        and x.shape[0] >= max_rows
-    if ok:
-        for n, st in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-            ok = ok and (st == inner or n == 1)
-            inner *= n
-    if not ok or inner != width:
-        raise KvxError(f"{what}: not {max_rows} device rows of {width} {itemsize}-byte items",
-                       KVX_EINVAL)
-    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else width)
+    if x is not None and x.is_cuda and x.element_size() == itemsize:
+        size, stride = x.shape, x.stride()
+        n = len(size)
+        if n == 2:
+            ok = size[1] == width and (stride[1] == 1 or width == 1)
+        elif n == 3:
+            ok = size[1] * size[2] == width and (stride[2] == 1 or size[2] == 1) \
+                and (stride[1] == size[2] or size[1] == 1)
+        else:
+            ok = False
+        if ok and size[0] >= max_rows:
+            return x.data_ptr(), (stride[0] if size[0] > 1 else width)
+    raise KvxError(f"{what}: not {max_rows} device rows of {width} {itemsize}-byte items",
+                   KVX_EINVAL)
 
 
 def _nbytes(workspace, nbytes):
