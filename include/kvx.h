@@ -656,7 +656,7 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              head (b, h), for every head.
  *   max_rows   host: rows the row arrays hold, >= q_start[B]. Rows from
  *              q_start[B] on are neither read nor written. With 0 the row
- *              arrays may be NULL.
+ *              arrays may be NULL; more than 2^30 is KVX_ERANGE.
  *   slots      device int64 [max_rows][Hkv]: where the row's K and V of KV head
  *              h are, as a row index into the pool of h's group:
  *                  head-major pages:  (page * |G| + r) * P + t % P

@@ -26,6 +26,9 @@ int64_t row_stride(const kvx_cache *c, int64_t stride, int heads) {
   return stride * es;
 }
 
+// Row arrays hold at most this many rows (row indices and their steps stay in int32).
+constexpr int32_t kMaxRows = 1 << 30;
+
 bool workspace_ok(const void *ws, size_t bytes, size_t need) {
   return ws && aligned(ws, 256) && bytes >= need;
 }
@@ -210,6 +213,7 @@ extern "C" int kvx_build_tables(const kvx_cache *c, const int32_t *kv_len, const
   if (!c || !kv_len || !new_len || !pages_in || !pages_out || !free_pages || !free_in ||
       !free_out || !q_start || max_rows < 0 || (max_rows > 0 && !slots))
     return KVX_EINVAL;
+  if (max_rows > kMaxRows) return KVX_ERANGE;
   if (pages_in == pages_out || free_in == free_out || !aligned(slots, 8)) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   TablesParams p;
@@ -239,6 +243,7 @@ extern "C" int kvx_append_kv(const kvx_cache *c, const void *k_new, int64_t k_st
                              size_t workspace_bytes, void *stream) {
   if (!c || !q_start || max_rows < 0) return KVX_EINVAL;
   if (max_rows > 0 && (!k_new || !v_new || !slots)) return KVX_EINVAL;
+  if (max_rows > kMaxRows) return KVX_ERANGE;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8)) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   AppendParams p;
@@ -272,7 +277,7 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
                              void *workspace, size_t workspace_bytes, void *stream) {
   if (!c || !q_start || !kv_len || max_rows < 0) return KVX_EINVAL;
   if (max_rows > 0 && (!q || !out)) return KVX_EINVAL;
-  if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
+  if (max_q < 1 || max_q > KVX_MAX_TREE || max_rows > kMaxRows) return KVX_ERANGE;
   if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 4)) return KVX_EINVAL;
   TreeParams p;
@@ -324,6 +329,7 @@ extern "C" int kvx_tree_commit(const kvx_cache *c, const int32_t *q_start, const
   if (!c || !q_start || !path || !n_acc || !kv_len || !kv_len_out || max_rows < 0 ||
       (max_rows > 0 && !slots) || path_stride < 1)
     return KVX_EINVAL;
+  if (max_rows > kMaxRows) return KVX_ERANGE;
   if (!aligned(slots, 8)) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   CommitParams p;

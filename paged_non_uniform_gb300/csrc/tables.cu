@@ -81,8 +81,10 @@ __device__ __forceinline__ int owner(const int *s, int n, int k) {
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesParams p) {
   extern __shared__ int sm[];
-  __shared__ unsigned long long total[2][KVX_MAX_GROUPS];  // alloc, release
-  __shared__ unsigned long long rows_total;
+  // sums of alloc and release by group, and of the new rows: the low and the high 16
+  // bits of the terms apart (a 64-bit shared atomic is a loop; with 256 threads on one
+  // address it took 60 us)
+  __shared__ unsigned total[2 * KVX_MAX_GROUPS + 1][2];
   __shared__ int warp_sum[3][kWarps];
   __shared__ int free_in[KVX_MAX_GROUPS];
   __shared__ int8_t heads[KVX_MAX_KV_HEADS];  // heads by group
@@ -92,9 +94,14 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   const int B = c.B, G = c.G, Hkv = c.Hkv, P = c.P, lgP = c.lgP, tid = threadIdx.x;
   const int own = blockIdx.y;  // this block's group
   int *a_start = sm, *r_start = sm + (B + 1), *q_start = sm + 2 * (B + 1);
-  if (tid < KVX_MAX_GROUPS) total[0][tid] = total[1][tid] = 0;
+  if (tid <= 2 * KVX_MAX_GROUPS) total[tid][0] = total[tid][1] = 0;
+  auto add = [&](int k, int v) {
+    if (v <= 0) return;
+    atomicAdd(&total[k][0], (unsigned)v & 0xffffu);
+    if (v >> 16) atomicAdd(&total[k][1], (unsigned)v >> 16);
+  };
+  auto sum_of = [&](int k) { return (int64_t)total[k][0] + ((int64_t)total[k][1] << 16); };
   if (tid == 0) {
-    rows_total = 0;
     int n = 0;
     for (int g = 0; g < G; ++g) {
       head_off[g] = n;
@@ -123,22 +130,22 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     bad |= t < 0 || have < 0 || have > c.grp[g].stride || n > ((int64_t)c.grp[g].stride << lgP);
     const int need = (int)((n + P - 1) >> lgP);
     const int alloc = max(0, need - have), rel = max(0, have - need);
-    if (alloc) atomicAdd(&total[0][g], (unsigned long long)alloc);
-    if (rel) atomicAdd(&total[1][g], (unsigned long long)rel);
+    add(2 * g, alloc);
+    add(2 * g + 1, rel);
     if (g == own) {
       a_start[b] = alloc;
       r_start[b] = rel;
       q_start[b] = t;
-      if (t > 0) atomicAdd(&rows_total, (unsigned long long)t);
+      add(2 * KVX_MAX_GROUPS, t);
     }
   }
   bad = __syncthreads_or(bad);
   int short_list = 0;
   if (!bad) {
-    bad = rows_total > (unsigned long long)p.max_rows;
+    bad = sum_of(2 * KVX_MAX_GROUPS) > p.max_rows;
     for (int g = 0; g < G; ++g) {
       const int64_t f = free_in[g];
-      const int64_t a = (int64_t)total[0][g], r = (int64_t)total[1][g];
+      const int64_t a = sum_of(2 * g), r = sum_of(2 * g + 1);
       bad |= f < 0 || f + r > c.grp[g].pages;
       short_list |= a > f + r;
     }
@@ -189,30 +196,46 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     grp.table[(size_t)b * grp.stride + j] = popped((int)k);
   }
   // ---- slots of this group's heads, rows [r0, r1) of this block: consecutive threads
-  // take consecutive heads, then rows, so that a thread mostly stays in one
-  // sequence and a page id is read once for its neighbours
-  const int nh = grp.size;
+  // take consecutive heads, then rows. A thread keeps its head and steps through
+  // rows, mostly inside one sequence, whose lengths it then keeps too.
+  const int nh = grp.size, dr = kThreads / nh;
   const int r0 = (int)((int64_t)blockIdx.x * N / gridDim.x);
   const int r1 = (int)((int64_t)(blockIdx.x + 1) * N / gridDim.x);
-  const unsigned total_slots = (unsigned)(r1 - r0) * nh;
-  int b = 0, b_end = 0;  // q_start[b + 1] of the sequence of the last row
-  for (unsigned i = tid; i < total_slots; i += kThreads) {
-    const int row = r0 + (int)(i / (unsigned)nh), rank = (int)(i % (unsigned)nh);
+  const int rank = tid % nh, h = heads[head_off[own] + rank];
+  // slot = page * page_rows + off * off_rows + first
+  const int page_rows = nh << lgP, off_rows = c.token_major ? nh : 1;
+  const int first_row = c.token_major ? rank : rank << lgP;
+  const unsigned pages = (unsigned)grp.pages;
+  const int top = F + R - 1;
+  const int32_t *row_table = nullptr;
+  int shift = 0, have = 0, fresh = 0, b_end = 0;  // of the sequence that holds the row
+  const int stop = tid < dr * nh ? r1 : r0;
+  int64_t *out = p.slots + ((size_t)r0 + tid / nh) * Hkv + h;
+  const size_t out_step = (size_t)dr * Hkv;
+#pragma unroll 1
+  for (int row = r0 + tid / nh; row < stop; row += dr, out += out_step) {
     if (row >= b_end) {
-      b = owner(q_start, B, row);
+      const int b = owner(q_start, B, row);
       b_end = q_start[b + 1];
+      shift = __ldg(p.kv_len + (size_t)b * Hkv + h) - q_start[b];
+      have = __ldg(pages_in + b);
+      fresh = top - a_start[b] + have;  // page j is at list position fresh - j
+      row_table = grp.table + (size_t)b * grp.stride;
     }
-    const int h = heads[head_off[own] + rank];
-    const int t = __ldg(p.kv_len + (size_t)b * Hkv + h) + (row - q_start[b]);
-    const int j = t >> lgP, have = __ldg(pages_in + b);
-    const int page = j < have ? grp.table[(size_t)b * grp.stride + j]
-                              : popped(a_start[b] + (j - have));
-    int64_t slot = -1;
-    if (page >= 0 && page < grp.pages)
-      slot = pool_row(c, grp, page, rank, t & (P - 1));
+    const int t = row + shift, j = t >> lgP;
+    int page;
+    if (j < have)
+      page = row_table[j];
+    else if (fresh - j < F)
+      page = list[fresh - j];
     else
+      page = released(fresh - j - F);
+    int64_t slot = (int64_t)page * page_rows + ((t & (P - 1)) * off_rows + first_row);
+    if ((unsigned)page >= pages) {
+      slot = -1;
       atomicOr(p.status, KVX_DEV_BAD_PAGE);
-    p.slots[(size_t)row * Hkv + h] = slot;
+    }
+    *out = slot;
   }
 }
 
@@ -221,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st) {
   const int64_t slots = (int64_t)p.max_rows * p.c.Hkv;
   const int64_t want = (slots / p.c.G + 8 * kThreads - 1) / (8 * kThreads);
-  const int most = 1216 / p.c.G;  // eight blocks per SM over all groups
+  const int most = 912 / p.c.G;  // six blocks per SM over all groups
   const unsigned blocks = (unsigned)(want < 1 ? 1 : want > most ? most : want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, (unsigned)p.c.G);

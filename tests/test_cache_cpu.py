@@ -119,3 +119,17 @@ def test_reference_tables_by_hand():
     assert t[0].tolist() == [[5, 6, 7], [8, 7, 2]] and pages.tolist() == [[2, 3]]
     assert f[0].tolist() == [1, 2, 7, -1] and left.tolist() == [1] and qs.tolist() == [0, 2, 14]
     assert slots[:, 0].tolist() == [49, 50] + list(range(56, 64)) + list(range(16, 20))
+
+
+def test_row_count_limit(kvx):
+    c = make(kvx)
+    for name, good in (("kvx_build_tables", TABLES), ("kvx_append_kv", APPEND), ("kvx_tree_attn", TREE),
+                       ("kvx_tree_commit", COMMIT)):
+        refused(kvx, kvx.KVX_ERANGE, getattr(kvx, name), c, **{**good, "max_rows": (1 << 30) + 1})
+
+
+def test_bf16_pool_limit(kvx):
+    """A bf16 pool's pages times the larger of |G| and P / 8 stay in int32 (tensor-map coordinates)."""
+    refused(kvx, kvx.KVX_ERANGE, make, kvx, pages=(9, 2 ** 30), P=16)
+    make(kvx, pages=(9, 2 ** 30), P=16, dtype=kvx.KVX_F32)
+    make(kvx, pages=(9, 2 ** 30 - 2), P=16)
