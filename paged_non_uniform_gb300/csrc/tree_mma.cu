@@ -18,7 +18,8 @@
 //    the row's reference in one barrier with an OR a tile, and keep sums of their own;
 //  * warp 11 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
 //    8 new rows x the g heads) and cleans the V tiles that hold drafts or the
-//    head's end: rows past the end are zeroed (stale or padding data), and
+//    head's end: rows past the end are zeroed to a whole step of 16 keys (stale or
+//    padding data; the products stop there), and
 //    non-finite values of drafts are replaced by zero and noted, because a weight
 //    of 0 does not silence them for rows that do not see the draft; the epilogue
 //    adds them to the rows that do.
@@ -165,14 +166,14 @@ __device__ __noinline__ void rescale(uint32_t at, int cols, float f) {
   tmem_wait_st();
 }
 
-// Weights of 64 keys of a row from their scores, in place: per 16 keys, 8 columns of
+// Weights of (at most 64, by 16) keys of a row from their scores, in place: per 16 keys, 8 columns of
 // high parts and 8 of residuals (two keys a column), the A operands of two products.
 // Returns their sum.
-__device__ __forceinline__ float weigh(uint32_t s_at, float scale, float ref) {
+__device__ __forceinline__ float weigh(uint32_t s_at, int keys, float scale, float ref) {
   const uint64_t scale2 = pack2(scale, scale), ref2 = pack2(-ref, -ref);
   uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-  for (int c = 0; c < 64; c += 16) {
+  for (int c = 0; c < keys; c += 16) {
     uint32_t x[16], y[16];
     tmem_get16(s_at + c, x);
 #pragma unroll
@@ -375,16 +376,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     produce<D, true>(mp, range, base + C::kVs, v_full, v_empty, abort, lane);
   } else if (warp == 10) {
     if (lane == 0) {
-      constexpr uint32_t kS = mma_desc(128, kTile, false), kO = mma_desc(128, D, true);
+      constexpr uint32_t kS = mma_desc(128, 0, false), kO = mma_desc(128, D, true);
       int n = 0;
       for (int i = 0;; ++i) {
         const TreeItem &it = item_at(i);
         const int tiles = it.t1 - it.t0;
+        // keys from the item's first tile on
+        const int keys = it.head.n + it.head.T - it.t0 * kTile;
         if (*abort || tiles <= 0) break;
         // (the queries are loaded once the item before is done with Q and O)
         wait(q_full, i & 1, abort, p.status);
         for (int j = 0; j < tiles; ++j, ++n) {
           const int ks = n % C::kK, vs = n % C::kV;
+          const int steps = min(kTile, keys - j * kTile + 15) / 16;  // of 16 keys
           wait(k_full + 8 * ks, (n / C::kK) & 1, abort, p.status);
           tc_fence_after();
           if (!*abort) {
@@ -395,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < D / 16; ++e) {
               const uint32_t off = (e & 3) * 32;
               mma_ss(tS, smem_desc(base + (e >> 2) * C::kQHalf + off, 0, 1024),
-                     smem_desc(k + (e >> 2) * 1024 + off, 0, C::kGroup), kS, e > 0);
+                     smem_desc(k + (e >> 2) * 1024 + off, 0, C::kGroup), kS + (steps << 18),
+                     e > 0);
             }
           }
           mma_commit(s_full);
@@ -408,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t v = base + C::kVs + vs * C::kTileBytes;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
+              if (k >= steps) break;
               const uint64_t b = smem_desc(v + k * 2 * C::kGroup, 1024, C::kGroup);
               mma_ts(tO, tS + 16 * k, b, kO, !(first && k == 0));
               mma_ts(tO, tS + 16 * k + 8, b, kO, true);
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint8_t *v0 = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * 1024 + (x & 7) * 16;
           auto v = [&](int row) { return v0 + (row >> 3) * C::kGroup + (row & 7) * 128; };
 #pragma unroll 4
-          for (int row = valid + lane / CPR; row < kTile; row += RPW)
+          for (int row = valid + lane / CPR; row < ((valid + 15) & ~15); row += RPW)
             *(uint4 *)v(row) = make_uint4(0, 0, 0, 0);
           for (int r0 = first; r0 < valid; r0 += 4 * RPW) {
             uint4 y[4];
@@ -542,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       float m_acc = -INFINITY;       // reference of the folded output
       for (int j = 0; j < tiles; ++j) {
         const int u0 = (it.t0 + j) * kTile - it.head.n;  // the tile's first key as a draft
+        // keys of this thread, to whole steps of 16; a tile past its head's end has fewer
+        const int keys = live ? min(64, (it.head.T - u0 - half * 64 + 15) & ~15) : 0;
         wait(s_full, n++ & 1, abort, p.status);
         tc_fence_after();
         const bool turn = j > 0 && j % kFold == 0;  // O starts afresh
@@ -562,10 +570,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             m_acc = m;
           }
-          if (u0 + kTile > 0)
-            hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, row), row < rows,
-                      u0 + half * 64, s_at);
-          top = top_score(s_at) * p.scale_log2;
+          if (keys > 0) {
+            if (u0 + kTile > 0)
+              hide_keys(p, it.head, tree_first(p, it) + tree_div_g(p, row), row < rows,
+                        u0 + half * 64, s_at);
+            top = top_score(s_at) * p.scale_log2;
+          }
         }
         // The reference is the maximum of a row's first tile and rises only when a score
         // passes it by more than kGrow: weights and sums are then at most 2^kGrow times
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             rescale(o_at, D / 2, f);
           m = mn;
         }
-        if (live) l += weigh(s_at, p.scale_log2, m == -INFINITY ? 0.f : m);
+        if (keys > 0) l += weigh(s_at, keys, p.scale_log2, m == -INFINITY ? 0.f : m);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready);
