@@ -260,7 +260,7 @@ int kvx_plan_set_trace(kvx_plan *plan, int64_t *dev_trace);
 /* Failure-detection test hook (no effect unless called). The tensor-core
  * kernel's thread block `block` arms the barrier of its first pipeline stage
  * but issues none of its loads, so the wait for that stage runs out after
- * wait_limit_ns (1 ms .. 10 s; every pipeline wait uses this limit, 2 s by
+ * wait_limit_ns (1 ms .. 4 s; every pipeline wait uses this limit, 2 s by
  * default). The call then finishes with KVX_DEV_TIMEOUT set in the workspace
  * status word; its output is undefined, the CUDA context stays usable, and the
  * workspace must be cleared before the next call. block < 0 turns the stall
@@ -671,9 +671,10 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  * negative, descending or past max_rows, or whose kv_len is negative or
  * does not fit its page table together with its new rows, is treated as
  * having no new rows, and KVX_DEV_BAD_LENGTH is set.
- * Launch: one kernel each, a programmatic dependent of the kernel before it
- * on the stream that waits for that kernel before it reads or writes
- * anything. All may be captured into a CUDA graph, also as their first call.
+ * Launch: one kernel each (kvx_tree_attn: two, the second folds heads that were
+ * cut over blocks), a programmatic dependent of the kernel before it on the
+ * stream that waits for that kernel before it reads or writes anything. All may
+ * be captured into a CUDA graph, also as their first call.
  * ------------------------------------------------------------------------- */
 typedef struct kvx_cache kvx_cache;
 
@@ -693,6 +694,15 @@ int kvx_cache_create(const kvx_shape *shape, const int32_t *head_group,
                      int32_t *const *page_tables, const int32_t *page_table_stride,
                      kvx_cache **out);
 void kvx_cache_destroy(kvx_cache *cache);
+
+/* Failure-detection test hook (no effect unless called), as kvx_plan_inject_stall: block
+ * `block` of kvx_tree_attn's tensor-core kernel waits for one arrival more than its first
+ * K tile gets, so that the wait runs out after wait_limit_ns (1 ms .. 4 s; every
+ * pipeline wait of later calls with this cache uses this limit, 2 s by default). The
+ * call then finishes with KVX_DEV_TIMEOUT in its status word; its output is undefined,
+ * the CUDA context stays usable. block < 0 turns the stall off (the limit stays as
+ * given). Errors: KVX_EINVAL, KVX_ERANGE. */
+int kvx_cache_inject_stall(kvx_cache *cache, int32_t block, uint64_t wait_limit_ns);
 
 /* ---------------------------------------------------------------------------
  * kvx_build_tables -- page tables and slot maps from request lengths, on the
@@ -719,6 +729,8 @@ void kvx_cache_destroy(kvx_cache *cache);
  *   q_start     written: exclusive sums of new_len, [B+1].
  *   slots       written for rows [0, q_start[B]); -1 where the page id is
  *               outside the pool (KVX_DEV_BAD_PAGE).
+ * A page belongs to one sequence: the ids in a group's tables and free list are
+ * distinct (there are no reference counts; kvx_frame_* has them).
  * Table entries past pages_out and free-list entries past free_out keep
  * stale ids. A call repeated with the same inputs gives the same result (the
  * counts are not updated in place), which lets a graph be replayed.
@@ -778,7 +790,11 @@ int kvx_append_kv(const kvx_cache *cache, const void *k_new, int64_t k_stride,
  * T_b = 1 with mask NULL is one decode step with device lengths. The keys are
  * split over the GPU from the lengths, on the device; pieces of a head
  * are merged by log-sum-exp in a fixed order (equal inputs give equal bits).
- * Page ids outside a pool read as zero rows (KVX_DEV_BAD_PAGE).
+ * Page ids outside a pool read as zero rows (KVX_DEV_BAD_PAGE). bf16 caches run
+ * on the tensor cores (tcgen05), with weights of 16 significant bits and fp32 sums;
+ * fp32 caches on the CUDA cores. More work than 2^31 units of a fifth of a tile (64
+ * or 128 keys for 32 or 128 query rows), reachable only through aliased
+ * pages, is refused whole (KVX_DEV_BAD_LENGTH).
  * Errors: KVX_EINVAL, KVX_ERANGE (max_q), KVX_ECUDA.
  * ------------------------------------------------------------------------- */
 int kvx_tree_attn_workspace_bytes(const kvx_cache *cache, int32_t max_q, size_t *bytes);

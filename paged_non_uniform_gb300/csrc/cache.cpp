@@ -194,6 +194,8 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
   for (int gi = 0; gi < G; ++gi)
     d.grp[gi] = {page_tables[gi],  (char *)k_pools[gi],   (char *)v_pools[gi],
                  pool_pages[gi],   page_table_stride[gi], size[gi]};
+  c->stall_block = -1;
+  c->wait_ns = 2000000000u;
   c->have_maps = s->dtype == KVX_BF16;
   for (int gi = 0; gi < G && c->have_maps; ++gi)
     c->have_maps = encode_map(&c->k_maps[gi], c, d.grp[gi].k, d.grp[gi]) &&
@@ -203,6 +205,14 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
 }
 
 extern "C" void kvx_cache_destroy(kvx_cache *c) { delete c; }
+
+extern "C" int kvx_cache_inject_stall(kvx_cache *c, int32_t block, uint64_t wait_limit_ns) {
+  if (!c) return KVX_EINVAL;
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > 4000000000ull) return KVX_ERANGE;
+  c->stall_block = block < 0 ? -1 : block;
+  c->wait_ns = (uint32_t)wait_limit_ns;
+  return KVX_OK;
+}
 
 extern "C" int kvx_build_tables(const kvx_cache *c, const int32_t *kv_len, const int32_t *new_len,
                                 const int32_t *pages_in, int32_t *pages_out,
@@ -305,6 +315,8 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   p.fold = (float *)(ws + w.fold);
   p.max_rows = max_rows;
   p.max_q = max_q;
+  p.stall_block = c->stall_block;
+  p.wait_ns = c->wait_ns;
   p.words = (max_q + 31) / 32;
   p.group_tokens = t.tokens;
   p.group_rows = t.rows;

@@ -93,6 +93,8 @@ struct TreeParams {
   int32_t group_rows;              // room for its query rows
   int32_t recip_g;                 // ceil(2^16 / g): r * recip_g >> 16 = r / g for r <= 1024
   float scale_log2;                // scale * log2(e)
+  int32_t stall_block;             // failure-detection test (-1: none)
+  uint32_t wait_ns;                // limit of every pipeline wait
 };
 
 // Workspace of tree attention: header | split row groups | partial (m, l) | partial o |
@@ -131,4 +133,6 @@ struct kvx_cache {
   CUtensorMap k_maps[KVX_MAX_GROUPS];
   CUtensorMap v_maps[KVX_MAX_GROUPS];
   bool have_maps;
+  int32_t stall_block;  // kvx_cache_inject_stall
+  uint32_t wait_ns;
 };

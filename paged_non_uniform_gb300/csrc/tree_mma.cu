@@ -19,18 +19,18 @@
 //  * warp 11 hands out the items, loads their queries ([half][rows][128 bytes], boxes of
 //    8 new rows x the g heads) and cleans the V tiles that hold drafts or the
 //    head's end: rows past the end are zeroed to a whole step of 16 keys (stale or
-//    padding data; the products stop there), and
-//    non-finite values of drafts are replaced by zero and noted, because a weight
-//    of 0 does not silence them for rows that do not see the draft; the epilogue
-//    adds them to the rows that do.
+//    padding data; the products stop there), and non-finite values of drafts are
+//    replaced by zero and noted, because a weight of 0 does not silence them for rows
+//    that do not see the draft; the epilogue adds them to the rows that do.
 // P is kept as a bf16 high part and a bf16 residual (two products): with the
 // high part alone the weights would be off by 2^-9, with both by 2^-18, below
 // the fp32 output's other errors. They overwrite the scores they came from, column
 // block by column block.
 // Loops are kept rolled and the per-item path short: the roles run side by side on
 // one instruction cache.
-// Every mbarrier wait gives up after two seconds, sets KVX_DEV_TIMEOUT and lets
-// all roles run to their end without waiting, loading or multiplying.
+// Every mbarrier wait gives up after p.wait_ns (2 s unless a test shortens it), sets
+// KVX_DEV_TIMEOUT and lets all roles run to their end without waiting, loading or
+// multiplying.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stddef.h>
@@ -46,7 +46,6 @@ constexpr int kTile = 128;       // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kSoft = 256;       // threads of the softmax warps
 constexpr int kMinTiles = 1;     // tiles a block takes at least
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 16.f;    // log2 growth of the maximum that raises the reference
 // Tiles after which the output leaves tensor memory for an fp32 sum: the
 // tensor cores truncate each of the 16 additions a tile makes to every output
@@ -95,17 +94,17 @@ struct alignas(128) MmaParams {
 // Bounded wait for the phase of `bar` with the given parity. When it runs out, or
 // another role's has, waits end at once and the block runs down.
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *abort,
-                                     uint32_t *status) {
+                                     const TreeParams &p) {
   if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
+  const uint32_t t0 = timer_ns32();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return;
     if (*abort) return;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (timer_ns32() - t0 > p.wait_ns) {
       *abort = 1;
-      atomicOr(status, KVX_DEV_TIMEOUT);
+      atomicOr(p.status, KVX_DEV_TIMEOUT);
       return;
     }
   }
@@ -166,9 +165,9 @@ __device__ __noinline__ void rescale(uint32_t at, int cols, float f) {
   tmem_wait_st();
 }
 
-// Weights of (at most 64, by 16) keys of a row from their scores, in place: per 16 keys, 8 columns of
-// high parts and 8 of residuals (two keys a column), the A operands of two products.
-// Returns their sum.
+// Weights of keys (at most 64, whole steps of 16) of a row from their scores, in place:
+// per 16 keys, 8 columns of high parts and 8 of residuals (two keys a column), the A
+// operands of two products. Returns their sum.
 __device__ __forceinline__ float weigh(uint32_t s_at, int keys, float scale, float ref) {
   const uint64_t scale2 = pack2(scale, scale), ref2 = pack2(-ref, -ref);
   uint64_t sum[2] = {0, 0};
@@ -289,7 +288,7 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
 #pragma unroll
     for (int i = 0; i + 1 < kAhead; ++i) pages[i] = pages[i + 1];
     pages[kAhead - 1] = page_of();
-    if (n >= kN) wait(empty0 + 8 * slot, ((n / kN) - 1) & 1, abort, p.status);
+    if (n >= kN) wait(empty0 + 8 * slot, ((n / kN) - 1) & 1, abort, p);
     if (__any_sync(0xffffffffu, *abort)) return;
     const uint32_t full = full0 + 8 * slot;
     if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * box * 128 * C::kHalves));
@@ -337,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) {
-      mbar_init(k_full + 8 * i, 1);
+      // (failure-detection test: one arrival more than will come, so that the wait
+      // for this block's first K tile runs out)
+      mbar_init(k_full + 8 * i, i == 0 && (int)blockIdx.x == p.stall_block ? 2 : 1);
       mbar_init(k_empty + 8 * i, 1);
     }
     for (int i = 0; i < C::kV; ++i) {
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const TreeRange range = tree_range<kThreads, kTile>(p, kMinTiles, ctl.warp_sum, &ctl.range);
   // Item i of the block (the last is followed by one without tiles).
   auto item_at = [&](int i) -> const TreeItem & {
-    wait(i_full + 8 * (i % kItems), (i / kItems) & 1, abort, p.status);
+    wait(i_full + 8 * (i % kItems), (i / kItems) & 1, abort, p);
     return ctl.item[i % kItems];
   };
 
@@ -385,11 +386,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int keys = it.head.n + it.head.T - it.t0 * kTile;
         if (*abort || tiles <= 0) break;
         // (the queries are loaded once the item before is done with Q and O)
-        wait(q_full, i & 1, abort, p.status);
+        wait(q_full, i & 1, abort, p);
         for (int j = 0; j < tiles; ++j, ++n) {
           const int ks = n % C::kK, vs = n % C::kV;
           const int steps = min(kTile, keys - j * kTile + 15) / 16;  // of 16 keys
-          wait(k_full + 8 * ks, (n / C::kK) & 1, abort, p.status);
+          wait(k_full + 8 * ks, (n / C::kK) & 1, abort, p);
           tc_fence_after();
           if (!*abort) {
             // (P of the tile before was read by products issued before: MMAs of one
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           mma_commit(s_full);
           mma_commit(k_empty + 8 * ks);
-          wait(v_ready + 8 * vs, (n / C::kV) & 1, abort, p.status);
-          wait(p_ready, n & 1, abort, p.status);
+          wait(v_ready + 8 * vs, (n / C::kV) & 1, abort, p);
+          wait(p_ready, n & 1, abort, p);
           tc_fence_after();
           if (!*abort) {
             const bool first = j % kFold == 0;  // overwrites O
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive(i_full + 8 * (i % kItems));
       }
       if (!more) break;
-      if (i > 0) wait(i_done, (i - 1) & 1, abort, p.status);
+      if (i > 0) wait(i_done, (i - 1) & 1, abort, p);
       if (!__any_sync(0xffffffffu, *abort)) {
         // lane -> (box of 8 new rows, half): at most 16 * 2 of them
         const int boxes = (tree_rows(p, it) + kTreeBox * p.c.g - 1) / (kTreeBox * p.c.g);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t notes[4] = {0, 0, 0, 0};
       for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
         const int slot = n % C::kV, t0 = tile * kTile;
-        wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p.status);
+        wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p);
         if (t0 + kTile > it.head.n) {
           const int first = max(0, it.head.n - t0), valid = min(kTile, len - t0);
           // chunk (16 bytes) x of a row: half x >> 3, place x & 7
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int u0 = (it.t0 + j) * kTile - it.head.n;  // the tile's first key as a draft
         // keys of this thread, to whole steps of 16; a tile past its head's end has fewer
         const int keys = live ? min(64, (it.head.T - u0 - half * 64 + 15) & ~15) : 0;
-        wait(s_full, n++ & 1, abort, p.status);
+        wait(s_full, n++ & 1, abort, p);
         tc_fence_after();
         const bool turn = j > 0 && j % kFold == 0;  // O starts afresh
         float top = -INFINITY;
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // ---- epilogue
       decide(i + 1);
-      wait(o_full, i & 1, abort, p.status);  // (all have left the last tile)
+      wait(o_full, i & 1, abort, p);  // (all have left the last tile)
       tc_fence_after();
       ctl.swap[half][row] = l;
       named_sync(1, kSoft);

@@ -152,6 +152,7 @@ lib.kvx_cache_create.argtypes = [_c.POINTER(kvx_shape), _vp, _vp, _vp, _vp, _vp,
                                  _c.POINTER(_vp)]
 lib.kvx_cache_destroy.argtypes = [_vp]
 lib.kvx_cache_destroy.restype = None
+lib.kvx_cache_inject_stall.argtypes = [_vp, _c.c_int32, _c.c_uint64]
 lib.kvx_build_tables.argtypes = [_vp] * 8 + [_c.c_int32, _vp, _vp, _vp, _c.c_size_t, _vp]
 lib.kvx_append_kv.argtypes = [_vp, _vp, _c.c_int64, _vp, _c.c_int64, _vp, _vp, _c.c_int32, _vp,
                               _c.c_size_t, _vp]
@@ -577,6 +578,11 @@ class Cache:
                                     ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
         self.handle = h.value
         self._keep = (list(k_pools), list(v_pools), list(page_tables))
+
+    def inject_stall(self, block: int, wait_limit_ns: int) -> None:
+        """Failure-detection test hook: see kvx_cache_inject_stall."""
+        _check(lib.kvx_cache_inject_stall(self.handle, int(block), int(wait_limit_ns)),
+               "kvx_cache_inject_stall")
 
     def destroy(self) -> None:
         if self.handle:

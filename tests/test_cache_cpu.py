@@ -133,3 +133,13 @@ def test_bf16_pool_limit(kvx):
     refused(kvx, kvx.KVX_ERANGE, make, kvx, pages=(9, 2 ** 30), P=16)
     make(kvx, pages=(9, 2 ** 30), P=16, dtype=kvx.KVX_F32)
     make(kvx, pages=(9, 2 ** 30 - 2), P=16)
+
+
+def test_inject_stall_refusals(kvx):
+    c = make(kvx)
+    for limit in (0, 999_999, 4_000_000_001):
+        refused(kvx, kvx.KVX_ERANGE, c.inject_stall, 0, limit)
+    c.inject_stall(3, 1_000_000)
+    c.inject_stall(-1, 2_000_000_000)
+    c.destroy()
+    refused(kvx, kvx.KVX_EINVAL, c.inject_stall, 0, 1_000_000)

@@ -351,3 +351,92 @@ def test_long_items_leave_tensor_memory_in_time(T, D):
     err = (out.view(T * g, D).double() - want).abs()
     assert bool((err <= tol).all()), (float(err.max()), float((err / tol).max()))
     assert kvx.kvx_workspace_status(ws) == 0
+
+
+def batch_reference(kp, vp, tables, kv, q_start, q, see, scale, P):
+    """float64 attention of every sequence and head on the GPU: pools [pages][P][D] of one head group of
+    one head each, tables [Hkv][B][stride]; see[b]: bool [T][T]."""
+    Hkv, g = len(kp), q.shape[1] // len(kp)
+    out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(out)
+    for b in range(kv.shape[0]):
+        r0, r1 = int(q_start[b]), int(q_start[b + 1])
+        if r0 == r1:
+            continue
+        hide = torch.from_numpy(~see[b]).cuda()
+        for h in range(Hkv):
+            n = int(kv[b, h])
+            t = torch.arange(n + r1 - r0, device="cuda")
+            rows = tables[h][b][t // P].long() * P + t % P
+            k, v = kp[h].view(-1, kp[h].shape[-1])[rows].double(), vp[h].view(-1, vp[h].shape[-1])[rows].double()
+            x = torch.einsum("tgd,ld->tgl", q[r0:r1, h * g:(h + 1) * g].double(), k) * scale
+            x[:, :, n:] = x[:, :, n:].masked_fill(hide[:, None], -float("inf"))
+            p = torch.nan_to_num(torch.softmax(x, -1))  # rows that see nothing
+            out[r0:r1, h * g:(h + 1) * g] = p @ v
+            mag[r0:r1, h * g:(h + 1) * g] = p @ v.abs()
+    return out, mag
+
+
+@pytest.mark.parametrize("dtype,g,tmax,hi", [("bf16", 4, 8, 700), ("bf16", 5, 48, 5000), ("bf16", 8, 128, 900),
+                                             ("bf16", 2, 1, 3000), ("f32", 3, 20, 800)])
+def test_many_ragged_sequences(dtype, g, tmax, hi):
+    """Batches in which every block has several items of unlike lengths, cut at any tile: 60 sequences
+    x 4 heads with budgets of their own, some sequences without rows, some heads without a cache."""
+    r = np.random.default_rng(tmax)
+    B, Hkv, D, P = 60, 4, 128, 16
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(tmax)
+    kv = r.integers(0, hi + 1, (B, Hkv))
+    kv[r.random((B, Hkv)) < 0.05] = 0
+    T = r.integers(0, tmax + 1, B)
+    q_start = np.concatenate([[0], np.cumsum(T)]).astype(np.int32)
+    N = int(q_start[-1])
+    stride = -(-(hi + tmax) // P)
+    kp = [torch.empty(B * stride, P, D, dtype=tt, device="cuda").normal_(generator=gen) for _ in range(Hkv)]
+    vp = [torch.empty(B * stride, P, D, dtype=tt, device="cuda").normal_(generator=gen) for _ in range(Hkv)]
+    tables = [torch.randperm(B * stride, generator=gen, device="cuda").int().view(B, stride) for _ in range(Hkv)]
+    q = torch.empty(N, Hkv * g, D, dtype=tt, device="cuda").normal_(generator=gen)
+    W = (tmax + 31) // 32
+    see = [np.tril(r.random((t, t)) < 0.4) for t in T]  # (rows that see no draft among them)
+    words = np.zeros((N, W), np.uint32)
+    for b in range(B):
+        for i in range(T[b]):
+            for j in np.flatnonzero(see[b][i]):
+                words[q_start[b] + i, j // 32] |= np.uint32(1 << (j % 32))
+    cache = kvx.Cache(B, Hkv * g, Hkv, D, P, Hkv, kvx.KVX_BF16 if dtype == "bf16" else kvx.KVX_F32,
+                      list(range(Hkv)), kp, vp, [B * stride] * Hkv, tables, [stride] * Hkv)
+    ws = torch.zeros(kvx.kvx_tree_attn_workspace_bytes(cache, tmax) // 4, dtype=torch.int32, device="cuda")
+    out = torch.full((N, Hkv * g, D), float("nan"), device="cuda")
+    args = (cache, q, torch.from_numpy(q_start).cuda(), N, tmax, torch.from_numpy(kv.astype(np.int32)).cuda(),
+            torch.from_numpy(words.view(np.int32)).cuda(), 0.0, out, ws)
+    kvx.kvx_tree_attn(*args)
+    torch.cuda.synchronize()
+    first = out.clone()
+    for _ in range(5):
+        kvx.kvx_tree_attn(*args)
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)  # equal inputs give equal bits
+    assert kvx.kvx_workspace_status(ws) == 0
+    want, mag = batch_reference(kp, vp, tables, kv, q_start, q, see, D ** -0.5, P)
+    # error_bound of tree_cases with |s| <= 8 (128-dim dot products of N(0, 1), scaled; largest of 10^7
+    # draws below 6), s_abs <= 14 (mean 7.2, deviation 0.6), at most hi + 128 keys
+    u = 2.0 ** -24
+    weight = 2 * u * 130 * 14 + 3 * u * 24 + 2.0 ** -22
+    tol = (2 * weight + 2.0 ** -18 + 4 * u * (hi + 192) + 4 * u) * mag
+    err = (out.double() - want).abs()
+    assert bool((err <= tol).all()), (float(err.max()), float((err / tol.clamp(min=1e-30)).max()))
+
+
+def test_wait_that_runs_out_is_reported():
+    """A block whose first K tile never arrives gives up after the limit: the call ends with
+    KVX_DEV_TIMEOUT, and the next call on a cleared workspace is right."""
+    s = Setup(Case("bf16", 128, 2, 4, (0, 0), kv=((3000, 700), (900, 20)), T=(16, 9), seed=17)).upload()
+    want = s.run().copy()
+    s.cache.inject_stall(1, 20_000_000)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status() & kvx.KVX_DEV_TIMEOUT
+    s.cache.inject_stall(-1, 2_000_000_000)
+    kvx.kvx_workspace_clear(s.ws)
+    assert np.array_equal(s.run(), want)
+    assert s.status() == 0
