@@ -12,7 +12,8 @@
 //  * warps 8 and 9 load K and V tiles from their pages into two rings (bulk
 //    tensor loads, one box a page of at most 128 rows, landing as [8-row group][half
 //    of the dims][8 rows][128 bytes], 128-byte swizzled);
-//  * warp 10 issues the MMAs: S, then O += P V of the tile;
+//  * warp 10 issues the MMAs: S, then O += P V of the tile. An item's first scores are
+//    computed under the epilogue of the item before;
 //  * warps 0-3 and 4-7 do the softmax: a query row belongs to two threads, one for each
 //    half of a tile's keys (a thread can only reach one lane of TMEM). They agree on
 //    the row's reference in one barrier with an OR a tile, and keep sums of their own;
@@ -52,7 +53,7 @@ constexpr float kGrow = 16.f;    // log2 growth of the maximum that raises the r
 // element, which over 200 tiles was measured as 5e-5 of the output, growing
 // linearly; over 16 tiles it stays below 5e-6.
 constexpr int kFold = 16;
-constexpr int kItems = 8;        // item slots: more than V tiles in flight, plus one
+constexpr int kItems = 4;        // item slots: the epilogue is at most three items behind
 
 struct alignas(16) Ctl {  // small shared state
   uint64_t bars[28];
@@ -75,7 +76,7 @@ struct Cfg {
   static constexpr int kGroup = 1024 * kHalves;        // K, V: all dims of 8 rows together
   static constexpr int kSlots = (111 * 1024 - kTileBytes) / kTileBytes;  // K and V tiles
   static constexpr int kV = (kSlots + 1) / 2, kK = kSlots - kV;
-  static_assert(kK >= 1 && kV + 1 < kItems, "ring depths");
+  static_assert(kK >= 1, "ring depths");
   static constexpr int kBars = 2 * kK + 3 * kV + 5 + kItems;
   static constexpr int kKs = kTileBytes, kVs = kKs + kK * kTileBytes;
   static constexpr int kCtl = kVs + kV * kTileBytes;
@@ -326,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t p_ready = s_full + 8;           // weights of a tile are ready
   const uint32_t o_full = p_ready + 8;           // the output of an item is complete
   const uint32_t q_full = o_full + 8;            // queries of an item are loaded
-  const uint32_t i_done = q_full + 8;            // the softmax warps are done with an item
-  const uint32_t i_full = i_done + 8;            // [kItems] an item is written
+  const uint32_t q_empty = q_full + 8;           // the last scores of an item are done
+  const uint32_t i_full = q_empty + 8;           // [kItems] an item is written
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   if (base & 1023u) {  // no toolchain places it so; nothing below would hold
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(p_ready, kSoft / 32);
     mbar_init(o_full, 1);
     mbar_init(q_full, 1);
-    mbar_init(i_done, kSoft / 32);
+    mbar_init(q_empty, 1);
     for (int i = 0; i < kItems; ++i) mbar_init(i_full + 8 * i, 1);
     ctl.abort = 0;
     fence_barrier_init();
@@ -385,7 +386,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         // keys from the item's first tile on
         const int keys = it.head.n + it.head.T - it.t0 * kTile;
         if (*abort || tiles <= 0) break;
-        // (the queries are loaded once the item before is done with Q and O)
         wait(q_full, i & 1, abort, p);
         for (int j = 0; j < tiles; ++j, ++n) {
           const int ks = n % C::kK, vs = n % C::kV;
@@ -406,11 +406,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           mma_commit(s_full);
           mma_commit(k_empty + 8 * ks);
+          if (j == tiles - 1) mma_commit(q_empty);
           wait(v_ready + 8 * vs, (n / C::kV) & 1, abort, p);
           wait(p_ready, n & 1, abort, p);
           tc_fence_after();
           if (!*abort) {
-            const bool first = j % kFold == 0;  // overwrites O
+            // overwrites O (of the item before: its epilogue came before these weights)
+            const bool first = j % kFold == 0;
             const uint32_t v = base + C::kVs + vs * C::kTileBytes;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive(i_full + 8 * (i % kItems));
       }
       if (!more) break;
-      if (i > 0) wait(i_done, (i - 1) & 1, abort, p);
+      if (i > 0) wait(q_empty, (i - 1) & 1, abort, p);
       if (!__any_sync(0xffffffffu, *abort)) {
         // lane -> (box of 8 new rows, half): at most 16 * 2 of them
         const int boxes = (tree_rows(p, it) + kTreeBox * p.c.g - 1) / (kTreeBox * p.c.g);
@@ -637,9 +639,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                          ctl.notes[i % kItems], dst);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(i_done);
     }
   }
   __syncthreads();

@@ -24,11 +24,11 @@
 
 namespace kvx {
 
-// Measured on 256 sequences of 100 to 1000 tokens: an item costs a block of the
-// tensor-core kernel 3.3 us and a tile 2.4 us; with the charge the slowest block ended
-// after 125 us instead of 136 (the call: 117 us instead of 130).
+// Measured with the tensor-core kernel on 256 sequences of 100 to 1000 tokens / 16 of 2k to
+// 32k with trees of up to 48 tokens: an item charged as 3 fifths of a tile 119 / 179 us,
+// 5: 119 / 175, 7: 120.5 / 173, 9: 122.5 / 174; without a charge the first took 130.
 constexpr int kTileCost = 5;
-constexpr int kItemCost = 7;
+constexpr int kItemCost = 6;
 
 struct TreeHead {
   int b, h;      // sequence, KV head
