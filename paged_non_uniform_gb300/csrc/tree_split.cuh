@@ -79,7 +79,7 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const
 }
 
 struct TreeRange {
-  int units;       // cost of all heads
+  int units;       // cost of all heads (little work: to whole parts)
   int blocks;      // blocks with work
   int begin, end;  // this block's part of it
   int head;        // the head that holds `begin`
@@ -133,11 +133,15 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
     if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     all = 0;
   }
-  const int units = (int)all, want = units / (min_tiles * kTileCost);
-  const int blocks = want < 1 ? 1 : min(want, (int)gridDim.x);
-  const bool work = (int)blockIdx.x < blocks && units > 0;
+  // Little work: parts of exactly `least`, so that a block has no more tiles than that
+  // stands for (the last part may be shorter).
+  const int least = min_tiles * kTileCost, total = (int)all;
+  const bool little = total / least < (int)gridDim.x;
+  const int blocks = little ? (total + least - 1) / least : (int)gridDim.x;
+  const int units = little ? blocks * least : total;
+  const bool work = (int)blockIdx.x < blocks;
   const int begin = work ? tree_bound(units, blocks, blockIdx.x) : 0;
-  const int end = work ? tree_bound(units, blocks, blockIdx.x + 1) : 0;
+  const int end = work ? min(total, tree_bound(units, blocks, blockIdx.x + 1)) : 0;
   const int64_t mine = before + x - s;
   if (!work) {
     if (tid == 0) *shared = {units, blocks, 0, 0, 0, 0, {}};
