@@ -104,22 +104,21 @@ template <int NT, int kTile>
 __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_tiles,
                                                 int64_t *warp_sum /* shared, NT / 32 */,
                                                 TreeRange *shared) {
-  const int heads = p.c.B * p.c.Hkv;
-  const int per = (heads + NT - 1) / NT;
+  // Each warp takes a run of heads, its lanes one head in turn.
+  const int heads = p.c.B * p.c.Hkv, run = (heads + NT / 32 - 1) / (NT / 32);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lo = min(heads, tid * per), hi = min(heads, lo + per);
+  const int lo = min(heads, warp * run), hi = min(heads, lo + run);
   int64_t s = 0;
-  for (int i = lo; i < hi; ++i) {
-    const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), blockIdx.x == 0);
-    s += t.cost();
+  TreeRaw raw = tree_raw(p, lo + lane), raw1 = tree_raw(p, lo + lane + 32);
+  for (int i = lo + lane; i < hi; i += 32) {  // (lengths loaded two steps ahead)
+    const TreeRaw raw2 = tree_raw(p, i + 64);
+    s += tree_head<kTile>(p, i, raw, blockIdx.x == 0).cost();
+    raw = raw1;
+    raw1 = raw2;
   }
-  int64_t x = s;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) warp_sum[warp] = x;
+  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane == 0) warp_sum[warp] = s;
   __syncthreads();
   int64_t before = 0, all = 0;
 #pragma unroll
@@ -142,19 +141,27 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
   const bool work = (int)blockIdx.x < blocks;
   const int begin = work ? tree_bound(units, blocks, blockIdx.x) : 0;
   const int end = work ? min(total, tree_bound(units, blocks, blockIdx.x + 1)) : 0;
-  const int64_t mine = before + x - s;
   if (!work) {
     if (tid == 0) *shared = {units, blocks, 0, 0, 0, 0, {}};
-  } else if (begin >= mine && begin < mine + s) {
-    int base = (int)mine;
-    for (int i = lo; i < hi; ++i) {
-      const TreeHead t = tree_head<kTile>(p, i, tree_raw(p, i), false);
+  } else if (begin >= before && begin < before + s) {
+    // this warp's run holds it: 32 heads at a time
+    if (lane == 0) *shared = {units, blocks, 0, 0, 0, 0, {}};
+    __syncwarp();
+    int base = (int)before;
+    for (int i0 = lo; i0 < hi && base <= begin; i0 += 32) {
+      const int i = i0 + lane;
+      TreeHead t = {};
+      if (i < hi) t = tree_head<kTile>(p, i, tree_raw(p, i), false);
       const int u = (int)t.cost();
-      if (begin < base + u) {
-        *shared = {units, blocks, begin, end, i, base, t};
-        break;
+      int x = u;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
       }
-      base += u;
+      if (begin >= base + x - u && begin < base + x)
+        *shared = {units, blocks, begin, end, i, base + x - u, t};
+      base += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   __syncthreads();
