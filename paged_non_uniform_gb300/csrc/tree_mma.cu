@@ -263,7 +263,8 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
   const int P = p.c.P, box = min(P, kTile);
   const int per = kTile / box;  // boxes of a tile: lane i loads box i
   // Two walks over the tiles: `ahead` runs kAhead tiles before `now` and reads
-  // the page ids, so that neither the lengths nor the page table hold up a load.
+  // the page ids, so that neither the lengths nor the page table hold up a load (but
+  // the first tile is on its way before the others' are looked up).
   constexpr int kAhead = 3;
   TileWalk now(p, range), ahead(p, range);
   auto page_of = [&]() {
@@ -278,17 +279,13 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
     return page;
   };
   int pages[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) pages[i] = page_of();
+  pages[0] = page_of();
   for (int n = 0; now.more; ++n) {
     const TreeHead &h = now.it.head;
     const int gi = p.c.head_grp[h.h], rank = p.c.head_row[h.h];
     const int slot = n % kN, valid = min(kTile, h.n + h.T - now.tile * kTile);
     const int boxes = (valid + box - 1) / box;
     int page = pages[0];
-#pragma unroll
-    for (int i = 0; i + 1 < kAhead; ++i) pages[i] = pages[i + 1];
-    pages[kAhead - 1] = page_of();
     if (n >= kN) wait(empty0 + 8 * slot, ((n / kN) - 1) & 1, abort, p);
     if (__any_sync(0xffffffffu, *abort)) return;
     const uint32_t full = full0 + 8 * slot;
@@ -307,6 +304,12 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
                   kIsV ? &mp.tmV[gi] : &mp.tmK[gi], 0, 0, 0, c3, c4, full, pol);
     }
     now.step(p);
+#pragma unroll 1
+    for (int k = n ? 1 : kAhead; k; --k) {
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) pages[i] = pages[i + 1];
+      pages[kAhead - 1] = page_of();
+    }
   }
 }
 
