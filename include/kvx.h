@@ -774,7 +774,8 @@ int kvx_append_kv(const kvx_cache *cache, const void *k_new, int64_t k_stride,
  * rows t = n[b][h] + u, u < T_b, visible if bit u of the row's mask is set;
  *     out[q_start[b] + i][j] = sum over visible t of softmax(s)_t * v_t,
  * and zeros for a row that sees nothing. What a row does not see has no
- * influence on it, NaN and infinities included. K and V of the new rows are
+ * influence on it, NaN and infinities included; a non-finite element of v_t that it
+ * sees makes that element of its output non-finite, not always of the same kind. K and V of the new rows are
  * read from their pages (kvx_append_kv).
  *   q          device [max_rows] rows of Hq * D elements of the cache's dtype,
  *              16-byte aligned, q_stride elements apart (>= Hq * D, a multiple

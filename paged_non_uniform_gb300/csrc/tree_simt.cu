@@ -11,6 +11,9 @@
 // A tile that holds drafts or the head's end takes a separate path that skips
 // what a row does not see instead of multiplying it by zero, so that NaN and
 // infinities in unseen rows, and padding, have no influence.
+// fp32 products have no tensor-core form of their precision; the multiply-adds bound long
+// inputs, latency short ones: two sequences of 37 to 100 tokens 12.9 us with the merge.
+// (16 sequences of 8k to 32k took 1.08 ms here in bf16, 85 us on the tensor cores.)
 #include <math.h>
 
 #include "tree_split.cuh"

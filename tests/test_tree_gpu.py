@@ -313,10 +313,10 @@ def test_guard_bands():
 
 @pytest.mark.parametrize("T,D", [(3, 64), (40, 64), (40, 128)])
 def test_long_items_leave_tensor_memory_in_time(T, D):
-    """One head of 1.4 M keys: every block works on 72 tiles of it, so that its output is folded
-    into the fp32 sum several times (twice with the tiles taken in turn, four times with 160 rows). The
-    tensor cores truncate what they add: 16 additions to an output element a tile, each off by at most
-    2^-23 of the sum so far, over the 16 tiles between folds; the folds and the merge round like fp32."""
+    """One head of 1.4 M keys: every block works on 36 tiles of it (72 with 160 rows, which are two row
+    groups), so that its output is folded into the fp32 sum twice or four times. The tensor cores
+    truncate what they add: 16 additions to an output element a tile, each off by at most 2^-23 of the sum
+    so far, over the 16 tiles between folds; the folds and the merge round like fp32."""
     n, g = 1_400_000, 4
     P, len_ = 128, 1_400_000 + T
     pages = -(-len_ // P)
