@@ -16,7 +16,8 @@
 // neither, which is what makes a repeated call give the same result.
 // Measured on one GB300: a verify step (16 sequences, 3 groups) 6.5 us, all latency: two
 // passes of loads, the sums and their scan; 256 prompts (1.17 M rows, 9.4 M slots of 8
-// bytes) 24 us, of which the slots' 75 MB are 11.
+// bytes) 21 us, of which a plain fill with the slots' 75 MB would take 10 and the sums,
+// which every block makes, 5.
 #include "ptx.cuh"
 #include "tree.h"
 
@@ -215,8 +216,21 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   const int stop = tid < dr * nh ? r1 : r0;
   int64_t *out = p.slots + ((size_t)r0 + tid / nh) * Hkv + h;
   const size_t out_step = (size_t)dr * Hkv;
-#pragma unroll 1
-  for (int row = r0 + tid / nh; row < stop; row += dr, out += out_step) {
+  auto page_of = [&](int t) {
+    const int j = t >> lgP, at = fresh - j;
+    if (j >= have && at >= F) return released(at - F);
+    return *(j < have ? row_table + j : list + at);
+  };
+  auto put = [&](int64_t *to, int t, int page) {
+    int64_t slot = (int64_t)page * page_rows + ((t & (P - 1)) * off_rows + first_row);
+    if ((unsigned)page >= pages) {
+      slot = -1;
+      atomicOr(p.status, KVX_DEV_BAD_PAGE);
+    }
+    *to = slot;
+  };
+  int row = r0 + tid / nh;
+  while (row < stop) {
     if (row >= b_end) {
       const int b = owner(q_start, B, row);
       b_end = q_start[b + 1];
@@ -225,20 +239,19 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
       fresh = top - a_start[b] + have;  // page j is at list position fresh - j
       row_table = grp.table + (size_t)b * grp.stride;
     }
-    const int t = row + shift, j = t >> lgP;
-    int page;
-    if (j < have)
-      page = row_table[j];
-    else if (fresh - j < F)
-      page = list[fresh - j];
-    else
-      page = released(fresh - j - F);
-    int64_t slot = (int64_t)page * page_rows + ((t & (P - 1)) * off_rows + first_row);
-    if ((unsigned)page >= pages) {
-      slot = -1;
-      atomicOr(p.status, KVX_DEV_BAD_PAGE);
+    if (row + 3 * dr < min(stop, b_end)) {  // four at a time: their page ids load together
+      int page[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) page[u] = page_of(row + u * dr + shift);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) put(out + u * out_step, row + u * dr + shift, page[u]);
+      row += 4 * dr;
+      out += 4 * out_step;
+    } else {
+      put(out, row + shift, page_of(row + shift));
+      row += dr;
+      out += out_step;
     }
-    *out = slot;
   }
 }
 
@@ -247,7 +260,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t st) {
   const int64_t slots = (int64_t)p.max_rows * p.c.Hkv;
   const int64_t want = (slots / p.c.G + 8 * kThreads - 1) / (8 * kThreads);
-  const int most = 912 / p.c.G;  // six blocks per SM over all groups
+  // four blocks per SM over all groups (256 prompts: two 23 us, four 21, six 27.5, eight 24.5)
+  const int most = 608 / p.c.G;
   const unsigned blocks = (unsigned)(want < 1 ? 1 : want > most ? most : want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, (unsigned)p.c.G);
