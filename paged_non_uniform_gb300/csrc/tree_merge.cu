@@ -4,7 +4,11 @@
 // out[row] = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the partials c of the
 // row group in block order (M the largest m_c), so the result does not depend on
 // timing. One warp takes a row: lanes hold the partials' weights, then each lane one
-// float4 (D = 128) or float2 of the row, eight partials' loads in flight.
+// float4 (D = 128) or float2 of the row, four partials' loads in flight: more of them
+// cost registers, and with those the blocks that start while attention still runs. Figures
+// for one sequence of 2k / 16 of 8k to 32k, attention and merge: two rows a warp and eight
+// loads 17.7 / 85.3 us, one row and eight 15.6 / 85.2, one row and four 16.0 / 83.2, 16
+// loads 16.1 / 87.9.
 // Why a launch of its own: the block that finishes a head last used to fold it inside
 // the attention launch. With eight heads cut in seven pieces of 64 rows that took 20 us,
 // because a few blocks folded several heads one after the other, in code that no cache
@@ -16,7 +20,7 @@ namespace kvx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerBlock = 16;
+constexpr int kRowsPerBlock = kThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
@@ -25,8 +29,8 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_const
   pdl_wait();
   const TreeSplit s = p.split[blockIdx.y];
   const int lane = threadIdx.x & 31;
-  const int r_end = min(s.rows, ((int)blockIdx.x + 1) * kRowsPerBlock);
-  for (int r = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5); r < r_end; r += kThreads / 32) {
+  const int r = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5);
+  if (r < s.rows) {
     // row r of partial c: the first is its block's last piece, the others are their
     // blocks' first
     auto at = [&](int c) {
@@ -47,10 +51,10 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_const
         L = fmaf(f, ml.y, L);
       }
       const int n = min(32, s.parts - c0);
-      for (int c = 0; c < n; c += 8) {
-        alignas(16) float v[8][E];
+      for (int c = 0; c < n; c += 4) {
+        alignas(16) float v[4][E];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const float *src = p.part_o + at(c0 + c + u) * D + lane * E;
           if (c + u >= n) {
 #pragma unroll
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_const
           }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const float w = __shfl_sync(0xffffffffu, f, (c + u) & 31);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);

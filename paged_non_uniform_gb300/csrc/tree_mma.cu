@@ -31,9 +31,10 @@
 // one instruction cache, and a change of the code's order alone moves the shortest
 // items by 3 %.
 // Measured on one GB300 (a call in a graph): 16 sequences of 8k to 32k, 16 drafts, 4
-// query heads a KV head, 85 us for 427 MB, of which about 15 are the ramp, the last output
-// and the merge (tensor pipe 38 % busy); 8 x 122k, 24 drafts, 655 us for 4.0 GB (6.1
-// TB/s); 256 of 100 to 1000, 1 to 8 drafts, 121 us for 448 MB; one of 2k, 17.7 us. A tile
+// query heads a KV head, 84 us for 427 MB, of which about 15 are the ramp, the last output
+// and the merge (tensor pipe 39 % busy); 8 x 122k, 24 drafts, 650 to 690 us by GPU for 4.0
+// GB (5.8 to 6.1 TB/s); 256 of 100 to 1000, 1 to 8 drafts, 122 us for 448 MB; one of 2k,
+// 16 us. A tile
 // takes a block about 3.3 us: scores, softmax and output products one after the other, which
 // two blocks per SM hide from each other for the most part. Tried and slower: tiles or V
 // slots of 64 keys; a second V slot where 64 query rows leave room for it; the products
