@@ -369,16 +369,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     ctl.abort = 0;
     fence_barrier_init();
   }
-  if (warp == 10) tmem_alloc(smem_u32(&ctl.tmem), 256);
   if (warp >= 8 && warp < 10 && lane < p.c.G)
     prefetch_tensormap(warp == 8 ? &mp.tmK[lane] : &mp.tmV[lane]);
   if (warp == 11 && lane == 0) prefetch_tensormap(&mp.tmQ);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tS = ctl.tmem, tO = tS + kTile;  // TMEM columns of S and O
   pdl_wait();
+  // (only now: a kernel before that has yet to allocate tensor memory must not find it taken)
+  if (warp == 10) {
+    tmem_alloc(smem_u32(&ctl.tmem), 256);
+    tc_fence_before();
+  }
   const TreeRange range = tree_range<kThreads, kTile>(p, kMinTiles, ctl.warp_sum, &ctl.range);
+  tc_fence_after();  // (the search for the block's part synchronises it)
+  const uint32_t tS = ctl.tmem, tO = tS + kTile;  // TMEM columns of S and O
   // Item i of the block (the last is followed by one without tiles).
   auto item_at = [&](int i) -> const TreeItem & {
     wait(i_full + 8 * (i % kItems), (i / kItems) & 1, abort, p);
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int x = lane % CPR;
           uint8_t *v0 = smem + C::kVs + slot * C::kTileBytes + (x >> 3) * 1024 + (x & 7) * 16;
           auto v = [&](int row) { return v0 + (row >> 3) * C::kGroup + (row & 7) * 128; };
-#pragma unroll 4
+#pragma unroll 1
           for (int row = valid + lane / CPR; row < ((valid + 15) & ~15); row += RPW)
             *(uint4 *)v(row) = make_uint4(0, 0, 0, 0);
           for (int r0 = first; r0 < valid; r0 += 4 * RPW) {

@@ -440,3 +440,24 @@ def test_wait_that_runs_out_is_reported():
     kvx.kvx_workspace_clear(s.ws)
     assert np.array_equal(s.run(), want)
     assert s.status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Two caches' attention in two streams, each with a workspace of its own and its call repeated back
+    to back: the outputs are those of each alone, bit for bit."""
+    sets = [Setup(Case("bf16", 128, 4, 4, (0, 1, 1, 0), kv=((3000, 700, 900, 10),) * 8, T=(16, 5) * 4,
+                       seed=31)).upload(),
+            Setup(Case("bf16", 64, 2, 8, (0, 0), kv=((2000, 2000),) * 12, T=(40, 1, 33) * 4,
+                       seed=32)).upload()]
+    want = [s.run().copy() for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in sets:
+        s.out.fill_(-7.0)
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for s, st in zip(sets, streams):
+            s.attend(stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, want):
+        assert np.array_equal(s.out.cpu().numpy(), w)
+        assert s.status() == 0
