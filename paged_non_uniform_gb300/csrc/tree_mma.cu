@@ -223,6 +223,34 @@ __device__ __forceinline__ void add_fold(uint32_t (&x)[16], const float4 *acc, f
   }
 }
 
+// Adds half an output row to its fp32 sum, scaled by f where there is one yet.
+template <int D>
+__device__ __noinline__ void fold_out(uint32_t o_at, float4 *acc, bool more, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t x[16];
+    tmem_get16(o_at + 16 * c, x);
+    if (more) add_fold(x, acc + 4 * c * 128, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      __stcg((uint4 *)acc + (4 * c + e) * 128,
+             make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+  }
+}
+
+// The other way round: adds the fp32 sum, scaled by f, to the half row.
+template <int D>
+__device__ __noinline__ void unfold_out(uint32_t o_at, const float4 *acc, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t x[16];
+    tmem_get16(o_at + 16 * c, x);
+    add_fold(x, acc + 4 * c * 128, f);
+    tmem_st16(o_at + 16 * c, x);
+  }
+  tmem_wait_st();
+}
+
 // Adds to half an output row (from dim d0 on) the non-finite values of the noted drafts
 // that new row i sees: their weight is positive, so the sum is what they are.
 template <int D>
@@ -241,6 +269,29 @@ __device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, 
       const float b = __uint_as_float((uint32_t)__ldg(v + d0 + d) << 16);
       if (!isfinite(b)) out[d] += b;
     }
+  }
+}
+
+// Zeroes the non-finite elements of rows r0 .. of a V tile (32 rows' worth of chunks, lanes as in
+// the loop that found one) and notes their drafts.
+template <int D>
+__device__ __noinline__ void note_rows(uint8_t *v0, int r0, int valid, int u0, int lane,
+                                       uint32_t *notes) {
+  constexpr int CPR = D / 8, RPW = 32 / CPR;
+  for (int k = 0; k < 4; ++k) {
+    const int row = r0 + k * RPW + lane / CPR;
+    bool hit = false;
+    if (row < valid) {
+      uint32_t *at = (uint32_t *)(v0 + (row >> 3) * (D * 16) + (row & 7) * 128);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t e = at[i];
+        const uint32_t bad = ((e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+                             ((e & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+        if (bad) at[i] = e & ~bad;
+        hit |= bad != 0;
+      }
+    }
+    if (hit) atomicOr(notes + ((u0 + row) >> 5), 1u << ((u0 + row) & 31));
   }
 }
 
@@ -474,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                       policy_evict_first());
       }
       const int len = it.head.n + it.head.T;
-      uint32_t notes[4] = {0, 0, 0, 0};
+      if (lane < 4) ctl.notes[i % kItems][lane] = 0;
+      __syncwarp();
       for (int tile = it.t0; tile < it.t1; ++tile, ++n) {
         const int slot = n % C::kV, t0 = tile * kTile;
         wait(v_full + 8 * slot, (n / C::kV) & 1, abort, p);
@@ -504,36 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 odd |= (e[i] & 0x7f80u) == 0x7f80u || (e[i] & 0x7f800000u) == 0x7f800000u;
             }
             if (!__any_sync(0xffffffffu, odd)) continue;
-            // rare: zero the elements and note their drafts
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              const int row = r0 + k * RPW + lane / CPR;
-              bool hit = false;
-              if (row < valid) {
-                uint32_t *at = (uint32_t *)v(row);
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t e = at[i];
-                  const uint32_t bad = ((e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
-                                       ((e & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-                  if (bad) at[i] = e & ~bad;
-                  hit |= bad != 0;
-                }
-              }
-              const uint32_t who = __ballot_sync(0xffffffffu, hit);
-              for (int rr = 0; rr < RPW; ++rr) {
-                const int u = t0 + r0 + k * RPW + rr - it.head.n;
-                const uint32_t part = CPR == 32 ? ~0u : (1u << (CPR % 32)) - 1u;
-                if (!(who & (part << (rr * CPR)))) continue;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (i == (u >> 5)) notes[i] |= 1u << (u & 31);
-              }
-            }
-          }
-          if (lane < 4) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e == lane) ctl.notes[i % kItems][e] = notes[e];
+            note_rows<D>(v0, r0, valid, t0 - it.head.n, lane, ctl.notes[i % kItems]);
           }
         }
         fence_async_shared();
@@ -575,17 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (live) {
           if (turn) {
             // fold the tensor cores' sum of the last kFold tiles into fp32 (see kFold)
-            const float f = tree_weight(m_acc, m);
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[16];
-              tmem_get16(o_at + 16 * c, x);
-              if (j > kFold) add_fold(x, acc + 4 * c * 128, f);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                __stcg((uint4 *)acc + (4 * c + e) * 128,
-                       make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
-            }
+            fold_out<D>(o_at, acc, j > kFold, tree_weight(m_acc, m));
             m_acc = m;
           }
           if (keys > 0) {
@@ -633,12 +646,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (ok && half == 0) p.part_ml[at] = make_float2(m, l);
         }
         dst += half * (D / 2);
-        const float fa = tree_weight(m_acc, m);
+        if (folded) unfold_out<D>(o_at, acc, tree_weight(m_acc, m));
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[16];
           tmem_get16(o_at + 16 * c, x);
-          if (folded) add_fold(x, acc + 4 * c * 128, fa);
           if (ok) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
