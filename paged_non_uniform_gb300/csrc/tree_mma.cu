@@ -27,18 +27,19 @@
 // high part alone the weights would be off by 2^-9, with both by 2^-18, below
 // the fp32 output's other errors. They overwrite the scores they came from, column
 // block by column block.
-// Loops are kept rolled and the per-item path short: the roles run side by side on
-// one instruction cache, and a change of the code's order alone moves the shortest
-// items by 3 %.
+// Loops are kept rolled, rare paths out of line and the waits small: the roles run side by
+// side on one instruction cache. With the output products and the waits unrolled, 256
+// short sequences took 121 us instead of 102 (ragged trees 171 instead of 175).
 // Measured on one GB300 (a call in a graph): 16 sequences of 8k to 32k, 16 drafts, 4
-// query heads a KV head, 84 us for 427 MB, of which about 15 are the ramp, the last output
+// query heads a KV head, 84.5 us for 427 MB, of which about 15 are the ramp, the last output
 // and the merge (tensor pipe 39 % busy); 8 x 122k, 24 drafts, 650 to 690 us by GPU for 4.0
-// GB (5.8 to 6.1 TB/s); 256 of 100 to 1000, 1 to 8 drafts, 125 us for 448 MB; one of 2k,
-// 16.5 us. A tile takes a block about 3.3 us: scores, softmax and output products one
+// GB (5.8 to 6.1 TB/s); 256 of 100 to 1000, 1 to 8 drafts, 102 us for 448 MB; one of 2k,
+// 16.2 us. A tile takes a block about 3.3 us: scores, softmax and output products one
 // after the other, which two blocks per SM hide from each other for the most part. Tried
 // and slower: tiles or V slots of 64 keys; a second V slot where 64 query rows leave room
 // for it; the products transposed, so that few query rows fill the tensor cores (a tile
-// 2.6 us, but an item 3 to 4 us more); prefetching tiles into L2.
+// 2.6 us, but an item 3 to 4 us more); prefetching tiles into L2. (Measured against
+// 86 us for the first and 120 for the short sequences.)
 // Every mbarrier wait gives up after p.wait_ns (2 s unless a test shortens it), sets
 // KVX_DEV_TIMEOUT and lets all roles run to their end without waiting, loading or
 // multiplying.
@@ -103,21 +104,14 @@ struct alignas(128) MmaParams {
 };
 
 // Bounded wait for the phase of `bar` with the given parity. When it runs out, or
-// another role's has, waits end at once and the block runs down.
+// another role's has, waits end at once, the block runs down and reports it at its end.
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *abort,
                                      const TreeParams &p) {
   if (mbar_try_wait(bar, parity)) return;
   const uint32_t t0 = timer_ns32();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return;
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort) return;
-    if (timer_ns32() - t0 > p.wait_ns) {
-      *abort = 1;
-      atomicOr(p.status, KVX_DEV_TIMEOUT);
-      return;
-    }
+    if (timer_ns32() - t0 > p.wait_ns) *abort = 1;
   }
 }
 
@@ -479,13 +473,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!*abort) {
             // overwrites O (of the item before: its epilogue came before these weights)
             const bool first = j % kFold == 0;
-            const uint32_t v = base + C::kVs + vs * C::kTileBytes;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) {
-              if (k >= steps) break;
-              const uint64_t b = smem_desc(v + k * 2 * C::kGroup, 1024, C::kGroup);
-              mma_ts(tO, tS + 16 * k, b, kO, !(first && k == 0));
-              mma_ts(tO, tS + 16 * k + 8, b, kO, true);
+            uint64_t v = smem_desc(base + C::kVs + vs * C::kTileBytes, 1024, C::kGroup);
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k, v += 2 * C::kGroup / 16) {
+              mma_ts(tO, tS + 16 * k, v, kO, !(first && k == 0));
+              mma_ts(tO, tS + 16 * k + 8, v, kO, true);
             }
           }
           mma_commit(v_empty + 8 * vs);
@@ -674,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // unless a wait ran out.
   if (*abort) {
     if (tid == 0) {
+      atomicOr(p.status, KVX_DEV_TIMEOUT);
       // bounded: bulk loads land within microseconds of their issue
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 20000000ull) {

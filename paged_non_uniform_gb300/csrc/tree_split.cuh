@@ -24,9 +24,9 @@
 
 namespace kvx {
 
-// Measured with the tensor-core kernel on 256 sequences of 100 to 1000 tokens / 16 of 2k to
-// 32k with trees of up to 48 tokens: an item charged as 3 fifths of a tile 119 / 179 us,
-// 5: 119 / 175, 7: 120.5 / 173, 9: 122.5 / 174; without a charge the first took 130.
+// Measured with the tensor-core kernel on 256 sequences of 100 to 1000 tokens / 32 of 1k to
+// 32k with trees of up to 48 tokens: an item charged as 4 fifths of a tile 101.4 / 176 us,
+// 6: 102 / 175, 8: 104.6 / 174; an earlier form without a charge took 130 instead of 117.
 constexpr int kTileCost = 5;
 constexpr int kItemCost = 6;
 
