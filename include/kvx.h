@@ -671,6 +671,8 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  * negative, descending or past max_rows, or whose kv_len is negative or
  * does not fit its page table together with its new rows, is treated as
  * having no new rows, and KVX_DEV_BAD_LENGTH is set.
+ * The device of the cache's memory has to be the current one (addresses do not
+ * tell the library; the Python binding checks its tensors).
  * Launch: one kernel each (kvx_tree_attn: two, the second folds heads that were
  * cut over blocks), a programmatic dependent of the kernel before it on the
  * stream that waits for that kernel before it reads or writes anything. All may

@@ -515,27 +515,30 @@ class Frame:
 # ---------------------------------------------------------------------------
 # Speculative-decoding step (cache calls)
 
-def _dense(x, what: str, itemsize: int, count: int = 0):
-    """Address of a dense device array: integer addresses pass, tensors must be
-    contiguous, of the given item size and hold at least `count` items."""
+def _dense(cache, x, what: str, itemsize: int, count: int = 0):
+    """Address of a dense device array: integer addresses pass (and None, where nothing is
+    needed), tensors must be contiguous, of the given item size, on the cache's device, and
+    hold at least `count` items."""
     try:
         if x.is_cuda and x.is_contiguous() and x.element_size() == itemsize \
-                and x.numel() >= count:
+                and x.numel() >= count and cache.device in (None, x.get_device()):
             return x.data_ptr()
     except AttributeError:
-        if isinstance(x, int):
+        if isinstance(x, int) or (x is None and count == 0):
             return x
     raise KvxError(f"{what}: not a dense device array of {count} {itemsize}-byte items",
                    KVX_EINVAL)
 
 
-def _rows(x, what: str, itemsize: int, width: int, max_rows: int):
+def _rows(cache, x, what: str, width: int, max_rows: int):
     """(address, row stride in elements) of [max_rows] rows of `width` elements:
     a tensor [rows][width] or [rows][heads][D] whose rows are dense, a row
     stride apart; for an integer address, the rows are dense."""
-    if isinstance(x, int):
+    if isinstance(x, int) or (x is None and max_rows == 0):
         return x, width
-    if x is not None and x.is_cuda and x.element_size() == itemsize:
+    itemsize = cache.item
+    if x is not None and x.is_cuda and x.element_size() == itemsize \
+            and cache.device in (None, x.get_device()):
         size, stride = x.shape, x.stride()
         n = len(size)
         if n == 2:
@@ -551,6 +554,14 @@ def _rows(x, what: str, itemsize: int, width: int, max_rows: int):
                    KVX_EINVAL)
 
 
+def _on_device(cache) -> None:
+    """Refuses a call while another device than the cache's is current: the launch would go
+    there."""
+    if cache.device is not None and cache.current_device() != cache.device:
+        raise KvxError(f"the cache is on device {cache.device}, which is not the current one",
+                       KVX_EINVAL)
+
+
 def _nbytes(workspace, nbytes):
     if nbytes is None:
         return workspace.numel() * workspace.element_size()
@@ -560,7 +571,8 @@ def _nbytes(workspace, nbytes):
 class Cache:
     """Owner of one kvx_cache handle (kvx_cache_create): the shape, head groups,
     pools and page tables of a paged cache. Keeps the tensors it was given
-    alive."""
+    alive. Calls with it are refused while another device than theirs is current,
+    and for tensors of another device."""
 
     def __init__(self, B, Hq, Hkv, D, page_size, num_groups, dtype, head_group, k_pools, v_pools,
                  pool_pages, page_tables, page_table_stride, layout=KVX_LAYOUT_HEAD_MAJOR):
@@ -572,12 +584,23 @@ class Cache:
         if hg.size != Hkv or any(len(x) != num_groups
                                  for x in (k_pools, v_pools, page_tables, pp, ps)):
             raise KvxError("kvx_cache_create: array lengths", KVX_EINVAL)
+        self._find_device([*k_pools, *v_pools, *page_tables])
         h = _vp()
         _check(lib.kvx_cache_create(_c.byref(self.shape), hg.ctypes.data, _ptr_array(k_pools),
                                     _ptr_array(v_pools), pp.ctypes.data, _ptr_array(page_tables),
                                     ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
         self.handle = h.value
         self._keep = (list(k_pools), list(v_pools), list(page_tables))
+
+    def _find_device(self, arrays) -> None:
+        self.device = None  # of the tensors given; None for addresses
+        devices = {x.get_device() for x in arrays if x is not None and not isinstance(x, int)}
+        if devices:
+            import torch
+            self.current_device = torch._C._cuda_getDevice
+            self.device = devices.pop()
+        if devices or self.device == -1:
+            raise KvxError("kvx_cache_create: tensors on several devices or on none", KVX_EINVAL)
 
     def inject_stall(self, block: int, wait_limit_ns: int) -> None:
         """Failure-detection test hook: see kvx_cache_inject_stall."""
@@ -599,28 +622,33 @@ class Cache:
 def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pages, free_in,
                      free_out, max_rows, q_start, slots, workspace, workspace_bytes=None,
                      stream=None) -> None:
+    _on_device(cache)
     s = cache.shape
     B, G, n = s.B, s.num_groups, int(max_rows)
     if len(free_pages) != G:
         raise KvxError("kvx_build_tables: one free list per head group", KVX_EINVAL)
     rc = lib.kvx_build_tables(
-        cache.handle, _dense(kv_len, "kv_len", 4, B * s.Hkv), _dense(new_len, "new_len", 4, B),
-        _dense(pages_in, "pages_in", 4, G * B), _dense(pages_out, "pages_out", 4, G * B),
-        _ptr_array(free_pages), _dense(free_in, "free_in", 4, G),
-        _dense(free_out, "free_out", 4, G), n, _dense(q_start, "q_start", 4, B + 1),
-        _dense(slots, "slots", 8, n * s.Hkv), _dptr(workspace),
+        cache.handle, _dense(cache, kv_len, "kv_len", 4, B * s.Hkv),
+        _dense(cache, new_len, "new_len", 4, B), _dense(cache, pages_in, "pages_in", 4, G * B),
+        _dense(cache, pages_out, "pages_out", 4, G * B),
+        _ptr_array([_dense(cache, f, "free_pages", 4) for f in free_pages]),
+        _dense(cache, free_in, "free_in", 4, G),
+        _dense(cache, free_out, "free_out", 4, G), n, _dense(cache, q_start, "q_start", 4, B + 1),
+        _dense(cache, slots, "slots", 8, n * s.Hkv), _dptr(workspace),
         _nbytes(workspace, workspace_bytes), _stream(stream))
     _check(rc, "kvx_build_tables")
 
 
 def kvx_append_kv(cache: Cache, k_new, v_new, q_start, slots, max_rows, workspace,
                   workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
     s = cache.shape
     n = int(max_rows)
-    k, ks = _rows(k_new, "k_new", cache.item, s.Hkv * s.D, n)
-    v, vs = _rows(v_new, "v_new", cache.item, s.Hkv * s.D, n)
-    rc = lib.kvx_append_kv(cache.handle, k, ks, v, vs, _dense(q_start, "q_start", 4, s.B + 1),
-                           _dense(slots, "slots", 8, n * s.Hkv), n, _dptr(workspace),
+    k, ks = _rows(cache, k_new, "k_new", s.Hkv * s.D, n)
+    v, vs = _rows(cache, v_new, "v_new", s.Hkv * s.D, n)
+    rc = lib.kvx_append_kv(cache.handle, k, ks, v, vs,
+                           _dense(cache, q_start, "q_start", 4, s.B + 1),
+                           _dense(cache, slots, "slots", 8, n * s.Hkv), n, _dptr(workspace),
                            _nbytes(workspace, workspace_bytes), _stream(stream))
     _check(rc, "kvx_append_kv")
 
@@ -634,28 +662,31 @@ def kvx_tree_attn_workspace_bytes(cache: Cache, max_q: int) -> int:
 
 def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale, out, workspace,
                   workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
     s = cache.shape
     n, T = int(max_rows), int(max_q)
-    qp, qs = _rows(q, "q", cache.item, s.Hq * s.D, n)
-    mp = None if mask is None else _dense(mask, "mask", 4, n * ((T + 31) // 32))
-    rc = lib.kvx_tree_attn(cache.handle, qp, qs, _dense(q_start, "q_start", 4, s.B + 1), n, T,
-                           _dense(kv_len, "kv_len", 4, s.B * s.Hkv), mp, float(scale),
-                           _dense(out, "out", 4, n * s.Hq * s.D), _dptr(workspace),
+    qp, qs = _rows(cache, q, "q", s.Hq * s.D, n)
+    mp = None if mask is None else _dense(cache, mask, "mask", 4, n * ((T + 31) // 32))
+    rc = lib.kvx_tree_attn(cache.handle, qp, qs,
+                           _dense(cache, q_start, "q_start", 4, s.B + 1), n, T,
+                           _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv), mp, float(scale),
+                           _dense(cache, out, "out", 4, n * s.Hq * s.D), _dptr(workspace),
                            _nbytes(workspace, workspace_bytes), _stream(stream))
     _check(rc, "kvx_tree_attn")
 
 
 def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len, kv_len_out,
                     workspace, path_stride=None, workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
     s = cache.shape
     n = int(max_rows)
     if path_stride is None:
         path_stride = path.shape[1]
     rc = lib.kvx_tree_commit(
-        cache.handle, _dense(q_start, "q_start", 4, s.B + 1),
-        _dense(slots, "slots", 8, n * s.Hkv), n,
-        _dense(path, "path", 4, s.B * int(path_stride)), int(path_stride),
-        _dense(n_acc, "n_acc", 4, s.B), _dense(kv_len, "kv_len", 4, s.B * s.Hkv),
-        _dense(kv_len_out, "kv_len_out", 4, s.B * s.Hkv), _dptr(workspace),
+        cache.handle, _dense(cache, q_start, "q_start", 4, s.B + 1),
+        _dense(cache, slots, "slots", 8, n * s.Hkv), n,
+        _dense(cache, path, "path", 4, s.B * int(path_stride)), int(path_stride),
+        _dense(cache, n_acc, "n_acc", 4, s.B), _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv),
+        _dense(cache, kv_len_out, "kv_len_out", 4, s.B * s.Hkv), _dptr(workspace),
         _nbytes(workspace, workspace_bytes), _stream(stream))
     _check(rc, "kvx_tree_commit")

@@ -143,3 +143,53 @@ def test_inject_stall_refusals(kvx):
     c.inject_stall(-1, 2_000_000_000)
     c.destroy()
     refused(kvx, kvx.KVX_EINVAL, c.inject_stall, 0, 1_000_000)
+
+
+class OnDevice:
+    """Stands in for a dense tensor on a device of the given index."""
+    is_cuda = True
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def element_size(self):
+        return 4
+
+    def numel(self):
+        return 1 << 20
+
+    def data_ptr(self):
+        return A
+
+
+def test_tensors_of_another_device_are_refused(kvx):
+    pytest.importorskip("torch")
+    E = kvx.KVX_EINVAL
+    refused(kvx, E, make, kvx, kp=[OnDevice(0), OnDevice(1)])
+    refused(kvx, E, make, kvx, kp=[OnDevice(-1), A])
+    c = make(kvx, kp=[OnDevice(1), A], tables=[A, OnDevice(1)])
+    c.current_device = lambda: 0  # another device is current
+    refused(kvx, E, kvx.kvx_build_tables, c, **TABLES)
+    refused(kvx, E, kvx.kvx_append_kv, c, **APPEND)
+    refused(kvx, E, kvx.kvx_tree_attn, c, **TREE)
+    refused(kvx, E, kvx.kvx_tree_commit, c, **COMMIT)
+    c.current_device = lambda: 1
+    for key in ("kv_len", "q_start", "free_in", "pages_out"):
+        refused(kvx, E, kvx.kvx_build_tables, c, **{**TABLES, key: OnDevice(0)})
+    refused(kvx, E, kvx.kvx_build_tables, c, **{**TABLES, "free_pages": [A, OnDevice(0)]})
+    refused(kvx, E, kvx.kvx_tree_commit, c, **{**COMMIT, "path": OnDevice(0)})
+    refused(kvx, E, kvx.kvx_tree_attn, c, **{**TREE, "mask": OnDevice(0)})
+    c.destroy()
+
+
+def test_no_rows_need_no_row_arrays(kvx):
+    c = make(kvx)
+    kvx.kvx_append_kv(c, None, None, A, None, 0, A, 256, 0)
+    refused(kvx, kvx.KVX_EINVAL, kvx.kvx_append_kv, c, None, None, A, None, 1, A, 256, 0)
+    c.destroy()
