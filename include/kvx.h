@@ -275,14 +275,17 @@ int kvx_plan_inject_stall(kvx_plan *plan, int32_t block, uint64_t wait_limit_ns)
  * stage that holds a head's newest page (the page of its last kept token),
  * and waits before anything else. q, seq_len and head_budget are still read
  * after the wait, and the L2 warm-up of short launches is skipped.
- * Precondition: if the kernel before the call lets its dependents start early
- * (programmatic dependent launch), it writes none of the page-table entries
- * or K/V pages the call reads, except each head's newest page and that page's
- * page-table entry (the load warp reads the entries again after the wait and
- * loads the newest page only then). An ordinary
- * kernel lets its dependents start only when it has completed, so any kernel
- * qualifies that does not use programmatic launch; so do the library's own
- * kernels, none of which write pages or page tables while a dependent may run.
+ * Precondition: a kernel that may still run when the call starts writes none
+ * of the page-table entries or K/V pages the call reads, except each head's
+ * newest page and that page's page-table entry (the load warp reads the
+ * entries again after the wait and loads the newest page only then). That can
+ * be the kernel before the call, if it lets its dependents start early
+ * (programmatic dependent launch), and one further back, if every kernel from
+ * it on does. An ordinary kernel lets its dependents start only when it has
+ * completed, so any kernel qualifies that does not use programmatic launch; so
+ * do the library's own kernels, in any order: those that write pages or page
+ * tables (kvx_append_kv, kvx_tree_commit, kvx_build_tables, kvx_pack_kept) let
+ * their dependents start only when all of it is written.
  * enable: 0 or 1. Errors: KVX_EINVAL. */
 int kvx_plan_set_early_kv(kvx_plan *plan, int32_t enable);
 
@@ -675,8 +678,11 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  * tell the library; the Python binding checks its tensors).
  * Launch: one kernel each (kvx_tree_attn: two, the second folds heads that were
  * cut over blocks), a programmatic dependent of the kernel before it on the
- * stream that waits for that kernel before it reads or writes anything. All may
- * be captured into a CUDA graph, also as their first call.
+ * stream that waits for that kernel before it reads or writes anything. The three
+ * calls that write pages or page tables let their own dependents start only when
+ * they have written everything, so that kvx_decode_attn with early K/V loads may
+ * follow any of them. All may be captured into a CUDA graph, also as their first
+ * call.
  * ------------------------------------------------------------------------- */
 typedef struct kvx_cache kvx_cache;
 

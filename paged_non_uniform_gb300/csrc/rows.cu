@@ -19,7 +19,6 @@ __device__ __forceinline__ int64_t pool_rows(const CacheDev &c, int grp) {
 // pool[slots[r][h]] = new[r][h] for K and V. One thread per 16-byte chunk of a
 // (row, head), K and V together.
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  pdl_launch_dependents();
   pdl_wait();
   const CacheDev &c = p.c;
   const int cpr = c.row_bytes >> 4;  // chunks of a row: 8, 16 or 32
@@ -45,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     *(uint4 *)(c.grp[grp].k + dst) = kv;
     *(uint4 *)(c.grp[grp].v + dst) = vv;
   }
+  __threadfence();
 }
 
 // row n + j <- row n + path[j]. One thread owns one 16-byte column of K or V of
@@ -53,7 +53,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 // eight loads therefore may precede its eight stores, and no thread reads what
 // another writes.
 __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitParams p) {
-  pdl_launch_dependents();
   pdl_wait();
   const CacheDev &c = p.c;
   const int b = blockIdx.y;
@@ -110,6 +109,7 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
     for (int u = 0; u < 8; ++u)
       if (to[u] >= 0) *(uint4 *)(pool + to[u] * c.row_bytes) = v[u];
   }
+  __threadfence();
 }
 
 cudaLaunchConfig_t config(dim3 grid, cudaStream_t st, cudaLaunchAttribute *attr) {

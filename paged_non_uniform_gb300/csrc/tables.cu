@@ -14,6 +14,8 @@
 // in its owner's table through the sums instead of the list, so no block waits
 // for another. Table entries below `have` are never written, list entries below F
 // neither, which is what makes a repeated call give the same result.
+// Dependents start only when the tables are written (no early trigger, and a fence at
+// the end): a decode call with early loads reads page ids before its dependency wait.
 // Measured on one GB300: a verify step (16 sequences, 3 groups) 6.5 us, all latency: two
 // passes of loads, the sums and their scan; 256 prompts (1.17 M rows, 9.4 M slots of 8
 // bytes) 21 us, of which a plain fill with the slots' 75 MB would take 10 and the sums,
@@ -93,7 +95,6 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   __shared__ int free_in[KVX_MAX_GROUPS];
   __shared__ int8_t heads[KVX_MAX_KV_HEADS];  // heads by group
   __shared__ int head_off[KVX_MAX_GROUPS + 1];
-  pdl_launch_dependents();
   const CacheDev &c = p.c;
   const int B = c.B, G = c.G, Hkv = c.Hkv, P = c.P, lgP = c.lgP, tid = threadIdx.x;
   const int own = blockIdx.y;  // this block's group
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
       out += out_step;
     }
   }
+  __threadfence();
 }
 
 }  // namespace

@@ -1,0 +1,28 @@
+"""Rules of the cache kernels' sources that a run cannot show to be broken without a race."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_non_uniform_gb300",
+                    "csrc")
+
+
+def kernels(name):
+    """{kernel name: its source} of a file: from its __global__ to the next closing brace in column 0."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    return {re.search(r"(\w+)\(const __grid_constant__", part).group(1): part[:part.index("\n}\n")]
+            for part in text.split("__global__")[1:]}
+
+
+@pytest.mark.parametrize("source,names", [("rows.cu", {"append_kernel", "commit_kernel"}),
+                                          ("tables.cu", {"tables_kernel"})])
+def test_page_writers_hold_their_dependents_back(source, names):
+    """A decode call with early loads reads pages and page tables before its dependency wait. Kernels
+    that write them must neither release their dependents early nor finish before their writes are
+    performed."""
+    found = kernels(source)
+    assert set(found) == names
+    for name, body in found.items():
+        assert "pdl_launch_dependents" not in body, name
+        assert body.rstrip().endswith("__threadfence();"), name
