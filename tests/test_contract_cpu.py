@@ -1,0 +1,36 @@
+"""Limits that the header states, against the library (host calls only)."""
+import os
+import re
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def kvx():
+    from paged_non_uniform_gb300 import build
+    build.build()
+    from paged_non_uniform_gb300 import kvx as k
+    return k
+
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "kvx.h")
+
+
+def comment_of(function):
+    """The header's comment before a function's declaration, as one line."""
+    text = open(HEADER).read()
+    text = text[:text.index(f"\nint {function}(")]
+    return " ".join(re.sub(r"\n \* ?", "\n", text[text.rindex("/*"):]).split())
+
+
+def test_stated_stall_limits_are_the_accepted_ones(kvx):
+    """1 ms up to the stated number of seconds is accepted, a nanosecond more or less is not."""
+    plan = kvx.kvx_plan_create(1, 4, 1, 128, 16, 1, kvx.KVX_BF16, [[64]], [64], [0])
+    cache = kvx.Cache(1, 4, 1, 128, 16, 1, kvx.KVX_BF16, [0], [1 << 20], [1 << 20], [9], [1 << 20], [4])
+    for function, handle in (("kvx_plan_inject_stall", plan.handle), ("kvx_cache_inject_stall", cache.handle)):
+        most = int(re.search(r"\(1 ms \.\. (\d+) s", comment_of(function)).group(1)) * 10 ** 9
+        call = getattr(kvx.lib, function)
+        for ns in (10 ** 6, most):
+            assert call(handle, -1, ns) == kvx.KVX_OK, (function, ns)
+        for ns in (10 ** 6 - 1, most + 1):
+            assert call(handle, -1, ns) == kvx.KVX_ERANGE, (function, ns)
