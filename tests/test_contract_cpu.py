@@ -25,7 +25,7 @@ def comment_of(function):
 
 def test_stated_stall_limits_are_the_accepted_ones(kvx):
     """1 ms up to the stated number of seconds is accepted, a nanosecond more or less is not."""
-    plan = kvx.kvx_plan_create(1, 4, 1, 128, 16, 1, kvx.KVX_BF16, [[64]], [64], [0])
+    plan = kvx.kvx_plan_create(1, 4, 1, 128, 16, 1, kvx.KVX_BF16, [[64]], [64], [0], num_ctas=4)
     cache = kvx.Cache(1, 4, 1, 128, 16, 1, kvx.KVX_BF16, [0], [1 << 20], [1 << 20], [9], [1 << 20], [4])
     for function, handle in (("kvx_plan_inject_stall", plan.handle), ("kvx_cache_inject_stall", cache.handle)):
         most = int(re.search(r"\(1 ms \.\. (\d+) s", comment_of(function)).group(1)) * 10 ** 9
