@@ -562,10 +562,20 @@ def _on_device(cache) -> None:
                        KVX_EINVAL)
 
 
-def _nbytes(workspace, nbytes):
-    if nbytes is None:
-        return workspace.numel() * workspace.element_size()
-    return int(nbytes)
+def _workspace(cache, x, nbytes):
+    """(address, bytes) of a call's workspace: a dense tensor on the cache's device (`nbytes`, where
+    given, is at most its size), or an integer address of `nbytes` bytes."""
+    try:
+        if x.is_cuda and x.is_contiguous() and cache.device in (None, x.get_device()):
+            have = x.numel() * x.element_size()
+            if nbytes is None:
+                return x.data_ptr(), have
+            if 0 <= nbytes <= have:
+                return x.data_ptr(), int(nbytes)
+    except AttributeError:
+        if isinstance(x, int) and nbytes is not None and nbytes >= 0:
+            return x, int(nbytes)
+    raise KvxError("workspace: not a dense device array of its size on the cache's device", KVX_EINVAL)
 
 
 class Cache:
@@ -625,6 +635,7 @@ def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pa
     _on_device(cache)
     s = cache.shape
     B, G, n = s.B, s.num_groups, int(max_rows)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
     if len(free_pages) != G:
         raise KvxError("kvx_build_tables: one free list per head group", KVX_EINVAL)
     rc = lib.kvx_build_tables(
@@ -634,8 +645,7 @@ def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pa
         _ptr_array([_dense(cache, f, "free_pages", 4) for f in free_pages]),
         _dense(cache, free_in, "free_in", 4, G),
         _dense(cache, free_out, "free_out", 4, G), n, _dense(cache, q_start, "q_start", 4, B + 1),
-        _dense(cache, slots, "slots", 8, n * s.Hkv), _dptr(workspace),
-        _nbytes(workspace, workspace_bytes), _stream(stream))
+        _dense(cache, slots, "slots", 8, n * s.Hkv), wp, wb, _stream(stream))
     _check(rc, "kvx_build_tables")
 
 
@@ -646,10 +656,10 @@ def kvx_append_kv(cache: Cache, k_new, v_new, q_start, slots, max_rows, workspac
     n = int(max_rows)
     k, ks = _rows(cache, k_new, "k_new", s.Hkv * s.D, n)
     v, vs = _rows(cache, v_new, "v_new", s.Hkv * s.D, n)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
     rc = lib.kvx_append_kv(cache.handle, k, ks, v, vs,
                            _dense(cache, q_start, "q_start", 4, s.B + 1),
-                           _dense(cache, slots, "slots", 8, n * s.Hkv), n, _dptr(workspace),
-                           _nbytes(workspace, workspace_bytes), _stream(stream))
+                           _dense(cache, slots, "slots", 8, n * s.Hkv), n, wp, wb, _stream(stream))
     _check(rc, "kvx_append_kv")
 
 
@@ -666,12 +676,12 @@ def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale
     s = cache.shape
     n, T = int(max_rows), int(max_q)
     qp, qs = _rows(cache, q, "q", s.Hq * s.D, n)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
     mp = None if mask is None else _dense(cache, mask, "mask", 4, n * ((T + 31) // 32))
     rc = lib.kvx_tree_attn(cache.handle, qp, qs,
                            _dense(cache, q_start, "q_start", 4, s.B + 1), n, T,
                            _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv), mp, float(scale),
-                           _dense(cache, out, "out", 4, n * s.Hq * s.D), _dptr(workspace),
-                           _nbytes(workspace, workspace_bytes), _stream(stream))
+                           _dense(cache, out, "out", 4, n * s.Hq * s.D), wp, wb, _stream(stream))
     _check(rc, "kvx_tree_attn")
 
 
@@ -680,6 +690,7 @@ def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len,
     _on_device(cache)
     s = cache.shape
     n = int(max_rows)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
     if path_stride is None:
         path_stride = path.shape[1]
     rc = lib.kvx_tree_commit(
@@ -687,6 +698,5 @@ def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len,
         _dense(cache, slots, "slots", 8, n * s.Hkv), n,
         _dense(cache, path, "path", 4, s.B * int(path_stride)), int(path_stride),
         _dense(cache, n_acc, "n_acc", 4, s.B), _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv),
-        _dense(cache, kv_len_out, "kv_len_out", 4, s.B * s.Hkv), _dptr(workspace),
-        _nbytes(workspace, workspace_bytes), _stream(stream))
+        _dense(cache, kv_len_out, "kv_len_out", 4, s.B * s.Hkv), wp, wb, _stream(stream))
     _check(rc, "kvx_tree_commit")

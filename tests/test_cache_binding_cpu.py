@@ -1,0 +1,67 @@
+"""What the binding's cache calls check of the arrays that they are given. Stand-ins for device
+tensors serve, and no call passes every check, so nothing is launched."""
+import pytest
+
+from test_cache_cpu import A, APPEND, COMMIT, TABLES, TREE, kvx, make, refused  # noqa: F401
+
+torch = pytest.importorskip("torch")
+
+CALLS = [("kvx_build_tables", TABLES), ("kvx_append_kv", APPEND), ("kvx_tree_attn", TREE),
+         ("kvx_tree_commit", COMMIT)]
+
+
+class Dev:
+    """Stands in for a device tensor."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.int32, device=1, contiguous=True):
+        self.shape, self.dtype, self.device, self.dense = shape, dtype, device, contiguous
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return self.dense
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def numel(self):
+        n = 1
+        for x in self.shape:
+            n *= x
+        return n
+
+    def stride(self):
+        out = [1]
+        for x in self.shape[:0:-1]:
+            out.insert(0, out[0] * x)
+        return tuple(out)
+
+    def data_ptr(self):
+        return A
+
+
+def on_device_1(kvx, **change):
+    """A cache on device 1, which is current. Its tables and pools fit make()'s shape."""
+    pool = dict(dtype=torch.bfloat16)
+    c = make(kvx, **{**dict(kp=[Dev(9 * 16, 64, **pool)] * 2, vp=[Dev(9 * 16, 64, **pool)] * 2,
+                            tables=[Dev(2, 4)] * 2), **change})
+    c.current_device = lambda: 1
+    return c
+
+
+@pytest.mark.parametrize("name,good", CALLS)
+def test_workspace_is_checked(kvx, name, good):
+    """On the cache's device, dense, and no smaller than it is said to be."""
+    c, call = on_device_1(kvx), getattr(kvx, name)
+    for bad in (Dev(1 << 20, device=0), Dev(1 << 20, contiguous=False), torch.zeros(1 << 10), None, "ws"):
+        for nbytes in (None, 256):
+            refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "workspace": bad, "workspace_bytes": nbytes})
+    for nbytes in (257, -1):
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "workspace": Dev(64), "workspace_bytes": nbytes})
+    refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "workspace": A, "workspace_bytes": None})
+    refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "workspace": A, "workspace_bytes": -1})
+    assert kvx._workspace(c, Dev(64), None) == (A, 256)
+    assert kvx._workspace(c, Dev(64), 255) == (A, 255)
+    assert kvx._workspace(c, A, 1 << 40) == (A, 1 << 40)
