@@ -600,6 +600,7 @@ class Cache:
                                     _ptr_array(v_pools), pp.ctypes.data, _ptr_array(page_tables),
                                     ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
         self.handle = h.value
+        self.pool_pages = pp.tolist()
         self._keep = (list(k_pools), list(v_pools), list(page_tables))
 
     def _find_device(self, arrays) -> None:
@@ -642,7 +643,8 @@ def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pa
         cache.handle, _dense(cache, kv_len, "kv_len", 4, B * s.Hkv),
         _dense(cache, new_len, "new_len", 4, B), _dense(cache, pages_in, "pages_in", 4, G * B),
         _dense(cache, pages_out, "pages_out", 4, G * B),
-        _ptr_array([_dense(cache, f, "free_pages", 4) for f in free_pages]),
+        _ptr_array([_dense(cache, f, "free_pages", 4, n)
+                    for f, n in zip(free_pages, cache.pool_pages)]),
         _dense(cache, free_in, "free_in", 4, G),
         _dense(cache, free_out, "free_out", 4, G), n, _dense(cache, q_start, "q_start", 4, B + 1),
         _dense(cache, slots, "slots", 8, n * s.Hkv), wp, wb, _stream(stream))

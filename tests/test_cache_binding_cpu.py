@@ -65,3 +65,11 @@ def test_workspace_is_checked(kvx, name, good):
     assert kvx._workspace(c, Dev(64), None) == (A, 256)
     assert kvx._workspace(c, Dev(64), 255) == (A, 255)
     assert kvx._workspace(c, A, 1 << 40) == (A, 1 << 40)
+
+
+def test_free_lists_hold_the_whole_pool(kvx):
+    """The call may push every page: a list with room for fewer ids than the pool has pages is refused."""
+    c = on_device_1(kvx, pages=(9, 12), kp=[A, A], vp=[A, A])
+    good = {**TABLES, "workspace": Dev(64), "workspace_bytes": None}
+    for lists in ([Dev(8), Dev(12)], [Dev(9), Dev(11)], [Dev(9), None], [Dev(9, device=0), Dev(12)]):
+        refused(kvx, kvx.KVX_EINVAL, kvx.kvx_build_tables, c, **{**good, "free_pages": lists})
