@@ -515,29 +515,39 @@ class Frame:
 # ---------------------------------------------------------------------------
 # Speculative-decoding step (cache calls)
 
-def _dense(cache, x, what: str, itemsize: int, count: int = 0):
+_kind_names: dict = {}
+
+
+def _kind(dtype) -> str:
+    """What a tensor's elements are to the library: signed and unsigned integers of a size alike."""
+    name = _kind_names.get(dtype)
+    if name is None:
+        name = str(dtype).removeprefix("torch.").removeprefix("u")
+        _kind_names[dtype] = name
+    return name
+
+
+def _dense(cache, x, what: str, kind: str, count: int = 0):
     """Address of a dense device array: integer addresses pass (and None, where nothing is
-    needed), tensors must be contiguous, of the given item size, on the cache's device, and
-    hold at least `count` items."""
+    needed), tensors must be contiguous, of the given element type, on the cache's device, and
+    hold at least `count` elements."""
     try:
-        if x.is_cuda and x.is_contiguous() and x.element_size() == itemsize \
+        if x.is_cuda and x.is_contiguous() and _kind(x.dtype) == kind \
                 and x.numel() >= count and cache.device in (None, x.get_device()):
             return x.data_ptr()
     except AttributeError:
         if isinstance(x, int) or (x is None and count == 0):
             return x
-    raise KvxError(f"{what}: not a dense device array of {count} {itemsize}-byte items",
-                   KVX_EINVAL)
+    raise KvxError(f"{what}: not a dense device array of {count} {kind} elements", KVX_EINVAL)
 
 
 def _rows(cache, x, what: str, width: int, max_rows: int):
-    """(address, row stride in elements) of [max_rows] rows of `width` elements:
-    a tensor [rows][width] or [rows][heads][D] whose rows are dense, a row
+    """(address, row stride in elements) of [max_rows] rows of `width` elements of the cache's
+    type: a tensor [rows][width] or [rows][heads][D] whose rows are dense, a row
     stride apart; for an integer address, the rows are dense."""
     if isinstance(x, int) or (x is None and max_rows == 0):
         return x, width
-    itemsize = cache.item
-    if x is not None and x.is_cuda and x.element_size() == itemsize \
+    if x is not None and x.is_cuda and _kind(x.dtype) == cache.kind \
             and cache.device in (None, x.get_device()):
         size, stride = x.shape, x.stride()
         n = len(size)
@@ -550,8 +560,7 @@ def _rows(cache, x, what: str, width: int, max_rows: int):
             ok = False
         if ok and size[0] >= max_rows:
             return x.data_ptr(), (stride[0] if size[0] > 1 else width)
-    raise KvxError(f"{what}: not {max_rows} device rows of {width} {itemsize}-byte items",
-                   KVX_EINVAL)
+    raise KvxError(f"{what}: not {max_rows} device rows of {width} {cache.kind} elements", KVX_EINVAL)
 
 
 def _on_device(cache) -> None:
@@ -588,7 +597,7 @@ class Cache:
                  pool_pages, page_tables, page_table_stride, layout=KVX_LAYOUT_HEAD_MAJOR):
         self.handle = None
         self.shape = kvx_shape(B, Hq, Hkv, D, page_size, num_groups, dtype, layout)
-        self.item = 2 if dtype == KVX_BF16 else 4
+        self.kind = "bfloat16" if dtype == KVX_BF16 else "float32"
         hg, ps = _i32(head_group), _i32(page_table_stride)
         pp = np.ascontiguousarray(np.asarray(pool_pages, dtype=np.int64))
         if hg.size != Hkv or any(len(x) != num_groups
@@ -640,14 +649,16 @@ def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pa
     if len(free_pages) != G:
         raise KvxError("kvx_build_tables: one free list per head group", KVX_EINVAL)
     rc = lib.kvx_build_tables(
-        cache.handle, _dense(cache, kv_len, "kv_len", 4, B * s.Hkv),
-        _dense(cache, new_len, "new_len", 4, B), _dense(cache, pages_in, "pages_in", 4, G * B),
-        _dense(cache, pages_out, "pages_out", 4, G * B),
-        _ptr_array([_dense(cache, f, "free_pages", 4, n)
+        cache.handle, _dense(cache, kv_len, "kv_len", "int32", B * s.Hkv),
+        _dense(cache, new_len, "new_len", "int32", B),
+        _dense(cache, pages_in, "pages_in", "int32", G * B),
+        _dense(cache, pages_out, "pages_out", "int32", G * B),
+        _ptr_array([_dense(cache, f, "free_pages", "int32", n)
                     for f, n in zip(free_pages, cache.pool_pages)]),
-        _dense(cache, free_in, "free_in", 4, G),
-        _dense(cache, free_out, "free_out", 4, G), n, _dense(cache, q_start, "q_start", 4, B + 1),
-        _dense(cache, slots, "slots", 8, n * s.Hkv), wp, wb, _stream(stream))
+        _dense(cache, free_in, "free_in", "int32", G),
+        _dense(cache, free_out, "free_out", "int32", G), n,
+        _dense(cache, q_start, "q_start", "int32", B + 1),
+        _dense(cache, slots, "slots", "int64", n * s.Hkv), wp, wb, _stream(stream))
     _check(rc, "kvx_build_tables")
 
 
@@ -660,8 +671,8 @@ def kvx_append_kv(cache: Cache, k_new, v_new, q_start, slots, max_rows, workspac
     v, vs = _rows(cache, v_new, "v_new", s.Hkv * s.D, n)
     wp, wb = _workspace(cache, workspace, workspace_bytes)
     rc = lib.kvx_append_kv(cache.handle, k, ks, v, vs,
-                           _dense(cache, q_start, "q_start", 4, s.B + 1),
-                           _dense(cache, slots, "slots", 8, n * s.Hkv), n, wp, wb, _stream(stream))
+                           _dense(cache, q_start, "q_start", "int32", s.B + 1),
+                           _dense(cache, slots, "slots", "int64", n * s.Hkv), n, wp, wb, _stream(stream))
     _check(rc, "kvx_append_kv")
 
 
@@ -679,11 +690,11 @@ def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale
     n, T = int(max_rows), int(max_q)
     qp, qs = _rows(cache, q, "q", s.Hq * s.D, n)
     wp, wb = _workspace(cache, workspace, workspace_bytes)
-    mp = None if mask is None else _dense(cache, mask, "mask", 4, n * ((T + 31) // 32))
+    mp = None if mask is None else _dense(cache, mask, "mask", "int32", n * ((T + 31) // 32))
     rc = lib.kvx_tree_attn(cache.handle, qp, qs,
-                           _dense(cache, q_start, "q_start", 4, s.B + 1), n, T,
-                           _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv), mp, float(scale),
-                           _dense(cache, out, "out", 4, n * s.Hq * s.D), wp, wb, _stream(stream))
+                           _dense(cache, q_start, "q_start", "int32", s.B + 1), n, T,
+                           _dense(cache, kv_len, "kv_len", "int32", s.B * s.Hkv), mp, float(scale),
+                           _dense(cache, out, "out", "float32", n * s.Hq * s.D), wp, wb, _stream(stream))
     _check(rc, "kvx_tree_attn")
 
 
@@ -696,9 +707,10 @@ def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len,
     if path_stride is None:
         path_stride = path.shape[1]
     rc = lib.kvx_tree_commit(
-        cache.handle, _dense(cache, q_start, "q_start", 4, s.B + 1),
-        _dense(cache, slots, "slots", 8, n * s.Hkv), n,
-        _dense(cache, path, "path", 4, s.B * int(path_stride)), int(path_stride),
-        _dense(cache, n_acc, "n_acc", 4, s.B), _dense(cache, kv_len, "kv_len", 4, s.B * s.Hkv),
-        _dense(cache, kv_len_out, "kv_len_out", 4, s.B * s.Hkv), wp, wb, _stream(stream))
+        cache.handle, _dense(cache, q_start, "q_start", "int32", s.B + 1),
+        _dense(cache, slots, "slots", "int64", n * s.Hkv), n,
+        _dense(cache, path, "path", "int32", s.B * int(path_stride)), int(path_stride),
+        _dense(cache, n_acc, "n_acc", "int32", s.B),
+        _dense(cache, kv_len, "kv_len", "int32", s.B * s.Hkv),
+        _dense(cache, kv_len_out, "kv_len_out", "int32", s.B * s.Hkv), wp, wb, _stream(stream))
     _check(rc, "kvx_tree_commit")

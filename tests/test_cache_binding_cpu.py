@@ -73,3 +73,39 @@ def test_free_lists_hold_the_whole_pool(kvx):
     good = {**TABLES, "workspace": Dev(64), "workspace_bytes": None}
     for lists in ([Dev(8), Dev(12)], [Dev(9), Dev(11)], [Dev(9), None], [Dev(9, device=0), Dev(12)]):
         refused(kvx, kvx.KVX_EINVAL, kvx.kvx_build_tables, c, **{**good, "free_pages": lists})
+
+
+INTS = {"kvx_build_tables": ["kv_len", "new_len", "pages_in", "pages_out", "free_in", "free_out", "q_start"],
+        "kvx_append_kv": ["q_start"], "kvx_tree_attn": ["q_start", "kv_len", "mask"],
+        "kvx_tree_commit": ["q_start", "path", "n_acc", "kv_len", "kv_len_out"]}
+
+
+@pytest.mark.parametrize("name,good", CALLS)
+def test_element_types_are_checked(kvx, name, good):
+    """An array of another type of the same size is refused: lengths and masks are integers, rows have the
+    cache's type, the output is fp32."""
+    c, call = on_device_1(kvx), getattr(kvx, name)
+    good = {**good, "workspace": Dev(1 << 20), "workspace_bytes": None}
+    for key in INTS[name]:
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, key: Dev(64, dtype=torch.float32)})
+    if name == "kvx_build_tables":
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "free_pages": [Dev(64, dtype=torch.float32)] * 2})
+    if "slots" in good:
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "slots": Dev(64, dtype=torch.float64)})
+    if name == "kvx_append_kv":
+        for key in ("k_new", "v_new"):
+            refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, key: Dev(4, 128, dtype=torch.float16)})
+    if name == "kvx_tree_attn":
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "q": Dev(4, 512, dtype=torch.int16)})
+        refused(kvx, kvx.KVX_EINVAL, call, c, **{**good, "out": Dev(4, 8, 64, dtype=torch.int32)})
+
+
+def test_accepted_element_types(kvx):
+    c = on_device_1(kvx)
+    for dtype, kind in ((torch.int32, "int32"), (torch.uint32, "int32"), (torch.int64, "int64"),
+                        (torch.float32, "float32")):
+        assert kvx._dense(c, Dev(64, dtype=dtype), "x", kind, 64) == A
+    assert kvx._rows(c, Dev(4, 2, 64, dtype=torch.bfloat16), "x", 128, 4) == (A, 128)
+    f = make(kvx, dtype=kvx.KVX_F32)
+    assert kvx._rows(f, Dev(4, 128, dtype=torch.float32), "x", 128, 4) == (A, 128)
+    refused(kvx, kvx.KVX_EINVAL, kvx._rows, f, Dev(4, 128, dtype=torch.bfloat16), "x", 128, 4)
