@@ -560,7 +560,8 @@ def _rows(cache, x, what: str, width: int, max_rows: int):
             ok = False
         if ok and size[0] >= max_rows:
             return x.data_ptr(), (stride[0] if size[0] > 1 else width)
-    raise KvxError(f"{what}: not {max_rows} device rows of {width} {cache.kind} elements", KVX_EINVAL)
+    raise KvxError(f"{what}: not {max_rows} device rows of {width} {cache.kind} elements",
+                   KVX_EINVAL)
 
 
 def _on_device(cache) -> None:
@@ -568,6 +569,14 @@ def _on_device(cache) -> None:
     there."""
     if cache.device is not None and cache.current_device() != cache.device:
         raise KvxError(f"the cache is on device {cache.device}, which is not the current one",
+                       KVX_EINVAL)
+
+
+def _check_pools(cache) -> None:
+    """Refuses a call that reads or writes pools whose tensors do not hold the pages that the cache
+    was given."""
+    if not cache.pools_fit:
+        raise KvxError("the cache's pools are not dense tensors of its type with pool_pages pages",
                        KVX_EINVAL)
 
 
@@ -584,14 +593,17 @@ def _workspace(cache, x, nbytes):
     except AttributeError:
         if isinstance(x, int) and nbytes is not None and nbytes >= 0:
             return x, int(nbytes)
-    raise KvxError("workspace: not a dense device array of its size on the cache's device", KVX_EINVAL)
+    raise KvxError("workspace: not a dense device array of its size on the cache's device",
+                   KVX_EINVAL)
 
 
 class Cache:
     """Owner of one kvx_cache handle (kvx_cache_create): the shape, head groups,
     pools and page tables of a paged cache. Keeps the tensors it was given
     alive. Calls with it are refused while another device than theirs is current,
-    and for tensors of another device."""
+    and for tensors of another device. Page-table tensors smaller than
+    [B][page_table_stride] are refused here, pool tensors that do not hold
+    pool_pages by the calls that touch them (kvx_build_tables does not)."""
 
     def __init__(self, B, Hq, Hkv, D, page_size, num_groups, dtype, head_group, k_pools, v_pools,
                  pool_pages, page_tables, page_table_stride, layout=KVX_LAYOUT_HEAD_MAJOR):
@@ -604,23 +616,45 @@ class Cache:
                                  for x in (k_pools, v_pools, page_tables, pp, ps)):
             raise KvxError("kvx_cache_create: array lengths", KVX_EINVAL)
         self._find_device([*k_pools, *v_pools, *page_tables])
+        for t, stride in zip(page_tables, ps.tolist()):
+            if not self._holds(t, 4 * B * stride, ("int32",)):
+                raise KvxError("kvx_cache_create: a page table is not a dense int32 tensor of "
+                               "[B][page_table_stride]", KVX_EINVAL)
         h = _vp()
         _check(lib.kvx_cache_create(_c.byref(self.shape), hg.ctypes.data, _ptr_array(k_pools),
                                     _ptr_array(v_pools), pp.ctypes.data, _ptr_array(page_tables),
                                     ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
         self.handle = h.value
         self.pool_pages = pp.tolist()
+        page = page_size * D * (2 if dtype == KVX_BF16 else 4)
+        size = np.bincount(hg, minlength=num_groups).tolist()
+        self.pools_fit = all(self._holds(x, n * z * page, (self.kind, "int8", "int16", "int32"))
+                             for pools in (k_pools, v_pools)
+                             for x, n, z in zip(pools, self.pool_pages, size))
         self._keep = (list(k_pools), list(v_pools), list(page_tables))
 
     def _find_device(self, arrays) -> None:
         self.device = None  # of the tensors given; None for addresses
-        devices = {x.get_device() for x in arrays if x is not None and not isinstance(x, int)}
+        try:
+            devices = {x.get_device() for x in arrays if x is not None and not isinstance(x, int)}
+        except AttributeError:
+            raise KvxError("kvx_cache_create: arrays are torch tensors or addresses",
+                           KVX_EINVAL) from None
         if devices:
             import torch
             self.current_device = torch._C._cuda_getDevice
             self.device = devices.pop()
         if devices or self.device == -1:
             raise KvxError("kvx_cache_create: tensors on several devices or on none", KVX_EINVAL)
+
+    @staticmethod
+    def _holds(x, nbytes: int, kinds) -> bool:
+        """Whether a tensor is dense, of one of the kinds (integers: raw storage) and large enough;
+        addresses are not looked into."""
+        if x is None or isinstance(x, int):
+            return True
+        return x.is_contiguous() and x.numel() * x.element_size() >= nbytes \
+            and (not hasattr(x, "dtype") or _kind(x.dtype) in kinds)
 
     def inject_stall(self, block: int, wait_limit_ns: int) -> None:
         """Failure-detection test hook: see kvx_cache_inject_stall."""
@@ -665,6 +699,7 @@ def kvx_build_tables(cache: Cache, kv_len, new_len, pages_in, pages_out, free_pa
 def kvx_append_kv(cache: Cache, k_new, v_new, q_start, slots, max_rows, workspace,
                   workspace_bytes=None, stream=None) -> None:
     _on_device(cache)
+    _check_pools(cache)
     s = cache.shape
     n = int(max_rows)
     k, ks = _rows(cache, k_new, "k_new", s.Hkv * s.D, n)
@@ -686,6 +721,7 @@ def kvx_tree_attn_workspace_bytes(cache: Cache, max_q: int) -> int:
 def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale, out, workspace,
                   workspace_bytes=None, stream=None) -> None:
     _on_device(cache)
+    _check_pools(cache)
     s = cache.shape
     n, T = int(max_rows), int(max_q)
     qp, qs = _rows(cache, q, "q", s.Hq * s.D, n)
@@ -701,6 +737,7 @@ def kvx_tree_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, mask, scale
 def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len, kv_len_out,
                     workspace, path_stride=None, workspace_bytes=None, stream=None) -> None:
     _on_device(cache)
+    _check_pools(cache)
     s = cache.shape
     n = int(max_rows)
     wp, wb = _workspace(cache, workspace, workspace_bytes)

@@ -109,3 +109,33 @@ def test_accepted_element_types(kvx):
     f = make(kvx, dtype=kvx.KVX_F32)
     assert kvx._rows(f, Dev(4, 128, dtype=torch.float32), "x", 128, 4) == (A, 128)
     refused(kvx, kvx.KVX_EINVAL, kvx._rows, f, Dev(4, 128, dtype=torch.bfloat16), "x", 128, 4)
+
+
+def test_page_tables_hold_their_strides(kvx):
+    for bad in (Dev(2, 3), Dev(7), Dev(2, 4, dtype=torch.float32), Dev(2, 4, contiguous=False)):
+        refused(kvx, kvx.KVX_EINVAL, on_device_1, kvx, tables=[Dev(2, 4), bad])
+    on_device_1(kvx, tables=[Dev(2, 4), Dev(9)]).destroy()
+
+
+@pytest.mark.parametrize("which", ["kp", "vp"])
+@pytest.mark.parametrize("dtype,right,wrong", [(1, torch.bfloat16, torch.float16), (0, torch.float32, torch.float64)])
+def test_pools_hold_their_pages(kvx, which, dtype, right, wrong):
+    """Too few rows, another type, not dense: the calls that touch pools refuse."""
+    full = (9 * 16, 64)
+    other = {"kp": "vp", "vp": "kp"}[which]
+    both = [Dev(*full, dtype=right)] * 2
+    fit = on_device_1(kvx, dtype=dtype, **{which: both, other: both})
+    assert fit.pools_fit
+    raw = [Dev(fit.pool_pages[0] * 16 * 64 * (4 if dtype == 0 else 2), dtype=torch.uint8)] * 2
+    assert on_device_1(kvx, dtype=dtype, **{which: raw, other: both}).pools_fit
+    for bad in (Dev(9 * 16 - 1, 64, dtype=right), Dev(*full, dtype=wrong),
+                Dev(*full, dtype=right, contiguous=False)):
+        c = on_device_1(kvx, dtype=dtype, **{which: [Dev(*full, dtype=right), bad], other: both})
+        for name, good in CALLS[1:]:
+            with pytest.raises(kvx.KvxError, match="pool_pages") as e:
+                getattr(kvx, name)(c, **good)
+            assert e.value.status == kvx.KVX_EINVAL
+
+
+def test_arrays_that_are_no_tensors(kvx):
+    refused(kvx, kvx.KVX_EINVAL, on_device_1, kvx, kp=["pool", A])
