@@ -742,6 +742,8 @@ def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len,
     n = int(max_rows)
     wp, wb = _workspace(cache, workspace, workspace_bytes)
     if path_stride is None:
+        if len(getattr(path, "shape", ())) != 2:
+            raise KvxError("path: not [B][path_stride], and no path_stride given", KVX_EINVAL)
         path_stride = path.shape[1]
     rc = lib.kvx_tree_commit(
         cache.handle, _dense(cache, q_start, "q_start", "int32", s.B + 1),

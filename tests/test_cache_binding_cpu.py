@@ -139,3 +139,11 @@ def test_pools_hold_their_pages(kvx, which, dtype, right, wrong):
 
 def test_arrays_that_are_no_tensors(kvx):
     refused(kvx, kvx.KVX_EINVAL, on_device_1, kvx, kp=["pool", A])
+
+
+def test_path_without_a_stride(kvx):
+    """An address, nothing or a flat tensor has no row stride of its own."""
+    c = on_device_1(kvx)
+    good = {**COMMIT, "workspace": Dev(64), "workspace_bytes": None, "path_stride": None}
+    for path in (A, None, Dev(4)):
+        refused(kvx, kvx.KVX_EINVAL, kvx.kvx_tree_commit, c, **{**good, "path": path})
