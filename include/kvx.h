@@ -670,6 +670,7 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              kvx_tree_attn at least kvx_tree_attn_workspace_bytes. Calls
  *              whose work may overlap on the GPU (two streams, two graphs)
  *              need workspaces of their own.
+ * Integer arrays are aligned to their element size (KVX_EINVAL otherwise).
  * Lengths are checked on the device. A sequence whose q_start entries are
  * negative, descending or past max_rows, or whose kv_len is negative or
  * does not fit its page table together with its new rows, is treated as

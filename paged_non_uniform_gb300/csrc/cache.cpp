@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "kvx_internal.h"
@@ -13,6 +14,13 @@ namespace kvx {
 namespace {
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+
+// The int32 arrays of a call.
+bool aligned_ints(std::initializer_list<const void *> arrays) {
+  for (const void *p : arrays)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
 
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -225,12 +233,14 @@ extern "C" int kvx_build_tables(const kvx_cache *c, const int32_t *kv_len, const
     return KVX_EINVAL;
   if (max_rows > kMaxRows) return KVX_ERANGE;
   if (pages_in == pages_out || free_in == free_out || !aligned(slots, 8)) return KVX_EINVAL;
+  if (!aligned_ints({kv_len, new_len, pages_in, pages_out, free_in, free_out, q_start}))
+    return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   TablesParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = c->dev;
   for (int gi = 0; gi < c->dev.G; ++gi) {
-    if (!free_pages[gi]) return KVX_EINVAL;
+    if (!free_pages[gi] || !aligned(free_pages[gi], 4)) return KVX_EINVAL;
     p.free_pages[gi] = free_pages[gi];
   }
   p.kv_len = kv_len;
@@ -255,6 +265,7 @@ extern "C" int kvx_append_kv(const kvx_cache *c, const void *k_new, int64_t k_st
   if (max_rows > 0 && (!k_new || !v_new || !slots)) return KVX_EINVAL;
   if (max_rows > kMaxRows) return KVX_ERANGE;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8)) return KVX_EINVAL;
+  if (!aligned(q_start, 4)) return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   AppendParams p;
   std::memset(&p, 0, sizeof(p));
@@ -289,7 +300,8 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
   if (max_rows > 0 && (!q || !out)) return KVX_EINVAL;
   if (max_q < 1 || max_q > KVX_MAX_TREE || max_rows > kMaxRows) return KVX_ERANGE;
   if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 4)) return KVX_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned_ints({mask, q_start, kv_len}))
+    return KVX_EINVAL;
   TreeParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = c->dev;
@@ -342,7 +354,8 @@ extern "C" int kvx_tree_commit(const kvx_cache *c, const int32_t *q_start, const
       (max_rows > 0 && !slots) || path_stride < 1)
     return KVX_EINVAL;
   if (max_rows > kMaxRows) return KVX_ERANGE;
-  if (!aligned(slots, 8)) return KVX_EINVAL;
+  if (!aligned(slots, 8) || !aligned_ints({q_start, path, n_acc, kv_len, kv_len_out}))
+    return KVX_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
   CommitParams p;
   std::memset(&p, 0, sizeof(p));

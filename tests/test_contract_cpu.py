@@ -34,3 +34,18 @@ def test_stated_stall_limits_are_the_accepted_ones(kvx):
             assert call(handle, -1, ns) == kvx.KVX_OK, (function, ns)
         for ns in (10 ** 6 - 1, most + 1):
             assert call(handle, -1, ns) == kvx.KVX_ERANGE, (function, ns)
+
+
+def test_unaligned_integer_arrays_are_refused(kvx):
+    """A kernel's load from an address that is not a multiple of its size would fault."""
+    from test_cache_cpu import A, APPEND, COMMIT, TABLES, TREE, make, refused
+    c = make(kvx)
+    for name, good, keys in (
+            ("kvx_build_tables", TABLES, ("kv_len", "new_len", "pages_in", "pages_out", "free_in", "free_out",
+                                          "q_start")),
+            ("kvx_append_kv", APPEND, ("q_start",)), ("kvx_tree_attn", TREE, ("q_start", "kv_len", "mask")),
+            ("kvx_tree_commit", COMMIT, ("q_start", "path", "n_acc", "kv_len", "kv_len_out"))):
+        for key in keys:
+            for off in (1, 2):
+                refused(kvx, kvx.KVX_EINVAL, getattr(kvx, name), c, **{**good, key: 4 * A + off})
+    refused(kvx, kvx.KVX_EINVAL, kvx.kvx_build_tables, c, **{**TABLES, "free_pages": [A, A + 2]})
