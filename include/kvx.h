@@ -761,8 +761,8 @@ int kvx_build_tables(const kvx_cache *cache, const int32_t *kv_len, const int32_
  *     pool_K(h)[slots[r][h]] = k_new[r][h],  same for V,  r < q_start[B].
  *   k_new, v_new  device [max_rows] rows of Hkv * D elements of the cache's
  *                 dtype, 16-byte aligned, k_stride / v_stride elements apart
- *                 (>= Hkv * D, a multiple of 16 bytes): slices of a fused
- *                 projection qualify.
+ *                 (>= Hkv * D, a multiple of 16 bytes, below 2^40 bytes):
+ *                 slices of a fused projection qualify.
  * A slot outside its pool is not written (KVX_DEV_BAD_BLOCK; -1 silently is
  * not). The slots of a call are distinct; of two equal ones either row, or
  * 16-byte pieces of both, may remain.
@@ -788,7 +788,7 @@ int kvx_append_kv(const kvx_cache *cache, const void *k_new, int64_t k_stride,
  * read from their pages (kvx_append_kv).
  *   q          device [max_rows] rows of Hq * D elements of the cache's dtype,
  *              16-byte aligned, q_stride elements apart (>= Hq * D, a multiple
- *              of 16 bytes).
+ *              of 16 bytes, below 2^40 bytes).
  *   max_q      host: largest T_b, 1 .. KVX_MAX_TREE; a sequence with more new
  *              rows is skipped (KVX_DEV_BAD_LENGTH).
  *   mask       device uint32 [max_rows][W], W = ceil(max_q / 32): bit u % 32 of

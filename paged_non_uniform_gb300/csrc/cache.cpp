@@ -26,11 +26,11 @@ bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
 int elem_bytes(const kvx_cache *c) { return c->shape.dtype == KVX_BF16 ? 2 : 4; }
 
-// A row array's stride in bytes, or 0 if it is not usable.
+// A row array's stride in bytes, or 0 if it is not usable (from 2^40 bytes on no tensor map
+// takes it).
 int64_t row_stride(const kvx_cache *c, int64_t stride, int heads) {
-  const int64_t es = elem_bytes(c);
-  if (stride < (int64_t)heads * c->shape.D || stride > ((int64_t)1 << 40) || stride * es % 16)
-    return 0;
+  const int64_t es = elem_bytes(c), limit = (int64_t)1 << 40;
+  if (stride < (int64_t)heads * c->shape.D || stride >= limit / es || stride * es % 16) return 0;
   return stride * es;
 }
 

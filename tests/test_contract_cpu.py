@@ -49,3 +49,15 @@ def test_unaligned_integer_arrays_are_refused(kvx):
             for off in (1, 2):
                 refused(kvx, kvx.KVX_EINVAL, getattr(kvx, name), c, **{**good, key: 4 * A + off})
     refused(kvx, kvx.KVX_EINVAL, kvx.kvx_build_tables, c, **{**TABLES, "free_pages": [A, A + 2]})
+
+
+def test_row_strides_past_a_tensor_map_are_refused(kvx):
+    """2^40 bytes: an argument error, not a failed launch."""
+    from test_cache_cpu import A, make
+    for dtype, item in ((kvx.KVX_BF16, 2), (kvx.KVX_F32, 4)):
+        c = make(kvx, dtype=dtype)
+        for stride in (2 ** 40 // item, 2 ** 40, 2 ** 62):
+            assert kvx.lib.kvx_tree_attn(c.handle, A, stride, A, 4, 2, A, None, 0.0, A, A, 1 << 40,
+                                         None) == kvx.KVX_EINVAL
+            assert kvx.lib.kvx_append_kv(c.handle, A, stride, A, 128, A, A, 4, A, 256, None) == kvx.KVX_EINVAL
+            assert kvx.lib.kvx_append_kv(c.handle, A, 128, A, stride, A, A, 4, A, 256, None) == kvx.KVX_EINVAL
