@@ -659,7 +659,8 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              head (b, h), for every head.
  *   max_rows   host: rows the row arrays hold, >= q_start[B]. Rows from
  *              q_start[B] on are neither read nor written. With 0 the row
- *              arrays may be NULL; more than 2^30 is KVX_ERANGE.
+ *              arrays may be NULL, and kvx_append_kv and kvx_tree_attn do
+ *              nothing; more than 2^30 is KVX_ERANGE.
  *   slots      device int64 [max_rows][Hkv]: where the row's K and V of KV head
  *              h are, as a row index into the pool of h's group:
  *                  head-major pages:  (page * |G| + r) * P + t % P
@@ -671,10 +672,12 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              whose work may overlap on the GPU (two streams, two graphs)
  *              need workspaces of their own.
  * Integer arrays are aligned to their element size (KVX_EINVAL otherwise).
- * Lengths are checked on the device. A sequence whose q_start entries are
- * negative, descending or past max_rows, or whose kv_len is negative or
- * does not fit its page table together with its new rows, is treated as
- * having no new rows, and KVX_DEV_BAD_LENGTH is set.
+ * Lengths are checked on the device; KVX_DEV_BAD_LENGTH says that some were out
+ * of range. A sequence whose q_start entries are negative, descending or past
+ * max_rows, or whose kv_len is negative or does not fit its page table together
+ * with its new rows, is treated as having no new rows. kvx_append_kv looks at
+ * q_start[B] only (a row's place is in its slots): below 0 it writes nothing,
+ * past max_rows the max_rows rows there are.
  * The device of the cache's memory has to be the current one (addresses do not
  * tell the library; the Python binding checks its tensors).
  * Launch: one kernel each (kvx_tree_attn: two, the second folds heads that were

@@ -22,7 +22,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   pdl_wait();
   const CacheDev &c = p.c;
   const int cpr = c.row_bytes >> 4;  // chunks of a row: 8, 16 or 32
-  const int rows = min(__ldg(p.q_start + c.B), p.max_rows);
+  const int stated = __ldg(p.q_start + c.B), rows = min(stated, p.max_rows);
+  if ((stated < 0 || stated > p.max_rows) && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   if (rows <= 0) return;
   const int64_t total = (int64_t)rows * c.Hkv * cpr;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
