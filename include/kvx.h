@@ -674,8 +674,11 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  * Integer arrays are aligned to their element size (KVX_EINVAL otherwise).
  * Lengths are checked on the device; KVX_DEV_BAD_LENGTH says that some were out
  * of range. A sequence whose q_start entries are negative, descending or past
- * max_rows, or whose kv_len is negative or does not fit its page table together
- * with its new rows, is treated as having no new rows. kvx_append_kv looks at
+ * max_rows is treated as having no new rows, and so is a head (b, h) whose kv_len
+ * is negative or does not fit its page table together with the new rows: its
+ * outputs, its cached rows and its length stay as they are, those of the
+ * sequence's other heads do not (kvx_build_tables refuses the whole call
+ * instead). kvx_append_kv looks at
  * q_start[B] only (a row's place is in its slots): below 0 it writes nothing,
  * past max_rows the max_rows rows there are.
  * The device of the cache's memory has to be the current one (addresses do not
@@ -828,7 +831,8 @@ int kvx_tree_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
  *   n_acc      device int32 [B], each in [0, min(T_b, path_stride)].
  *   kv_len_out device int32 [B][Hkv]; may be kv_len itself.
  * A sequence whose n_acc or path is out of range or not ascending keeps its
- * rows and its kv_len (KVX_DEV_BAD_LENGTH). A move whose source or target
+ * rows and its kv_len, and so does a head whose kv_len is out of range
+ * (KVX_DEV_BAD_LENGTH). A move whose source or target
  * slot is outside its pool is skipped (KVX_DEV_BAD_BLOCK).
  * Errors: KVX_EINVAL, KVX_ECUDA.
  * ------------------------------------------------------------------------- */

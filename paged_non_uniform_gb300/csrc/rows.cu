@@ -53,39 +53,38 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 // one head and walks j upwards: path ascends strictly, so path[j] >= j and
 // every source of a later j lies past all targets written so far. A batch of
 // eight loads therefore may precede its eight stores, and no thread reads what
-// another writes.
+// another writes. A block holds whole heads, whose lengths it checks and advances itself
+// (kv_out may be kv_len).
 __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitParams p) {
   pdl_wait();
   const CacheDev &c = p.c;
   const int b = blockIdx.y;
+  const int cpr = c.row_bytes >> 4;
+  const int per_head = 2 * cpr;  // K chunks, then V chunks: 16, 32 or 64
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  const int h = i / per_head, x = i - h * per_head;
+  const CacheGroup &g = c.grp[c.head_grp[min(h, c.Hkv - 1)]];
+  const size_t bh = (size_t)b * c.Hkv + h;
+  const int n = h < c.Hkv ? __ldg(p.kv_len + bh) : 0;
   const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1);
   const int a = __ldg(p.n_acc + b);
   const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.max_rows;
   const int *path = p.path + (size_t)b * p.path_stride;
-  bool ok = rows_ok && a >= 0 && a <= q1 - q0 && a <= p.path_stride;
-  if (ok) {
-    int bad = 0;
+  int bad = !(rows_ok && a >= 0 && a <= q1 - q0 && a <= p.path_stride);
+  if (!bad)
     for (int j = threadIdx.x; j < a; j += kThreads) {
       const int v = __ldg(path + j), before = j ? __ldg(path + j - 1) : -1;
       bad |= v <= before || v >= q1 - q0;
     }
-    ok = __syncthreads_or(bad) == 0;
-  }
-  if (blockIdx.x == 0) {
-    for (int h = threadIdx.x; h < c.Hkv; h += kThreads) {
-      const size_t i = (size_t)b * c.Hkv + h;
-      p.kv_out[i] = __ldg(p.kv_len + i) + (ok ? a : 0);
-    }
-    if (!ok && threadIdx.x == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
+  // of the sequence; the block has read its lengths before any of them is written
+  const bool seq_ok = __syncthreads_or(bad) == 0;
+  if (h >= c.Hkv) return;
+  const bool ok = seq_ok && n >= 0 && (int64_t)n + (q1 - q0) <= ((int64_t)g.stride << c.lgP);
+  if (x == 0) {
+    p.kv_out[bh] = n + (ok ? a : 0);
+    if (!ok) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   }
   if (!ok || a == 0) return;
-  const int cpr = c.row_bytes >> 4;
-  const int per_head = 2 * cpr;  // K chunks, then V chunks
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  const int h = i / per_head;
-  if (h >= c.Hkv) return;
-  const int x = i - h * per_head;
-  const CacheGroup &g = c.grp[c.head_grp[h]];
   char *pool = (x < cpr ? g.k : g.v) + (x < cpr ? x : x - cpr) * 16;
   const int64_t limit = g.pages * g.size * c.P;
   const int64_t *slots = p.slots + (size_t)q0 * c.Hkv + h;
