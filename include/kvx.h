@@ -803,7 +803,8 @@ int kvx_append_kv(const kvx_cache *cache, const void *k_new, int64_t k_stride,
  *              ignored. NULL: a chain, row i sees drafts 0 .. i.
  *   scale      score scale; 0 means 1/sqrt(D).
  *   out        device fp32 [max_rows][Hq][D], 16-byte aligned.
- * T_b = 1 with mask NULL is one decode step with device lengths. The keys are
+ * A head of more than 2^31 - 4097 tokens, its new rows included, is out of range
+ * (KVX_DEV_BAD_LENGTH). T_b = 1 with mask NULL is one decode step with device lengths. The keys are
  * split over the GPU from the lengths, on the device; pieces of a head
  * are merged by log-sum-exp in a fixed order (equal inputs give equal bits).
  * Page ids outside a pool read as zero rows (KVX_DEV_BAD_PAGE). bf16 caches run

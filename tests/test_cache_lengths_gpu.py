@@ -86,3 +86,37 @@ def test_commit_in_place_with_many_heads_again_and_again():
             assert np.array_equal(kv.cpu().numpy(), want), i
     torch.cuda.synchronize()
     assert np.array_equal(kv.cpu().numpy(), want) and s.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_at_the_longest_heads(dtype):
+    """Heads next to 2^31 tokens, all in one page that the table repeats: positions stay in int32 up to the
+    stated limit, past it a head is left out. The keys are zero, so that every weight is 1 and the sums are
+    whole numbers below 2^24 in each piece; V[r][d] is 1 where r % 64 = d, so the output is 1/64 up to one
+    page in 2^24, the division and the merge of at most 304 pieces (one rounding of 2^-24 each, of sum
+    and normaliser)."""
+    P, D, pages = 128, 64, 2 ** 24 - 1  # 2^31 - 128 tokens fit the table
+    limit = 2 ** 31 - 1 - 4096
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, pages, **i32)
+    k = torch.zeros(P, D, dtype=tt, device="cuda")
+    v = torch.eye(D, dtype=tt, device="cuda").repeat(2, 1).contiguous()
+    cache = kvx.Cache(1, 1, 1, D, P, 1, kvx.KVX_BF16 if dtype == "bf16" else kvx.KVX_F32, [0], [k], [v], [1],
+                      [table], [pages])
+    q = torch.ones(3, 1, D, dtype=tt, device="cuda")
+    ws = torch.zeros(kvx.kvx_tree_attn_workspace_bytes(cache, 3) // 4, **i32)
+    for T, n, good in ((1, limit - 1, True), (3, limit - 3, True), (1, limit, False), (3, limit - 2, False),
+                       (1, 2 ** 31 - 129, False), (2, 2 ** 31 - 130, False)):
+        out = torch.full((3, 1, D), -7.0, device="cuda")
+        kvx.kvx_tree_attn(cache, q, torch.tensor([0, T], **i32), 3, 3, torch.tensor([[n]], **i32), None, 0.0,
+                          out, ws)
+        torch.cuda.synchronize()
+        assert kvx.kvx_workspace_status(ws) == (0 if good else kvx.KVX_DEV_BAD_LENGTH), (T, n)
+        kvx.kvx_workspace_clear(ws)
+        assert bool((out[T:] == -7.0).all())
+        if good:
+            err = (out[:T].double() * 64 - 1).abs().max().item()
+            assert err <= 2.0 ** -23 + (2 * 304 + 2) * 2.0 ** -24, (T, n, err)
+        else:
+            assert bool((out == -7.0).all()), (T, n)
