@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   pdl_wait();
   const CacheDev &c = p.c;
   const int cpr = c.row_bytes >> 4;  // chunks of a row: 8, 16 or 32
-  const int stated = __ldg(p.q_start + c.B), rows = min(stated, p.max_rows);
+  const int stated = p.q_start[c.B], rows = min(stated, p.max_rows);
   if ((stated < 0 || stated > p.max_rows) && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   if (rows <= 0) return;
@@ -33,15 +33,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int ch = (int)(i - rh * cpr);
     const int64_t r = rh / c.Hkv;
     const int h = (int)(rh - r * c.Hkv);
-    const int64_t slot = __ldg(p.slots + rh);
+    const int64_t slot = p.slots[rh];
     const int grp = c.head_grp[h];
     if (slot < 0 || slot >= pool_rows(c, grp)) {
       if (slot != -1 && ch == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
       continue;
     }
     const int64_t src = (int64_t)h * c.row_bytes + ch * 16;
-    const uint4 kv = __ldg((const uint4 *)(p.k + r * p.k_stride + src));
-    const uint4 vv = __ldg((const uint4 *)(p.v + r * p.v_stride + src));
+    const uint4 kv = *(const uint4 *)(p.k + r * p.k_stride + src);
+    const uint4 vv = *(const uint4 *)(p.v + r * p.v_stride + src);
     const int64_t dst = slot * c.row_bytes + ch * 16;
     *(uint4 *)(c.grp[grp].k + dst) = kv;
     *(uint4 *)(c.grp[grp].v + dst) = vv;
@@ -65,15 +65,15 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
   const int h = i / per_head, x = i - h * per_head;
   const CacheGroup &g = c.grp[c.head_grp[min(h, c.Hkv - 1)]];
   const size_t bh = (size_t)b * c.Hkv + h;
-  const int n = h < c.Hkv ? __ldg(p.kv_len + bh) : 0;
-  const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1);
-  const int a = __ldg(p.n_acc + b);
+  const int n = h < c.Hkv ? p.kv_len[bh] : 0;
+  const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
+  const int a = p.n_acc[b];
   const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.max_rows;
   const int *path = p.path + (size_t)b * p.path_stride;
   int bad = !(rows_ok && a >= 0 && a <= q1 - q0 && a <= p.path_stride);
   if (!bad)
     for (int j = threadIdx.x; j < a; j += kThreads) {
-      const int v = __ldg(path + j), before = j ? __ldg(path + j - 1) : -1;
+      const int v = path[j], before = j ? path[j - 1] : -1;
       bad |= v <= before || v >= q1 - q0;
     }
   // of the sequence; the block has read its lengths before any of them is written
@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
       const int j = j0 + u;
       to[u] = -1;
       if (j >= a) continue;
-      const int s = __ldg(path + j);
+      const int s = path[j];
       if (s == j) continue;
-      const int64_t from = __ldg(slots + (size_t)s * c.Hkv), t = __ldg(slots + (size_t)j * c.Hkv);
+      const int64_t from = slots[(size_t)s * c.Hkv], t = slots[(size_t)j * c.Hkv];
       if (from < 0 || from >= limit || t < 0 || t >= limit) {
         if (x == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
         continue;

@@ -117,17 +117,17 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   }
   __syncthreads();
   pdl_wait();
-  if (tid < G) free_in[tid] = __ldg(p.free_in + tid);
+  if (tid < G) free_in[tid] = p.free_in[tid];
 
   // ---- lengths of every (group, sequence); sums of this block's group
   int bad = 0;
   for (int i = tid; i < G * B; i += kThreads) {
     const int g = i / B, b = i - g * B;
-    const int t = __ldg(p.new_len + b);
-    const int have = __ldg(p.pages_in + i);
+    const int t = p.new_len[b];
+    const int have = p.pages_in[i];
     int64_t n = 0;
     for (int k = head_off[g]; k < head_off[g + 1]; ++k) {
-      const int v = __ldg(p.kv_len + (size_t)b * Hkv + heads[k]);
+      const int v = p.kv_len[(size_t)b * Hkv + heads[k]];
       bad |= v < 0;
       n = max(n, (int64_t)v);
     }
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   if (bad || short_list) {  // the same verdict in every block: nothing changes
     if (first) {
       for (int b = tid; b < B; b += kThreads)
-        p.pages_out[(size_t)own * B + b] = __ldg(p.pages_in + (size_t)own * B + b);
+        p.pages_out[(size_t)own * B + b] = p.pages_in[(size_t)own * B + b];
       if (tid == 0) p.free_out[own] = free_in[own];
       if (own == 0) {
         for (int b = tid; b <= B; b += kThreads) p.q_start[b] = 0;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   const int32_t *pages_in = p.pages_in + (size_t)own * B;
   if (first)
     for (int b = tid; b < B; b += kThreads)
-      p.pages_out[(size_t)own * B + b] = __ldg(pages_in + b) + a_start[b] - r_start[b];
+      p.pages_out[(size_t)own * B + b] = pages_in[b] + a_start[b] - r_start[b];
   __syncthreads();
   exclusive_scans(sm, B, warp_sum);
   const CacheGroup &grp = c.grp[own];
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   // have - rel.
   auto released = [&](int r) {
     const int b = owner(r_start, B, r);
-    const int j = __ldg(pages_in + b) - (r_start[b + 1] - r_start[b]) + (r - r_start[b]);
+    const int j = pages_in[b] - (r_start[b + 1] - r_start[b]) + (r - r_start[b]);
     return grp.table[(size_t)b * grp.stride + j];
   };
   auto popped = [&](int k) {
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   for (int64_t r = at0; r < R; r += step) list[F + r] = released((int)r);
   for (int64_t k = at0; k < A; k += step) {
     const int b = owner(a_start, B, (int)k);
-    const int j = __ldg(pages_in + b) + ((int)k - a_start[b]);
+    const int j = pages_in[b] + ((int)k - a_start[b]);
     grp.table[(size_t)b * grp.stride + j] = popped((int)k);
   }
   // ---- slots of this group's heads, rows [r0, r1) of this block: consecutive threads
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     if (row >= b_end) {
       const int b = owner(q_start, B, row);
       b_end = q_start[b + 1];
-      shift = __ldg(p.kv_len + (size_t)b * Hkv + h) - q_start[b];
-      have = __ldg(pages_in + b);
+      shift = p.kv_len[(size_t)b * Hkv + h] - q_start[b];
+      have = pages_in[b];
       fresh = top - a_start[b] + have;  // page j is at list position fresh - j
       row_table = grp.table + (size_t)b * grp.stride;
     }

@@ -20,6 +20,10 @@ struct CacheGroup {
 };
 
 // The cache as the kernels see it (passed by value in their parameters).
+// The kernels are programmatic dependents: a grid may be resident while the kernel before it
+// still writes the lengths, tables, slots and rows that it will read. They are therefore read
+// with ordinary loads after the dependency wait, never through the non-coherent path (whose data
+// must not change while the grid runs, and whose loads may move ahead of the wait).
 struct CacheDev {
   CacheGroup grp[KVX_MAX_GROUPS];
   int32_t B, Hq, Hkv, D, g, G;

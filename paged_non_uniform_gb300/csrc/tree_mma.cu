@@ -260,7 +260,7 @@ __device__ __noinline__ void add_notes(const TreeParams &p, const TreeHead &hd, 
     const uint16_t *v = (const uint16_t *)(grp.v + pool_row(p.c, grp, pg, p.c.head_row[hd.h],
                                                             tok & (p.c.P - 1)) * (D * 2));
     for (int d = 0; d < D / 2; ++d) {
-      const float b = __uint_as_float((uint32_t)__ldg(v + d0 + d) << 16);
+      const float b = __uint_as_float((uint32_t)v[d0 + d] << 16);
       if (!isfinite(b)) out[d] += b;
     }
   }
@@ -328,7 +328,7 @@ __device__ __forceinline__ void produce(const MmaParams &mp, const TreeRange &ra
     const CacheGroup &grp = p.c.grp[p.c.head_grp[h.h]];
     const int tok = ahead.tile * kTile + lane * box;
     const int page = lane < per && tok < h.n + h.T
-                         ? __ldg(grp.table + (size_t)h.b * grp.stride + (tok >> p.c.lgP))
+                         ? grp.table[(size_t)h.b * grp.stride + (tok >> p.c.lgP)]
                          : 0;
     ahead.step(p);
     return page;

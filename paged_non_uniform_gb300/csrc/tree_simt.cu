@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
       float *dst = &sm.q[r][c * 4];
       if (r < rows) {
         const int nr = tree_div_g(p, r), j = r - nr * g;
-        *(float4 *)dst = __ldg((const float4 *)(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
-                                               ((size_t)hd.h * g + j) * (D * 4) + c * 16));
+        *(float4 *)dst = *(const float4 *)(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
+                                           ((size_t)hd.h * g + j) * (D * 4) + c * 16);
       } else {
         *(float4 *)dst = make_float4(0.f, 0.f, 0.f, 0.f);
       }

@@ -52,9 +52,9 @@ __device__ __forceinline__ TreeRaw tree_raw(const TreeParams &p, int hd) {
   TreeRaw r = {0, 0, 0};
   if (hd < p.c.B * p.c.Hkv) {
     const int b = hd / p.c.Hkv;
-    r.q0 = __ldg(p.q_start + b);
-    r.q1 = __ldg(p.q_start + b + 1);
-    r.n = __ldg(p.kv_len + hd);
+    r.q0 = p.q_start[b];
+    r.q1 = p.q_start[b + 1];
+    r.n = p.kv_len[hd];
   }
   return r;
 }
@@ -273,7 +273,7 @@ __device__ __forceinline__ uint32_t tree_mask_word(const TreeParams &p, const Tr
   uint32_t m;
   int last = t.T - 1;
   if (p.mask) {
-    m = w < p.words ? __ldg(p.mask + (size_t)(t.q0 + i) * p.words + w) : 0u;
+    m = w < p.words ? p.mask[(size_t)(t.q0 + i) * p.words + w] : 0u;
   } else {
     m = 0xffffffffu;
     last = i;

@@ -26,3 +26,12 @@ def test_page_writers_hold_their_dependents_back(source, names):
     for name, body in found.items():
         assert "pdl_launch_dependents" not in body, name
         assert body.rstrip().endswith("__threadfence();"), name
+
+
+@pytest.mark.parametrize("source", ["rows.cu", "tables.cu", "tree_mma.cu", "tree_simt.cu", "tree_merge.cu",
+                                    "tree_split.cuh"])
+def test_dependents_read_with_ordinary_loads(source):
+    """The non-coherent path is for memory that nobody writes while the grid runs. These grids may be
+    resident while the kernel before them writes their lengths, tables, slots and rows."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, source)).read())
+    assert "__ldg(" not in text and "ld.global.nc" not in text
