@@ -531,9 +531,10 @@ def _dense(cache, x, what: str, kind: str, count: int = 0):
     """Address of a dense device array: integer addresses pass (and None, where nothing is
     needed), tensors must be contiguous, of the given element type, on the cache's device, and
     hold at least `count` elements."""
+    dev = cache.device
     try:
-        if x.is_cuda and x.is_contiguous() and _kind(x.dtype) == kind \
-                and x.numel() >= count and cache.device in (None, x.get_device()):
+        if (x.is_cuda if dev is None else x.get_device() == dev) and x.is_contiguous() \
+                and (_kind_names.get(x.dtype) or _kind(x.dtype)) == kind and x.numel() >= count:
             return x.data_ptr()
     except AttributeError:
         if isinstance(x, int) or (x is None and count == 0):
@@ -547,8 +548,9 @@ def _rows(cache, x, what: str, width: int, max_rows: int):
     stride apart; for an integer address, the rows are dense."""
     if isinstance(x, int) or (x is None and max_rows == 0):
         return x, width
-    if x is not None and x.is_cuda and _kind(x.dtype) == cache.kind \
-            and cache.device in (None, x.get_device()):
+    dev = cache.device
+    if x is not None and (x.is_cuda if dev is None else x.get_device() == dev) \
+            and _kind(x.dtype) == cache.kind:
         size, stride = x.shape, x.stride()
         n = len(size)
         if n == 2:
@@ -583,9 +585,10 @@ def _check_pools(cache) -> None:
 def _workspace(cache, x, nbytes):
     """(address, bytes) of a call's workspace: a dense tensor on the cache's device (`nbytes`, where
     given, is at most its size), or an integer address of `nbytes` bytes."""
+    dev = cache.device
     try:
-        if x.is_cuda and x.is_contiguous() and cache.device in (None, x.get_device()):
-            have = x.numel() * x.element_size()
+        if (x.is_cuda if dev is None else x.get_device() == dev) and x.is_contiguous():
+            have = x.nbytes
             if nbytes is None:
                 return x.data_ptr(), have
             if 0 <= nbytes <= have:

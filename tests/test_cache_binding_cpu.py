@@ -32,6 +32,10 @@ class Dev:
             n *= x
         return n
 
+    @property
+    def nbytes(self):
+        return self.numel() * self.element_size()
+
     def stride(self):
         out = [1]
         for x in self.shape[:0:-1]:
