@@ -23,9 +23,11 @@ def test_page_writers_hold_their_dependents_back(source, names):
     performed."""
     found = kernels(source)
     assert set(found) == names
+    last_write = {"append_kernel": ".v + dst) =", "commit_kernel": "*(uint4 *)(pool", "tables_kernel": "grp.table["}
     for name, body in found.items():
         assert "pdl_launch_dependents" not in body, name
-        assert body.rstrip().endswith("__threadfence();"), name
+        writes = [m.end() for m in re.finditer(re.escape(last_write[name]), body)]
+        assert writes and "__threadfence();" in body[writes[-1]:], name
 
 
 @pytest.mark.parametrize("source", ["rows.cu", "tables.cu", "tree_mma.cu", "tree_simt.cu", "tree_merge.cu",
