@@ -200,8 +200,13 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
     d.head_row[h] = (int8_t)seen[head_group[h]]++;
   }
   for (int gi = 0; gi < G; ++gi)
-    d.grp[gi] = {page_tables[gi],  (char *)k_pools[gi],   (char *)v_pools[gi],
-                 pool_pages[gi],   page_table_stride[gi], size[gi]};
+    d.grp[gi] = {page_tables[gi],
+                 (char *)k_pools[gi],
+                 (char *)v_pools[gi],
+                 pool_pages[gi],
+                 page_table_stride[gi],
+                 size[gi],
+                 (int32_t)std::min((int64_t)page_table_stride[gi] * s->page_size, kMaxTokens)};
   c->stall_block = -1;
   c->wait_ns = 2000000000u;
   c->have_maps = s->dtype == KVX_BF16;

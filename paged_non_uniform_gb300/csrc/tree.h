@@ -11,12 +11,18 @@
 
 namespace kvx {
 
+// Tokens of a head in tree attention, new rows included: the kernels' positions run past the last
+// one by up to a tile, and those of the lanes that look up page ids by 31 boxes of 128 more,
+// within int32.
+constexpr int64_t kMaxTokens = INT32_MAX - 4096;
+
 // One head group of a cache: its page table [B][stride] and its pools.
 struct CacheGroup {
   int32_t *table;
   char *k, *v;
   int64_t pages;  // in each pool
   int32_t stride, size;
+  int32_t tokens;  // a sequence's room in the table, at most kMaxTokens
 };
 
 // The cache as the kernels see it (passed by value in their parameters).

@@ -30,10 +30,6 @@ namespace kvx {
 constexpr int kTileCost = 5;
 constexpr int kItemCost = 6;
 
-// Tokens of a head, new rows included: the kernels' positions run past the last one by up to a
-// tile, and those of the lanes that look up page ids by 31 boxes of 128 more, within int32.
-constexpr int kMaxTokens = INT32_MAX - 4096;
-
 struct TreeHead {
   int b, h;      // sequence, KV head
   int q0, T;     // first new row, new rows (0: nothing to do)
@@ -72,7 +68,7 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const
   t.T = r.q1 - r.q0;
   const CacheGroup &g = p.c.grp[p.c.head_grp[t.h]];
   const bool ok = r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.max_rows && t.T <= p.max_q && r.n >= 0 &&
-                  (int64_t)r.n + t.T <= min((int64_t)g.stride << p.c.lgP, (int64_t)kMaxTokens);
+                  r.n <= g.tokens - t.T;
   if (!ok) {
     if (report) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     t.T = t.n = 0;
