@@ -658,9 +658,11 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              0 = none). New row i of sequence b is token n[b][h] + i of
  *              head (b, h), for every head.
  *   max_rows   host: rows the row arrays hold, >= q_start[B]. Rows from
- *              q_start[B] on are neither read nor written. With 0 the row
- *              arrays may be NULL, and kvx_append_kv and kvx_tree_attn do
- *              nothing; more than 2^30 is KVX_ERANGE.
+ *              q_start[B] on are not written, and what they hold has no
+ *              influence (kvx_tree_attn loads queries eight rows at a time, so
+ *              up to seven of them may be read). With 0 the row arrays may be
+ *              NULL, and kvx_append_kv and kvx_tree_attn do nothing; more than
+ *              2^30 is KVX_ERANGE.
  *   slots      device int64 [max_rows][Hkv]: where the row's K and V of KV head
  *              h are, as a row index into the pool of h's group:
  *                  head-major pages:  (page * |G| + r) * P + t % P
@@ -671,6 +673,7 @@ int kvx_gather_coalesce_noalloc(const int32_t *block_table,
  *              kvx_tree_attn at least kvx_tree_attn_workspace_bytes. Calls
  *              whose work may overlap on the GPU (two streams, two graphs)
  *              need workspaces of their own.
+ * What a call writes overlaps none of its other arrays, but for kv_len_out.
  * Integer arrays are aligned to their element size (KVX_EINVAL otherwise).
  * Lengths are checked on the device; KVX_DEV_BAD_LENGTH says that some were out
  * of range. A sequence whose q_start entries are negative, descending or past

@@ -120,3 +120,16 @@ def test_attention_at_the_longest_heads(dtype):
             assert err <= 2.0 ** -23 + (2 * 304 + 2) * 2.0 ** -24, (T, n, err)
         else:
             assert bool((out == -7.0).all()), (T, n)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_behind_the_last_sequence_have_no_influence(dtype, bad):
+    """Query rows from q_start[B] on may share a load with the last sequence's; whatever they hold, the
+    outputs keep their bits."""
+    s = Setup(Case(dtype, 128, 2, 4, (0, 0), kv=((300, 20), (7, 140)), T=(5, 3)), extra_rows=9).upload()
+    want = s.run()
+    s.dq[s.N:] = bad
+    s.out.fill_(-7.0)
+    assert np.array_equal(s.run(), want) and np.all(want[s.N:] == -7.0)
+    assert s.status() == 0
