@@ -126,8 +126,10 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
-  // (more units than an int holds would be hundreds of times the device's memory,
-  // reachable only through aliased pages: refused whole)
+  // More units than an int holds are refused whole. Distinct pages cannot hold that many, but the
+  // margin is small: an fp32 cache of 288 GB with D = 64, g = 8 and 128 new rows a sequence has 32
+  // row groups a head and 32 KB a tile, 1.5e9 units with 262,144 heads,
+  // 1.4 times less (bf16: 5.7 times). Dearer tiles or items, or larger trees, need more bits.
   if (all > INT32_MAX) {
     if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     all = 0;

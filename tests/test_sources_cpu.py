@@ -37,3 +37,28 @@ def test_dependents_read_with_ordinary_loads(source):
     resident while the kernel before them writes their lengths, tables, slots and rows."""
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, source)).read())
     assert "__ldg(" not in text and "ld.global.nc" not in text
+
+
+def constant(source, name):
+    return int(re.search(rf"{name}\s*(?:=|\s)\s*(\d+)", open(os.path.join(CSRC, source)).read()).group(1))
+
+
+@pytest.mark.parametrize("source,item,D", [("tree_simt.cu", 4, 64), ("tree_simt.cu", 4, 128),
+                                           ("tree_mma.cu", 2, 64), ("tree_mma.cu", 2, 128)])
+def test_work_of_a_full_device_fits_the_cut(source, item, D):
+    """The cut of tree attention counts its units in 32 bits. The most that 288 GB of distinct pages can
+    ask for, with the most query heads a KV head, new rows, sequences and heads, stays below."""
+    header = os.path.join("..", "..", "include", "kvx.h")
+    g, tree = constant(header, "KVX_MAX_GQA"), constant(header, "KVX_MAX_TREE")
+    heads = constant(header, "KVX_MAX_CACHE_SEQS") * constant(header, "KVX_MAX_KV_HEADS")
+    tile = constant(source, "kTile")
+    if source == "tree_simt.cu":
+        tokens = constant(source, "kRows") // g
+    else:
+        box = constant("tree.h", "kTreeBox")
+        tokens = 128 // (box * g) * box
+    groups = -(-tree // tokens)
+    tiles = 288e9 / (2 * tile * D * item) + heads  # the last tile of a head may be partly filled
+    units = groups * (constant("tree_split.cuh", "kTileCost") * tiles
+                      + constant("tree_split.cuh", "kItemCost") * heads)
+    assert units < 2 ** 31, units
