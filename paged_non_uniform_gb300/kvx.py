@@ -549,19 +549,21 @@ def _rows(cache, x, what: str, width: int, max_rows: int):
     if isinstance(x, int) or (x is None and max_rows == 0):
         return x, width
     dev = cache.device
-    if x is not None and (x.is_cuda if dev is None else x.get_device() == dev) \
-            and _kind(x.dtype) == cache.kind:
-        size, stride = x.shape, x.stride()
-        n = len(size)
-        if n == 2:
-            ok = size[1] == width and (stride[1] == 1 or width == 1)
-        elif n == 3:
-            ok = size[1] * size[2] == width and (stride[2] == 1 or size[2] == 1) \
-                and (stride[1] == size[2] or size[1] == 1)
-        else:
-            ok = False
-        if ok and size[0] >= max_rows:
-            return x.data_ptr(), (stride[0] if size[0] > 1 else width)
+    try:
+        if (x.is_cuda if dev is None else x.get_device() == dev) and _kind(x.dtype) == cache.kind:
+            size, stride = x.shape, x.stride()
+            n = len(size)
+            if n == 2:
+                ok = size[1] == width and (stride[1] == 1 or width == 1)
+            elif n == 3:
+                ok = size[1] * size[2] == width and (stride[2] == 1 or size[2] == 1) \
+                    and (stride[1] == size[2] or size[1] == 1)
+            else:
+                ok = False
+            if ok and size[0] >= max_rows:
+                return x.data_ptr(), (stride[0] if size[0] > 1 else width)
+    except AttributeError:
+        pass
     raise KvxError(f"{what}: not {max_rows} device rows of {width} {cache.kind} elements",
                    KVX_EINVAL)
 

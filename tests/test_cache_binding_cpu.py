@@ -151,3 +151,10 @@ def test_path_without_a_stride(kvx):
     good = {**COMMIT, "workspace": Dev(64), "workspace_bytes": None, "path_stride": None}
     for path in (A, None, Dev(4)):
         refused(kvx, kvx.KVX_EINVAL, kvx.kvx_tree_commit, c, **{**good, "path": path})
+
+
+def test_rows_that_are_no_tensors(kvx):
+    import numpy as np
+    for c in (on_device_1(kvx), make(kvx)):
+        for bad in (np.zeros((4, 128), np.float32), [0.0], "rows", None):
+            refused(kvx, kvx.KVX_EINVAL, kvx._rows, c, bad, "rows", 128, 4)
