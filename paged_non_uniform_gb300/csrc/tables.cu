@@ -16,10 +16,10 @@
 // neither, which is what makes a repeated call give the same result.
 // Dependents start only when the tables are written (no early trigger, and a fence behind
 // the writes): a decode call with early loads reads page ids before its dependency wait.
-// Measured on one GB300: a verify step (16 sequences, 3 groups) 6.5 us, all latency: two
-// passes of loads, the sums and their scan; 256 prompts (1.17 M rows, 9.4 M slots of 8
-// bytes) 21 us, of which a plain fill with the slots' 75 MB would take 10 and the sums,
-// which every block makes, 5.
+// Measured on one GB300: a verify step (16 sequences, 3 groups) 8.0 us, all latency: two
+// passes of loads, the sums and their scan (6.7 when dependents were let go at once); 256
+// prompts (1.17 M rows, 9.4 M slots of 8 bytes) 21.8 us, of which a plain fill with the slots'
+// 75 MB would take 10 and the sums, which every block makes, 5.
 #include "ptx.cuh"
 #include "tree.h"
 

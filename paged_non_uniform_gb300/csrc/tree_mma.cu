@@ -32,9 +32,9 @@
 // short sequences took 121 us instead of 102 (ragged trees 171 instead of 175).
 // Measured on one GB300 (a call in a graph): 16 sequences of 8k to 32k, 16 drafts, 4
 // query heads a KV head, 84.5 us for 427 MB, of which about 15 are the ramp, the last output
-// and the merge (tensor pipe 39 % busy); 8 x 122k, 24 drafts, 650 to 690 us by GPU for 4.0
-// GB (5.8 to 6.1 TB/s); 256 of 100 to 1000, 1 to 8 drafts, 102 us for 448 MB; one of 2k,
-// 16.2 us. A tile takes a block about 3.3 us: scores, softmax and output products one
+// and the merge (tensor pipe 39 % busy); 8 x 122k, 24 drafts, 650 to 720 us by GPU for 4.0
+// GB (5.6 to 6.1 TB/s); 256 of 100 to 1000, 1 to 8 drafts, 102 us for 448 MB; one of 2k,
+// 16.1 us. A tile takes a block about 3.3 us: scores, softmax and output products one
 // after the other, which two blocks per SM hide from each other for the most part. Tried
 // and slower: tiles or V slots of 64 keys; a second V slot where 64 query rows leave room
 // for it; the products transposed, so that few query rows fill the tensor cores (a tile
