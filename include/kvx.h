@@ -1,9 +1,11 @@
 /*
  * kvx.h -- C ABI of the kvx library: decode-step attention over a paged KV
  * cache with non-uniform per-head budgets, the coalesced KV gather and the
- * block pager behind it, kept-set selection for sparse decode, and the steps
+ * block pager behind it, kept-set selection for sparse decode, the steps
  * of speculative decoding over the same pages (tables built on the GPU, K/V
- * append, attention for a tree of drafted tokens, branch commit).
+ * append, attention for a tree of drafted tokens, branch commit), and what keeps
+ * such a cache within a memory budget (attention with windows and sinks that
+ * accumulates weights, eviction by them, caches in 4 bits).
  *
  * Sources of the operations:
  *  - "Tangram: Unlocking Non-Uniform KV Cache for Efficient Multi-turn LLM
@@ -80,6 +82,8 @@ extern "C" {
 /* ---- element types --------------------------------------------------- */
 #define KVX_F32 0
 #define KVX_BF16 1
+#define KVX_Q4 4 /* kvx_cache_create only: K and V in 4 bits, see "A cache within a memory
+                    budget" below; queries and new rows are bf16 */
 
 /* ---- work-split policies (kvx_plan_create) ---------------------------- */
 /* Ahead-of-time balanced split (Tangram, AOT Load Balancing): the kept tokens
@@ -844,6 +848,114 @@ int kvx_tree_commit(const kvx_cache *cache, const int32_t *q_start, const int64_
                     int32_t max_rows, const int32_t *path, int32_t path_stride,
                     const int32_t *n_acc, const int32_t *kv_len, int32_t *kv_len_out,
                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * A cache within a memory budget.
+ *
+ * Three ways to read or keep less, on the cache handle above and with its
+ * conventions (device lengths, launch order, workspaces, capture):
+ *     kvx_window_attn    heads that look at a window of recent tokens and a few
+ *                        first ones; on request it adds up how much weight every
+ *                        cached token was given
+ *     kvx_evict          drops the tokens with the least weight (Tangram, Deterministic
+ *                        Budget Allocation: this is what holds a head to its budget)
+ *     KVX_Q4 caches      K and V in 4 bits: kvx_append_kv quantises, kvx_window_attn and
+ *                        kvx_read_kv read, kvx_evict moves
+ *
+ * KVX_Q4. k_pools and v_pools hold bytes; layout must be KVX_LAYOUT_HEAD_MAJOR. Every 64
+ * elements of a row share two bf16 numbers, step and lo, and element x is
+ * lo + step * code, code 0 .. 15. The P rows of a head in a page are one block of
+ * P * (D/2 + D/16) bytes: the codes [P][D/2], then [P][D/64]{step, lo}. A 32-bit word
+ * holds the codes of eight neighbouring elements, lowest bits first; word w of a row
+ * of 128 elements is stored at position 2 * (w % 8) + w / 8, of a row of 64 at w.
+ * kvx_append_kv takes bf16 rows and sets lo to the group's least element, step to
+ * bf16((greatest - lo) / 15) and code to min(15, rint((x - lo) / step)), in fp32 (0 where
+ * step is 0). A group with a non-finite element, or whose range overflows fp32, reads as NaN.
+ * Slots, page tables and kvx_build_tables are as for the other types. kvx_tree_attn and
+ * kvx_tree_commit do not take such a cache (KVX_EUNSUPPORTED), nor do plans.
+ *
+ * kvx_read_kv -- the reverse of kvx_append_kv:
+ *     k_out[r][h] = pool_K(h)[slots[r][h]],  same for V,  r < q_start[B].
+ *   k_out, v_out  as k_new and v_new of kvx_append_kv, written here; of a KVX_Q4
+ *                 cache the values lo + step * code rounded to bf16.
+ * A row whose slot is -1, or outside its pool (KVX_DEV_BAD_BLOCK), stays as it is.
+ * Errors: KVX_EINVAL, KVX_ERANGE (max_rows), KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_read_kv(const kvx_cache *cache, const int32_t *q_start, const int64_t *slots,
+                int32_t max_rows, void *k_out, int64_t k_stride, void *v_out, int64_t v_stride,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * kvx_window_attn -- attention of the new rows with a window and sinks per KV head.
+ *
+ * As kvx_tree_attn, but new row i of sequence b, at position n[b][h] + i of head h,
+ * sees the tokens t (cached or new) with
+ *     t <= n[b][h] + i   and   (t < sinks[h]   or   t > n[b][h] + i - window[h]):
+ * the window holds the row's own token, so window 1 is the token itself. Only the tiles
+ * of 64 tokens that some new row sees are read. A row that sees nothing (window 0,
+ * sinks 0) gives zeros, and so does one whose visible scores are all -inf.
+ * max_q = 1 is a decode step.
+ *   sinks, window  device int32 [Hkv], negative values count as 0; NULL: no sinks,
+ *                  and a window that holds everything.
+ *   weights        NULL, or a host array [num_groups] of device fp32 pools
+ *                  [pool_pages[g] * |G| * P], one number per row of the group's K pool
+ *                  (same row index). Then for every token t that was read,
+ *                      w_t = (t < n[b][h] ? w_t : 0) + sum of softmax_t
+ *                  over the sequence's new rows and the g query heads: new tokens start at 0.
+ *                  Weights of tokens that no row sees keep their value. Sums are made in
+ *                  a fixed order (equal inputs give equal bits).
+ *   workspace      >= kvx_window_attn_workspace_bytes(cache, max_q, weights != NULL). With
+ *                  weights it holds a score for every query row and token that the page
+ *                  tables have room for, 4 * max_q * g bytes a token of a head.
+ *   q, max_q, scale, out: as for kvx_tree_attn. 4-bit caches compute with lo + step * code
+ *                  unrounded.
+ * The same lengths are out of range, page ids outside a pool read as zero rows
+ * (KVX_DEV_BAD_PAGE; their weights are lost), and so much work that (tiles + 1) over all
+ * heads and groups of query rows pass 2^31 is refused whole (KVX_DEV_BAD_LENGTH).
+ * Launch: two kernels, with weights three.
+ * Errors: KVX_EINVAL, KVX_ERANGE (max_q, max_rows), KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_window_attn_workspace_bytes(const kvx_cache *cache, int32_t max_q, int32_t weigh,
+                                    size_t *bytes);
+
+int kvx_window_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
+                    const int32_t *q_start, int32_t max_rows, int32_t max_q,
+                    const int32_t *kv_len, const int32_t *sinks, const int32_t *window,
+                    float scale, float *out, float *const *weights, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * kvx_evict -- holds every head to its budget by dropping the tokens with the
+ * least weight.
+ *
+ * Head (b, h) with n = kv_len[b][h] tokens and m = min(n, budget[b][h]) keeps the last
+ * r = min(m, recent), the first f = min(m - r, sinks) and, of the tokens between, the
+ * m - r - f with the largest weights; equal weights (-0 equals 0): the lower index; NaN
+ * counts as less than any number. The kept tokens' K, V and weight move, in their
+ * order, to places 0 .. m-1 of the head's pages; kv_len_out[b][h] = m. What lies behind
+ * stays as it is; the next kvx_build_tables, given kv_len_out, releases the pages.
+ *   budget       device int32 [B][Hkv].
+ *   sinks, recent  host, >= 0.
+ *   weights      host array [num_groups] of device fp32 pools, as for kvx_window_attn.
+ *   weights_out  likewise: the weights' own pools (all of them), or others that overlap
+ *                none, which then receive the weights of all kept tokens.
+ *   kv_len_out   device int32 [B][Hkv]; may be kv_len itself.
+ *   workspace    >= kvx_evict_workspace_bytes(cache).
+ * A head whose kv_len does not fit its page table, or is negative, or whose budget is
+ * negative, stays as it is (KVX_DEV_BAD_LENGTH). A token of a page outside the pool counts
+ * as NaN, and a move from or to one is skipped (KVX_DEV_BAD_PAGE). A page belongs to one
+ * sequence, as for kvx_build_tables.
+ * Launch: two kernels; pages are written by the second, which lets its dependents start
+ * only when all is written. In it, waits for rows that have yet to be read by another block give
+ * up after 2 s (KVX_DEV_TIMEOUT; the rows in question are not written).
+ * Errors: KVX_EINVAL, KVX_ECUDA.
+ * ------------------------------------------------------------------------- */
+int kvx_evict_workspace_bytes(const kvx_cache *cache, size_t *bytes);
+
+int kvx_evict(const kvx_cache *cache, const int32_t *kv_len, const int32_t *budget,
+              int32_t sinks, int32_t recent, const float *const *weights,
+              float *const *weights_out, int32_t *kv_len_out, void *workspace,
+              size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,6 @@
 // cache.cpp -- the cache handle and the entry points of a speculative-decoding
-// step over it: argument validation (everything is checked before anything is
-// launched) and launches.
+// step over it, and of the calls that keep it within a memory budget: argument
+// validation (everything is checked before anything is launched) and launches.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -9,6 +9,7 @@
 
 #include "kvx_internal.h"
 #include "tree.h"
+#include "window.h"
 
 namespace kvx {
 namespace {
@@ -24,7 +25,8 @@ bool aligned_ints(std::initializer_list<const void *> arrays) {
 
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
-int elem_bytes(const kvx_cache *c) { return c->shape.dtype == KVX_BF16 ? 2 : 4; }
+// Of queries and new rows (4-bit caches take them in bf16).
+int elem_bytes(const kvx_cache *c) { return c->shape.dtype == KVX_F32 ? 4 : 2; }
 
 // A row array's stride in bytes, or 0 if it is not usable (from 2^40 bytes on no tensor map
 // takes it).
@@ -121,6 +123,55 @@ int tree_shape(const kvx_cache *c, TreeShape *t) {
   return KVX_OK;
 }
 
+// Scores that window attention leaves for its weights: visited keys of a head, row groups
+// and rows of a group, at most.
+int64_t score_keys(const kvx_cache *c) {
+  int64_t n = 0;
+  for (int gi = 0; gi < c->dev.G; ++gi) n = std::max(n, (int64_t)c->dev.grp[gi].tokens);
+  return (n + kWindowTile - 1) / kWindowTile * kWindowTile;
+}
+int score_groups(const WindowShape *t, int max_q) { return (max_q + t->tokens - 1) / t->tokens; }
+int score_rows(const kvx_cache *c, const WindowShape *t, int max_q) {
+  return (std::min(t->tokens, max_q) * c->dev.g + 3) / 4 * 4;
+}
+
+// Row groups, blocks and the workspace of a cache's window attention.
+int window_shape(const kvx_cache *c, int max_q, bool weigh, WindowShape *t) {
+  int32_t sms = 0;
+  const int rc = kvx_device_sm_count(&sms);
+  if (rc != KVX_OK) return rc;
+  const int g = c->dev.g;
+  t->blocks = sms * window_simt_blocks_per_sm();
+  t->rows = window_simt_rows();
+  t->tokens = t->rows / g;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);
+  TreeWs &w = t->ws;
+  w.split = KVX_WS_HEADER_BYTES;
+  w.part_ml = w.split + up(t->blocks * sizeof(TreeSplit));
+  w.part_o = w.part_ml + up(slots * t->rows * sizeof(float2));
+  w.fold = w.total = t->row_ml = t->total = w.part_o + up(slots * t->rows * row);
+  if (weigh) {
+    t->split_row = t->row_ml + up((size_t)c->dev.B * max_q * c->dev.Hq * sizeof(float2));
+    t->scores = t->split_row + up(t->blocks * sizeof(int32_t));
+    t->total = t->scores + up((size_t)c->dev.B * c->dev.Hkv * score_groups(t, max_q) *
+                              score_keys(c) * score_rows(c, t, max_q) * sizeof(float));
+  }
+  return KVX_OK;
+}
+
+// Units of an eviction, at most: every chunk that the page tables have room for.
+int64_t evict_units(const kvx_cache *c) {
+  int64_t n = 0;
+  for (int h = 0; h < c->dev.Hkv; ++h)
+    n += (int64_t)c->dev.B *
+         ((c->dev.grp[c->dev.head_grp[h]].tokens + (int64_t)kEvictChunk - 1) / kEvictChunk);
+  return n;
+}
+size_t evict_flags(const kvx_cache *c) {  // where the units' flags are in the workspace
+  return KVX_WS_HEADER_BYTES + (size_t)evict_units(c) * sizeof(EvictUnit);
+}
+
 }  // namespace
 }  // namespace kvx
 
@@ -156,8 +207,9 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
   if (s->Hq / s->Hkv > KVX_MAX_GQA) return KVX_EUNSUPPORTED;
   if (s->D != 64 && s->D != 128) return KVX_EUNSUPPORTED;
   if (!is_pow2(s->page_size) || s->page_size < 8 || s->page_size > 128) return KVX_EUNSUPPORTED;
-  if (s->dtype != KVX_F32 && s->dtype != KVX_BF16) return KVX_EUNSUPPORTED;
-  if (s->layout != KVX_LAYOUT_HEAD_MAJOR && s->layout != KVX_LAYOUT_TOKEN_MAJOR)
+  if (s->dtype != KVX_F32 && s->dtype != KVX_BF16 && s->dtype != KVX_Q4) return KVX_EUNSUPPORTED;
+  if (s->layout != KVX_LAYOUT_HEAD_MAJOR &&
+      (s->layout != KVX_LAYOUT_TOKEN_MAJOR || s->dtype == KVX_Q4))
     return KVX_EUNSUPPORTED;
   const int G = s->num_groups, Hkv = s->Hkv;
   int32_t size[KVX_MAX_GROUPS] = {0};
@@ -284,12 +336,14 @@ extern "C" int kvx_append_kv(const kvx_cache *c, const void *k_new, int64_t k_st
   p.slots = slots;
   p.status = (uint32_t *)workspace;
   p.max_rows = max_rows;
-  const cudaError_t e = launch_append(p, (cudaStream_t)stream);
+  const cudaError_t e = c->shape.dtype == KVX_Q4 ? launch_q4_append(p, (cudaStream_t)stream)
+                                                 : launch_append(p, (cudaStream_t)stream);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
 }
 
 extern "C" int kvx_tree_attn_workspace_bytes(const kvx_cache *c, int32_t max_q, size_t *bytes) {
   if (!c || !bytes) return KVX_EINVAL;
+  if (c->shape.dtype == KVX_Q4) return KVX_EUNSUPPORTED;
   if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
   TreeShape t;
   const int rc = tree_shape(c, &t);
@@ -302,6 +356,7 @@ extern "C" int kvx_tree_attn(const kvx_cache *c, const void *q, int64_t q_stride
                              const int32_t *kv_len, const uint32_t *mask, float scale, float *out,
                              void *workspace, size_t workspace_bytes, void *stream) {
   if (!c || !q_start || !kv_len || max_rows < 0) return KVX_EINVAL;
+  if (c->shape.dtype == KVX_Q4) return KVX_EUNSUPPORTED;
   if (max_rows > 0 && (!q || !out)) return KVX_EINVAL;
   if (max_q < 1 || max_q > KVX_MAX_TREE || max_rows > kMaxRows) return KVX_ERANGE;
   if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
@@ -358,6 +413,7 @@ extern "C" int kvx_tree_commit(const kvx_cache *c, const int32_t *q_start, const
   if (!c || !q_start || !path || !n_acc || !kv_len || !kv_len_out || max_rows < 0 ||
       (max_rows > 0 && !slots) || path_stride < 1)
     return KVX_EINVAL;
+  if (c->shape.dtype == KVX_Q4) return KVX_EUNSUPPORTED;
   if (max_rows > kMaxRows) return KVX_ERANGE;
   if (!aligned(slots, 8) || !aligned_ints({q_start, path, n_acc, kv_len, kv_len_out}))
     return KVX_EINVAL;
@@ -375,5 +431,149 @@ extern "C" int kvx_tree_commit(const kvx_cache *c, const int32_t *q_start, const
   p.max_rows = max_rows;
   p.path_stride = path_stride;
   const cudaError_t e = launch_commit(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_read_kv(const kvx_cache *c, const int32_t *q_start, const int64_t *slots,
+                           int32_t max_rows, void *k_out, int64_t k_stride, void *v_out,
+                           int64_t v_stride, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  if (!c || !q_start || max_rows < 0) return KVX_EINVAL;
+  if (max_rows > 0 && (!k_out || !v_out || !slots)) return KVX_EINVAL;
+  if (max_rows > kMaxRows) return KVX_ERANGE;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 8)) return KVX_EINVAL;
+  if (!aligned(q_start, 4)) return KVX_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  ReadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.k = (char *)k_out;
+  p.v = (char *)v_out;
+  p.k_stride = row_stride(c, k_stride, c->dev.Hkv);
+  p.v_stride = row_stride(c, v_stride, c->dev.Hkv);
+  if (!p.k_stride || !p.v_stride) return KVX_EINVAL;
+  p.q_start = q_start;
+  p.slots = slots;
+  p.status = (uint32_t *)workspace;
+  p.max_rows = max_rows;
+  p.q4 = c->shape.dtype == KVX_Q4;
+  const cudaError_t e = launch_read(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_window_attn_workspace_bytes(const kvx_cache *c, int32_t max_q, int32_t weigh,
+                                               size_t *bytes) {
+  if (!c || !bytes || (weigh != 0 && weigh != 1)) return KVX_EINVAL;
+  if (max_q < 1 || max_q > KVX_MAX_TREE) return KVX_ERANGE;
+  WindowShape t;
+  const int rc = window_shape(c, max_q, weigh != 0, &t);
+  if (rc == KVX_OK) *bytes = t.total;
+  return rc;
+}
+
+extern "C" int kvx_window_attn(const kvx_cache *c, const void *q, int64_t q_stride,
+                               const int32_t *q_start, int32_t max_rows, int32_t max_q,
+                               const int32_t *kv_len, const int32_t *sinks, const int32_t *window,
+                               float scale, float *out, float *const *weights, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+  if (!c || !q_start || !kv_len || max_rows < 0) return KVX_EINVAL;
+  if (max_rows > 0 && (!q || !out)) return KVX_EINVAL;
+  if (max_q < 1 || max_q > KVX_MAX_TREE || max_rows > kMaxRows) return KVX_ERANGE;
+  if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned_ints({q_start, kv_len, sinks, window}))
+    return KVX_EINVAL;
+  WindowParams p;
+  std::memset((void *)&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.q_stride = row_stride(c, q_stride, c->dev.Hq);
+  if (!p.q_stride) return KVX_EINVAL;
+  for (int gi = 0; weights && gi < c->dev.G; ++gi) {
+    if (!weights[gi] || !aligned(weights[gi], 4)) return KVX_EINVAL;
+    p.weights[gi] = weights[gi];
+  }
+  if (!workspace_ok(workspace, workspace_bytes, KVX_WS_HEADER_BYTES)) return KVX_EINVAL;
+  WindowShape t;
+  const int rc = window_shape(c, max_q, weights != nullptr, &t);
+  if (rc != KVX_OK) return rc;
+  if (workspace_bytes < t.total) return KVX_EINVAL;
+  if (max_rows == 0) return KVX_OK;
+  char *ws = (char *)workspace;
+  p.q = (const char *)q;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.sinks = sinks;
+  p.window = window;
+  p.out = out;
+  p.status = (uint32_t *)ws;
+  p.split = (TreeSplit *)(ws + t.ws.split);
+  p.part_ml = (float2 *)(ws + t.ws.part_ml);
+  p.part_o = (float *)(ws + t.ws.part_o);
+  if (weights) {
+    p.row_ml = (float2 *)(ws + t.row_ml);
+    p.split_row = (int32_t *)(ws + t.split_row);
+    p.scores = (float *)(ws + t.scores);
+    p.score_keys = score_keys(c);
+    p.score_rows = score_rows(c, &t, max_q);
+    p.score_groups = score_groups(&t, max_q);
+  }
+  p.max_rows = max_rows;
+  p.max_q = max_q;
+  p.stall_block = -1;
+  p.wait_ns = c->wait_ns;
+  p.group_tokens = t.tokens;
+  p.group_rows = t.rows;
+  p.recip_g = (65536 + c->dev.g - 1) / c->dev.g;
+  const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
+  p.scale_log2 = (float)((double)sc * 1.4426950408889634);
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = launch_window_simt(p, c->shape.dtype, t.blocks, st);
+  if (e == cudaSuccess) e = launch_tree_merge(p, t.blocks, st);
+  if (e == cudaSuccess && weights) e = launch_weigh(p, t.blocks, st);
+  return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
+}
+
+extern "C" int kvx_evict_workspace_bytes(const kvx_cache *c, size_t *bytes) {
+  if (!c || !bytes) return KVX_EINVAL;
+  *bytes = evict_flags(c) + ((size_t)evict_units(c) * sizeof(uint32_t) + 255) / 256 * 256;
+  return KVX_OK;
+}
+
+extern "C" int kvx_evict(const kvx_cache *c, const int32_t *kv_len, const int32_t *budget,
+                         int32_t sinks, int32_t recent, const float *const *weights,
+                         float *const *weights_out, int32_t *kv_len_out, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  if (!c || !kv_len || !budget || !weights || !weights_out || !kv_len_out) return KVX_EINVAL;
+  if (sinks < 0 || recent < 0) return KVX_EINVAL;
+  if (!aligned_ints({kv_len, budget, kv_len_out})) return KVX_EINVAL;
+  size_t need = 0;
+  kvx_evict_workspace_bytes(c, &need);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return KVX_EINVAL;
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = c->dev;
+  p.kv_len = kv_len;
+  p.budget = budget;
+  p.kv_out = kv_len_out;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.q4 = c->shape.dtype == KVX_Q4;
+  for (int gi = 0; gi < c->dev.G; ++gi) {
+    if (!weights[gi] || !weights_out[gi] || !aligned(weights[gi], 4) || !aligned(weights_out[gi], 4))
+      return KVX_EINVAL;
+    p.weights[gi] = weights[gi];
+    p.weights_out[gi] = weights_out[gi];
+    p.copy_weights |= weights[gi] != weights_out[gi];
+  }
+  // all in place or all elsewhere
+  for (int gi = 0; gi < c->dev.G; ++gi)
+    if (p.copy_weights && weights[gi] == weights_out[gi]) return KVX_EINVAL;
+  char *ws = (char *)workspace;
+  p.status = (uint32_t *)ws;
+  p.counters = (uint32_t *)ws + 16;
+  p.units = (EvictUnit *)(ws + KVX_WS_HEADER_BYTES);
+  p.read_done = (uint32_t *)(ws + evict_flags(c));
+  p.max_units = evict_units(c);
+  p.wait_ns = c->wait_ns;
+  const cudaError_t e = launch_evict(p, (cudaStream_t)stream);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);
 }

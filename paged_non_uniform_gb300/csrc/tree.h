@@ -35,7 +35,7 @@ struct CacheDev {
   int32_t B, Hq, Hkv, D, g, G;
   int32_t P, lgP;       // page size and its log2
   int32_t token_major;  // page layout
-  int32_t row_bytes;    // D elements
+  int32_t row_bytes;    // D elements (4-bit caches: of a new row)
   int8_t head_grp[KVX_MAX_KV_HEADS];
   int8_t head_row[KVX_MAX_KV_HEADS];
 };
@@ -105,6 +105,10 @@ struct TreeParams {
   float scale_log2;                // scale * log2(e)
   int32_t stall_block;             // failure-detection test (-1: none)
   uint32_t wait_ns;                // limit of every pipeline wait
+  // Window attention with weights (else null): (max, sum) of every new row and query head,
+  // [B][max_q][Hq], and [blocks] the row in it at which split[block] begins.
+  float2 *row_ml;
+  int32_t *split_row;
 };
 
 // Workspace of tree attention: header | split row groups | partial (m, l) | partial o |

@@ -76,6 +76,8 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const __grid_const
 #pragma unroll
     for (int w = 16; w; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
     const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees nothing
+    if (p.row_ml && lane == 0)
+      *tree_row_ml(p, p.split_row[blockIdx.y], s.h, r) = make_float2(M, L);
     float *out = tree_out(p, s.row0, s.h, r) + lane * E;
     if constexpr (E == 4)
       *(float4 *)out = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);

@@ -35,10 +35,28 @@ struct TreeHead {
   int q0, T;     // first new row, new rows (0: nothing to do)
   int n;         // cached tokens
   int tiles, groups;
-  // cost of a row group, and of the head
-  __device__ __forceinline__ int seg() const { return tiles ? kItemCost + kTileCost * tiles : 0; }
-  __device__ __forceinline__ int64_t cost() const { return (int64_t)seg() * groups; }
+  int lead, gap;  // windows (window_split.cuh): tiles before the gap, tiles left out
 };
+
+// What a tile and an item cost, by the kind of attention.
+__device__ __forceinline__ constexpr int tile_cost(const TreeParams &) { return kTileCost; }
+__device__ __forceinline__ constexpr int item_cost(const TreeParams &) { return kItemCost; }
+// A head's tiles: all of its keys.
+template <int kTile>
+__device__ __forceinline__ void tree_tiles(const TreeParams &, TreeHead &t) {
+  t.tiles = t.T > 0 ? (t.n + t.T + kTile - 1) / kTile : 0;
+  t.lead = t.gap = 0;
+}
+
+// Cost of a row group, and of the head.
+template <class Prm>
+__device__ __forceinline__ int tree_seg(const Prm &p, const TreeHead &t) {
+  return t.tiles ? item_cost(p) + tile_cost(p) * t.tiles : 0;
+}
+template <class Prm>
+__device__ __forceinline__ int64_t tree_cost(const Prm &p, const TreeHead &t) {
+  return (int64_t)tree_seg(p, t) * t.groups;
+}
 
 // The lengths of a head as they are in memory: loaded ahead of their use.
 struct TreeRaw {
@@ -57,8 +75,8 @@ __device__ __forceinline__ TreeRaw tree_raw(const TreeParams &p, int hd) {
 
 // Head `hd` from its lengths; lengths that do not fit their arrays give T = 0
 // and set KVX_DEV_BAD_LENGTH (in the one block that reports).
-template <int kTile>
-__device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const TreeRaw &r,
+template <int kTile, class Prm>
+__device__ __forceinline__ TreeHead tree_head(const Prm &p, int hd, const TreeRaw &r,
                                               bool report) {
   TreeHead t;
   t.b = hd / p.c.Hkv;
@@ -73,7 +91,7 @@ __device__ __forceinline__ TreeHead tree_head(const TreeParams &p, int hd, const
     if (report) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     t.T = t.n = 0;
   }
-  t.tiles = t.T > 0 ? (t.n + t.T + kTile - 1) / kTile : 0;
+  tree_tiles<kTile>(p, t);
   t.groups = t.T <= p.group_tokens ? 1 : (t.T + p.group_tokens - 1) / p.group_tokens;
   return t;
 }
@@ -100,8 +118,8 @@ __device__ __forceinline__ int tree_block_of(int units, int blocks, int u) {
 // Sums the costs of all heads over the block's NT threads and finds this block's range.
 // `min_tiles`: a block gets at least the cost of that many (one at least, so that every
 // block between a row group's first and last has a tile of it).
-template <int NT, int kTile>
-__device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_tiles,
+template <int NT, int kTile, class Prm>
+__device__ __forceinline__ TreeRange tree_range(const Prm &p, int min_tiles,
                                                 int64_t *warp_sum /* shared, NT / 32 */,
                                                 TreeRange *shared) {
   // Each warp takes a run of heads, its lanes one head in turn.
@@ -112,7 +130,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
   TreeRaw raw = tree_raw(p, lo + lane), raw1 = tree_raw(p, lo + lane + 32);
   for (int i = lo + lane; i < hi; i += 32) {  // (lengths loaded two steps ahead)
     const TreeRaw raw2 = tree_raw(p, i + 64);
-    s += tree_head<kTile>(p, i, raw, blockIdx.x == 0).cost();
+    s += tree_cost(p, tree_head<kTile>(p, i, raw, blockIdx.x == 0));
     raw = raw1;
     raw1 = raw2;
   }
@@ -136,7 +154,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
   }
   // Little work: parts of exactly `least`, so that a block has no more tiles than that
   // stands for (the last part may be shorter).
-  const int least = min_tiles * kTileCost, total = (int)all;
+  const int least = min_tiles * tile_cost(p), total = (int)all;
   const bool little = total / least < (int)gridDim.x;
   const int blocks = little ? (total + least - 1) / least : (int)gridDim.x;
   const int units = little ? blocks * least : total;
@@ -154,7 +172,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int min_til
       const int i = i0 + lane;
       TreeHead t = {};
       if (i < hi) t = tree_head<kTile>(p, i, tree_raw(p, i), false);
-      const int u = (int)t.cost();
+      const int u = (int)tree_cost(p, t);
       int x = u;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -184,16 +202,18 @@ struct TreeCursor {
   int at, end, base, hd;
   TreeHead head;
   TreeRaw raw1, raw2;
-  __device__ __forceinline__ TreeCursor(const TreeParams &p, const TreeRange &r)
+  template <class Prm>
+  __device__ __forceinline__ TreeCursor(const Prm &p, const TreeRange &r)
       : at(r.begin), end(r.end), base(r.base), hd(r.head), head(r.first) {
     if (at < end) {
       raw1 = tree_raw(p, hd + 1);
       raw2 = tree_raw(p, hd + 2);
     }
   }
-  __device__ __forceinline__ bool next(const TreeParams &p, TreeItem &it) {
+  template <class Prm>
+  __device__ __forceinline__ bool next(const Prm &p, TreeItem &it) {
     while (at < end) {
-      const int seg = head.seg();
+      const int seg = tree_seg(p, head);
       if (at - base >= seg * head.groups) {
         base += seg * head.groups;
         ++hd;
@@ -203,9 +223,9 @@ struct TreeCursor {
         continue;
       }
       const int group = head.groups == 1 ? 0 : (at - base) / seg;
-      const int start = base + group * seg, first = start + kItemCost;  // of its tile 0
-      const int t0 = max(0, at - first + kTileCost - 1) / kTileCost;
-      const int t1 = min(head.tiles, (max(0, end - first) + kTileCost - 1) / kTileCost);
+      const int start = base + group * seg, first = start + item_cost(p);  // of its tile 0
+      const int c = tile_cost(p), t0 = max(0, at - first + c - 1) / c;
+      const int t1 = min(head.tiles, (max(0, end - first) + c - 1) / c);
       at = start + seg;  // (past `end` where the row group runs on)
       if (t0 >= t1) continue;
       it.head = head;
@@ -250,16 +270,27 @@ __device__ __forceinline__ float *tree_out(const TreeParams &p, int row0, int h,
   return p.out + ((size_t)(row0 + i) * p.c.Hq + (size_t)h * p.c.g + j) * p.c.D;
 }
 
+// Where its maximum and sum go (window attention with weights).
+__device__ __forceinline__ int tree_ml_row(const TreeParams &p, int b, int first) {
+  return b * p.max_q + first;  // of a sequence's new row `first`
+}
+__device__ __forceinline__ float2 *tree_row_ml(const TreeParams &p, int row0, int h, int r) {
+  const int i = tree_div_g(p, r), j = r - i * p.c.g;
+  return p.row_ml + (size_t)(row0 + i) * p.c.Hq + (size_t)h * p.c.g + j;
+}
+
 // Describes the row group that starts in this block and runs past its end (one
 // thread; `it` is the block's last item, or null if it has none).
-__device__ __forceinline__ void tree_describe(const TreeParams &p, const TreeRange &r,
+template <class Prm>
+__device__ __forceinline__ void tree_describe(const Prm &p, const TreeRange &r,
                                               const TreeItem *it) {
   TreeSplit s = {0, 0, 0, 0};
   if (it && it->t0 == 0 && !tree_whole(*it)) {
     const int last = tree_block_of(
-        r.units, r.blocks, it->seg + kItemCost + kTileCost * (it->head.tiles - 1));
+        r.units, r.blocks, it->seg + item_cost(p) + tile_cost(p) * (it->head.tiles - 1));
     s = {last - (int)blockIdx.x + 1, it->head.q0 + tree_first(p, *it), it->head.h,
          tree_rows(p, *it)};
+    if (p.row_ml) p.split_row[blockIdx.x] = tree_ml_row(p, it->head.b, tree_first(p, *it));
   }
   p.split[blockIdx.x] = s;
 }

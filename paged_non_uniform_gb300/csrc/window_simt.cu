@@ -1,0 +1,302 @@
+// window_simt.cu -- attention with a sliding window and sink tokens over a paged
+// cache, on the CUDA cores, and its accumulated weights.
+//
+// out[row] = sum_t softmax(scale * <q_row, k_t>)_t v_t over the keys that the row sees
+// (window_split.cuh), in one pass over the visited tiles of 64 keys per group of 32 query
+// rows (running maximum and sum in fp32). K and V tiles are gathered from their
+// pages into shared memory as fp32; each thread computes a 4 x 4 block of scores and
+// accumulates 4 rows x D/16 dims of the output. A tile that some row sees only in part
+// takes a separate path that skips what a row does not see instead of multiplying
+// it by zero, so that NaN and infinities in unseen rows, and padding, have no influence.
+#include <math.h>
+
+#include "window_split.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kTile = kWindowTile;
+constexpr int kRows = 32;
+constexpr int kMinTiles = 2;
+
+template <int D>
+struct Smem {
+  float q[kRows][D + 4];
+  float k[kTile][D + 4];
+  float v[kTile][D + 4];
+  float p[kRows][kTile + 4];
+  uint32_t seen[kRows][2];  // visible keys of the tile, by row
+  int64_t warp_sum[kThreads / 32];
+  TreeRange range;
+};
+
+// Elements 4c .. 4c + 3 of a pool's row.
+template <int D, int kDtype>
+__device__ __forceinline__ float4 load4(const CacheDev &cd, const char *pool, int64_t row, int c) {
+  if constexpr (kDtype == KVX_F32) {
+    return *(const float4 *)(pool + row * (D * 4) + c * 16);
+  } else if constexpr (kDtype == KVX_BF16) {
+    const uint2 x = *(const uint2 *)(pool + row * (D * 2) + c * 8);
+    const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    const int w = c >> 1, at = D == 128 ? 2 * (w & 7) + (w >> 3) : w;
+    const uint32_t x = *(const uint16_t *)(pool + q4_codes(cd, row) + at * 4 + (c & 1) * 2);
+    const float2 p = unpack_bf16(*(const uint32_t *)(pool + q4_params(cd, row) + (w >> 3) * 4));
+    return make_float4(fmaf(p.x, (float)(x & 15), p.y), fmaf(p.x, (float)(x >> 4 & 15), p.y),
+                       fmaf(p.x, (float)(x >> 8 & 15), p.y), fmaf(p.x, (float)(x >> 12), p.y));
+  }
+}
+template <int D, int kDtype>
+__device__ __forceinline__ float4 load_q(const char *row, int c) {
+  if constexpr (kDtype == KVX_F32) return *(const float4 *)(row + c * 16);
+  const uint2 x = *(const uint2 *)(row + c * 8);
+  const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <int D, int kDtype>
+__global__ void __launch_bounds__(kThreads, 2)
+    window_simt_kernel(const __grid_constant__ WindowParams p) {
+  extern __shared__ float4 smem_raw[];
+  Smem<D> &sm = *(Smem<D> *)smem_raw;
+  constexpr int CPR = D / 4;  // 4-element chunks of a row
+  constexpr int ND = D / 64;
+  constexpr int kItem = kDtype == KVX_F32 ? 4 : 2;  // bytes of a query element
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  const TreeRange range = tree_range<kThreads, kTile>(p, kMinTiles, sm.warp_sum, &sm.range);
+  TreeCursor<kTile> cur(p, range);
+  TreeItem it;
+  bool any = false;
+  while (cur.next(p, it)) {
+    any = true;
+    const TreeHead &hd = it.head;
+    const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
+    const Window win = window_of(p, hd.h);
+    const int rank = p.c.head_row[hd.h], g = p.c.g, P = p.c.P;
+    const int32_t *table = grp.table + (size_t)hd.b * grp.stride;
+    const int i0 = tree_first(p, it), rows = tree_rows(p, it);
+    const int i1 = i0 + tree_div_g(p, rows - 1);
+    __syncthreads();  // the item before is done with shared memory
+    for (int i = tid; i < kRows * CPR; i += kThreads) {
+      const int r = i / CPR, c = i - r * CPR;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        const int nr = tree_div_g(p, r), j = r - nr * g;
+        x = load_q<D, kDtype>(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
+                                  ((size_t)hd.h * g + j) * (D * kItem), c);
+      }
+      *(float4 *)&sm.q[r][c * 4] = x;
+    }
+    float m[4], l[4], o[4][ND][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      m[a] = -INFINITY;
+      l[a] = 0.f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[a][d][0] = o[a][d][1] = o[a][d][2] = o[a][d][3] = 0.f;
+    }
+    for (int tile = it.t0; tile < it.t1; ++tile) {
+      const int t0 = window_tile(hd, tile) * kTile, valid = min(kTile, hd.n + hd.T - t0);
+      const bool edge = !window_all_seen(win, hd.n, i0, i1, t0, kTile);
+      __syncthreads();  // the tile before is consumed
+      for (int i = tid; i < kTile * CPR; i += kThreads) {
+        const int t = i / CPR, c = i - t * CPR;
+        float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
+        if (t < valid) {
+          const int tok = t0 + t;
+          const int page = table[tok >> p.c.lgP];
+          if (page >= 0 && page < grp.pages) {
+            const int64_t at = pool_row(p.c, grp, page, rank, tok & (P - 1));
+            dk = load4<D, kDtype>(p.c, grp.k, at, c);
+            dv = load4<D, kDtype>(p.c, grp.v, at, c);
+          } else if (c == 0) {
+            atomicOr(p.status, KVX_DEV_BAD_PAGE);
+          }
+        }
+        *(float4 *)&sm.k[t][c * 4] = dk;
+        *(float4 *)&sm.v[t][c * 4] = dv;
+      }
+      if (edge && tid < 2 * kRows) {
+        // visible keys of row r, word w: bits [32w, 32w + 32) of the tile
+        const int r = tid >> 1, w = tid & 1;
+        uint32_t bits = 0;
+        if (r < rows) {
+          const int pos = hd.n + i0 + tree_div_g(p, r);
+#pragma unroll 4
+          for (int e = 0; e < 32; ++e)
+            bits |= (window_sees(win, pos, t0 + 32 * w + e) ? 1u : 0u) << e;
+        }
+        sm.seen[r][w] = bits;
+      }
+      __syncthreads();
+      float s[4][4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 qa[4], kb[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) qa[a] = *(const float4 *)&sm.q[ty * 4 + a][d];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) kb[b] = *(const float4 *)&sm.k[tx + 16 * b][d];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            s[a][b] = fmaf(qa[a].x, kb[b].x, s[a][b]);
+            s[a][b] = fmaf(qa[a].y, kb[b].y, s[a][b]);
+            s[a][b] = fmaf(qa[a].z, kb[b].z, s[a][b]);
+            s[a][b] = fmaf(qa[a].w, kb[b].w, s[a][b]);
+          }
+      }
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        float mx = m[a];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = tx + 16 * b;
+          float x = s[a][b] * p.scale_log2;
+          if (edge && !((sm.seen[ty * 4 + a][t >> 5] >> (t & 31)) & 1u)) x = -INFINITY;
+          s[a][b] = x;
+          mx = fmaxf(mx, x);
+          if (p.scores && ty * 4 + a < rows)
+            window_scores(p, hd, it.group, (int64_t)tile * kTile + t)[ty * 4 + a] = x;
+        }
+#pragma unroll
+        for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float ref = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing
+        const float al = tree_weight(m[a], ref);
+        m[a] = mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float e = ex2(s[a][b] - ref);
+          sm.p[ty * 4 + a][tx + 16 * b] = e;
+          sum += e;
+        }
+#pragma unroll
+        for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        l[a] = l[a] * al + sum;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          o[a][d][0] *= al;
+          o[a][d][1] *= al;
+          o[a][d][2] *= al;
+          o[a][d][3] *= al;
+        }
+      }
+      __syncwarp();  // a row's scores are written and read by one half-warp
+      if (!edge) {
+#pragma unroll 2
+        for (int t = 0; t < kTile; t += 4) {
+          float pa[4][4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const float4 x = *(const float4 *)&sm.p[ty * 4 + a][t];
+            pa[a][0] = x.x;
+            pa[a][1] = x.y;
+            pa[a][2] = x.z;
+            pa[a][3] = x.w;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              const float4 vv = *(const float4 *)&sm.v[t + u][tx * 4 + 64 * d];
+#pragma unroll
+              for (int a = 0; a < 4; ++a) {
+                o[a][d][0] = fmaf(pa[a][u], vv.x, o[a][d][0]);
+                o[a][d][1] = fmaf(pa[a][u], vv.y, o[a][d][1]);
+                o[a][d][2] = fmaf(pa[a][u], vv.z, o[a][d][2]);
+                o[a][d][3] = fmaf(pa[a][u], vv.w, o[a][d][3]);
+              }
+            }
+        }
+      } else {
+        for (int t = 0; t < valid; ++t) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            if (!((sm.seen[ty * 4 + a][t >> 5] >> (t & 31)) & 1u)) continue;
+            const float x = sm.p[ty * 4 + a][t];
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              const float4 vv = *(const float4 *)&sm.v[t][tx * 4 + 64 * d];
+              o[a][d][0] = fmaf(x, vv.x, o[a][d][0]);
+              o[a][d][1] = fmaf(x, vv.y, o[a][d][1]);
+              o[a][d][2] = fmaf(x, vv.z, o[a][d][2]);
+              o[a][d][3] = fmaf(x, vv.w, o[a][d][3]);
+            }
+          }
+        }
+      }
+    }
+    const bool whole = tree_whole(it);
+    const int slot = whole ? 0 : tree_slot(it);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = ty * 4 + a;
+      if (r >= rows) continue;
+      float *dst;
+      float f = 1.f;
+      if (whole) {
+        dst = tree_out(p, hd.q0 + i0, hd.h, r);
+        f = l[a] == 0.f ? 0.f : 1.f / l[a];
+        if (p.row_ml && tx == 0)
+          *tree_row_ml(p, tree_ml_row(p, hd.b, i0), hd.h, r) = make_float2(m[a], l[a]);
+      } else {
+        const size_t at = (size_t)slot * kRows + r;
+        dst = p.part_o + at * D;
+        if (tx == 0) p.part_ml[at] = make_float2(m[a], l[a]);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        *(float4 *)(dst + tx * 4 + 64 * d) =
+            make_float4(o[a][d][0] * f, o[a][d][1] * f, o[a][d][2] * f, o[a][d][3] * f);
+    }
+  }
+  if (tid == 0) tree_describe(p, range, any ? &it : nullptr);
+}
+
+template <int D, int kDtype>
+cudaError_t launch_d(const WindowParams &p, int blocks, cudaStream_t st) {
+  const int bytes = (int)sizeof(Smem<D>);
+  static int8_t done[64];
+  cudaError_t e = raise_smem_limit(done, (const void *)window_simt_kernel<D, kDtype>, bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, window_simt_kernel<D, kDtype>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_t(const WindowParams &p, int dtype, int blocks, cudaStream_t st) {
+  if (dtype == KVX_F32) return launch_d<D, KVX_F32>(p, blocks, st);
+  if (dtype == KVX_BF16) return launch_d<D, KVX_BF16>(p, blocks, st);
+  return launch_d<D, KVX_Q4>(p, blocks, st);
+}
+
+}  // namespace
+
+int window_simt_rows() { return kRows; }
+int window_simt_blocks_per_sm() { return 2; }
+
+cudaError_t launch_window_simt(const WindowParams &p, int dtype, int blocks, cudaStream_t st) {
+  return p.c.D == 128 ? launch_t<128>(p, dtype, blocks, st) : launch_t<64>(p, dtype, blocks, st);
+}
+
+}  // namespace kvx

@@ -38,6 +38,7 @@ KVX_DEV_NO_PAGES = 32
 
 KVX_F32 = 0
 KVX_BF16 = 1
+KVX_Q4 = 4
 KVX_PLAN_BALANCED = 0
 KVX_PLAN_PER_HEAD = 1
 KVX_PLAN_UNIFORM = 2
@@ -161,6 +162,15 @@ lib.kvx_tree_attn.argtypes = [_vp, _vp, _c.c_int64, _vp, _c.c_int32, _c.c_int32,
                               _c.c_float, _vp, _vp, _c.c_size_t, _vp]
 lib.kvx_tree_commit.argtypes = [_vp, _vp, _vp, _c.c_int32, _vp, _c.c_int32, _vp, _vp, _vp, _vp,
                                 _c.c_size_t, _vp]
+lib.kvx_read_kv.argtypes = [_vp, _vp, _vp, _c.c_int32, _vp, _c.c_int64, _vp, _c.c_int64, _vp,
+                            _c.c_size_t, _vp]
+lib.kvx_window_attn_workspace_bytes.argtypes = [_vp, _c.c_int32, _c.c_int32,
+                                                _c.POINTER(_c.c_size_t)]
+lib.kvx_window_attn.argtypes = [_vp, _vp, _c.c_int64, _vp, _c.c_int32, _c.c_int32, _vp, _vp, _vp,
+                                _c.c_float, _vp, _vp, _vp, _c.c_size_t, _vp]
+lib.kvx_evict_workspace_bytes.argtypes = [_vp, _c.POINTER(_c.c_size_t)]
+lib.kvx_evict.argtypes = [_vp, _vp, _vp, _c.c_int32, _c.c_int32, _vp, _vp, _vp, _vp, _c.c_size_t,
+                          _vp]
 
 
 def kvx_status_string(status: int) -> str:
@@ -614,7 +624,7 @@ class Cache:
                  pool_pages, page_tables, page_table_stride, layout=KVX_LAYOUT_HEAD_MAJOR):
         self.handle = None
         self.shape = kvx_shape(B, Hq, Hkv, D, page_size, num_groups, dtype, layout)
-        self.kind = "bfloat16" if dtype == KVX_BF16 else "float32"
+        self.kind = "float32" if dtype == KVX_F32 else "bfloat16"  # of queries and new rows
         hg, ps = _i32(head_group), _i32(page_table_stride)
         pp = np.ascontiguousarray(np.asarray(pool_pages, dtype=np.int64))
         if hg.size != Hkv or any(len(x) != num_groups
@@ -631,9 +641,11 @@ class Cache:
                                     ps.ctypes.data, _c.byref(h)), "kvx_cache_create")
         self.handle = h.value
         self.pool_pages = pp.tolist()
-        page = page_size * D * (2 if dtype == KVX_BF16 else 4)
+        page = page_size * (D // 2 + D // 16 if dtype == KVX_Q4 else D * (4 if dtype == KVX_F32 else 2))
         size = np.bincount(hg, minlength=num_groups).tolist()
-        self.pools_fit = all(self._holds(x, n * z * page, (self.kind, "int8", "int16", "int32"))
+        self.pool_rows = [n * z * page_size for n, z in zip(self.pool_pages, size)]
+        kinds = ("int8", "int16", "int32") + (() if dtype == KVX_Q4 else (self.kind,))
+        self.pools_fit = all(self._holds(x, n * z * page, kinds)
                              for pools in (k_pools, v_pools)
                              for x, n, z in zip(pools, self.pool_pages, size))
         self._keep = (list(k_pools), list(v_pools), list(page_tables))
@@ -758,3 +770,73 @@ def kvx_tree_commit(cache: Cache, q_start, slots, max_rows, path, n_acc, kv_len,
         _dense(cache, kv_len, "kv_len", "int32", s.B * s.Hkv),
         _dense(cache, kv_len_out, "kv_len_out", "int32", s.B * s.Hkv), wp, wb, _stream(stream))
     _check(rc, "kvx_tree_commit")
+
+
+# ---------------------------------------------------------------------------
+# A cache within a memory budget
+
+def kvx_read_kv(cache: Cache, q_start, slots, max_rows, k_out, v_out, workspace,
+                workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
+    _check_pools(cache)
+    s = cache.shape
+    n = int(max_rows)
+    k, ks = _rows(cache, k_out, "k_out", s.Hkv * s.D, n)
+    v, vs = _rows(cache, v_out, "v_out", s.Hkv * s.D, n)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
+    rc = lib.kvx_read_kv(cache.handle, _dense(cache, q_start, "q_start", "int32", s.B + 1),
+                         _dense(cache, slots, "slots", "int64", n * s.Hkv), n, k, ks, v, vs, wp, wb,
+                         _stream(stream))
+    _check(rc, "kvx_read_kv")
+
+
+def _weights(cache, pools, what: str):
+    """Host array of the weight pools' addresses: one fp32 pool per head group, a number per row."""
+    if len(pools) != cache.shape.num_groups:
+        raise KvxError(f"{what}: one pool per head group", KVX_EINVAL)
+    return _ptr_array([_dense(cache, x, what, "float32", n) for x, n in zip(pools, cache.pool_rows)])
+
+
+def kvx_window_attn_workspace_bytes(cache: Cache, max_q: int, weigh: bool) -> int:
+    v = _c.c_size_t(0)
+    _check(lib.kvx_window_attn_workspace_bytes(cache.handle, int(max_q), int(weigh), _c.byref(v)),
+           "kvx_window_attn_workspace_bytes")
+    return int(v.value)
+
+
+def kvx_window_attn(cache: Cache, q, q_start, max_rows, max_q, kv_len, sinks, window, scale, out,
+                    weights, workspace, workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
+    _check_pools(cache)
+    s = cache.shape
+    n = int(max_rows)
+    qp, qs = _rows(cache, q, "q", s.Hq * s.D, n)
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
+    rc = lib.kvx_window_attn(
+        cache.handle, qp, qs, _dense(cache, q_start, "q_start", "int32", s.B + 1), n, int(max_q),
+        _dense(cache, kv_len, "kv_len", "int32", s.B * s.Hkv),
+        None if sinks is None else _dense(cache, sinks, "sinks", "int32", s.Hkv),
+        None if window is None else _dense(cache, window, "window", "int32", s.Hkv), float(scale),
+        _dense(cache, out, "out", "float32", n * s.Hq * s.D),
+        None if weights is None else _weights(cache, weights, "weights"), wp, wb, _stream(stream))
+    _check(rc, "kvx_window_attn")
+
+
+def kvx_evict_workspace_bytes(cache: Cache) -> int:
+    v = _c.c_size_t(0)
+    _check(lib.kvx_evict_workspace_bytes(cache.handle, _c.byref(v)), "kvx_evict_workspace_bytes")
+    return int(v.value)
+
+
+def kvx_evict(cache: Cache, kv_len, budget, sinks, recent, weights, weights_out, kv_len_out,
+              workspace, workspace_bytes=None, stream=None) -> None:
+    _on_device(cache)
+    _check_pools(cache)
+    s = cache.shape
+    wp, wb = _workspace(cache, workspace, workspace_bytes)
+    rc = lib.kvx_evict(cache.handle, _dense(cache, kv_len, "kv_len", "int32", s.B * s.Hkv),
+                       _dense(cache, budget, "budget", "int32", s.B * s.Hkv), int(sinks), int(recent),
+                       _weights(cache, weights, "weights"), _weights(cache, weights_out, "weights_out"),
+                       _dense(cache, kv_len_out, "kv_len_out", "int32", s.B * s.Hkv), wp, wb,
+                       _stream(stream))
+    _check(rc, "kvx_evict")
