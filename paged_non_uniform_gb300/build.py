@@ -18,12 +18,13 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvx.so")
 SOURCES = ["plan.cpp", "abi.cpp", "attn_mma.cu", "attn_simt.cu", "gather.cu", "select.cu",
            "frame.cu", "cache.cpp", "tables.cu", "rows.cu", "tree_simt.cu",
-           "tree_mma.cu", "tree_merge.cu", "window_simt.cu", "window_weigh.cu", "evict.cu",
+           "tree_mma.cu", "tree_merge.cu", "window_simt.cu", "window_bf16.cu", "window_q4.cu", "window_weigh.cu", "evict.cu",
            "q4_rows.cu"]
 HEADERS = [os.path.join(CSRC, "kvx_internal.h"), os.path.join(CSRC, "ptx.cuh"),
            os.path.join(CSRC, "split_merge.cuh"), os.path.join(CSRC, "tree.h"),
            os.path.join(CSRC, "tree_split.cuh"), os.path.join(CSRC, "tcgen05.cuh"),
            os.path.join(CSRC, "window.h"), os.path.join(CSRC, "window_split.cuh"),
+           os.path.join(CSRC, "window_mma.cuh"),
            os.path.join(ROOT, "include", "kvx.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

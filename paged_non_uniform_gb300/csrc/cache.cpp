@@ -68,15 +68,16 @@ bool encode(CUtensorMap *tm, const void *base, const cuuint64_t *dims, const cuu
 }
 
 // A 5-D bf16 tensor map over one head group's pool, whose box is one head's rows of a
-// page and lands as [8-row group][64-dim half][8 rows][128 bytes], 128-byte swizzled,
+// page, `tokens` of them, and lands as [8-row group][64-dim half][8 rows][128 bytes], 128-byte swizzled,
 // zeros outside: the same distance between all 8-row groups of a tile, which one
 // operand descriptor can express. Dims (innermost first):
 //   head-major pages:  {64 elements, 8 rows, D/64 halves, P/8 groups, pages * |G|}
 //   token-major pages: {64 elements, 8 rows, D/64 halves, pages * P/8 groups, |G|}
-bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g) {
+bool encode_map(CUtensorMap *tm, const kvx_cache *c, const void *pool, const CacheGroup &g,
+                int tokens) {
   const cuuint64_t row = (cuuint64_t)c->dev.row_bytes, P = (cuuint64_t)c->dev.P;
   const cuuint64_t n = (cuuint64_t)g.size, pages = (cuuint64_t)g.pages, halves = row / 128;
-  const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)P / 8, 1};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)tokens / 8, 1};
   if (c->dev.token_major) {
     const cuuint64_t dims[5] = {64, 8, halves, pages * P / 8, n};
     const cuuint64_t strides[4] = {row * n, 128, 8 * row * n, row};
@@ -141,8 +142,8 @@ int window_shape(const kvx_cache *c, int max_q, bool weigh, WindowShape *t) {
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
   const int g = c->dev.g;
-  t->blocks = sms * window_simt_blocks_per_sm();
-  t->rows = window_simt_rows();
+  t->blocks = sms * kWindowBlocksPerSm;
+  t->rows = c->shape.dtype == KVX_F32 ? window_simt_rows() : window_mma_rows(max_q * g);
   t->tokens = t->rows / g;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);
@@ -262,9 +263,12 @@ extern "C" int kvx_cache_create(const kvx_shape *s, const int32_t *head_group,
   c->stall_block = -1;
   c->wait_ns = 2000000000u;
   c->have_maps = s->dtype == KVX_BF16;
+  const int box = std::min(d.P, kWindowBox);
   for (int gi = 0; gi < G && c->have_maps; ++gi)
-    c->have_maps = encode_map(&c->k_maps[gi], c, d.grp[gi].k, d.grp[gi]) &&
-                   encode_map(&c->v_maps[gi], c, d.grp[gi].v, d.grp[gi]);
+    c->have_maps = encode_map(&c->k_maps[gi], c, d.grp[gi].k, d.grp[gi], d.P) &&
+                   encode_map(&c->v_maps[gi], c, d.grp[gi].v, d.grp[gi], d.P) &&
+                   encode_map(&c->k_boxes[gi], c, d.grp[gi].k, d.grp[gi], box) &&
+                   encode_map(&c->v_boxes[gi], c, d.grp[gi].v, d.grp[gi], box);
   *out = c;
   return KVX_OK;
 }
@@ -482,7 +486,8 @@ extern "C" int kvx_window_attn(const kvx_cache *c, const void *q, int64_t q_stri
   if (!std::isfinite(scale) || scale < 0.f) return KVX_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned_ints({q_start, kv_len, sinks, window}))
     return KVX_EINVAL;
-  WindowParams p;
+  WindowMmaParams mp;
+  WindowParams &p = mp.w;
   std::memset((void *)&p, 0, sizeof(p));
   p.c = c->dev;
   p.q_stride = row_stride(c, q_stride, c->dev.Hq);
@@ -518,7 +523,7 @@ extern "C" int kvx_window_attn(const kvx_cache *c, const void *q, int64_t q_stri
   }
   p.max_rows = max_rows;
   p.max_q = max_q;
-  p.stall_block = -1;
+  p.stall_block = c->stall_block;
   p.wait_ns = c->wait_ns;
   p.group_tokens = t.tokens;
   p.group_rows = t.rows;
@@ -526,7 +531,16 @@ extern "C" int kvx_window_attn(const kvx_cache *c, const void *q, int64_t q_stri
   const float sc = scale == 0.f ? 1.0f / std::sqrt((float)c->dev.D) : scale;
   p.scale_log2 = (float)((double)sc * 1.4426950408889634);
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_window_simt(p, c->shape.dtype, t.blocks, st);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (c->shape.dtype == KVX_F32) {
+    e = launch_window_simt(p, t.blocks, st);
+  } else if (c->shape.dtype == KVX_Q4) {
+    e = launch_window_q4(mp, t.blocks, st);
+  } else if (c->have_maps) {
+    std::memcpy(mp.tmK, c->k_boxes, sizeof(mp.tmK));
+    std::memcpy(mp.tmV, c->v_boxes, sizeof(mp.tmV));
+    e = launch_window_bf16(mp, t.blocks, st);
+  }
   if (e == cudaSuccess) e = launch_tree_merge(p, t.blocks, st);
   if (e == cudaSuccess && weights) e = launch_weigh(p, t.blocks, st);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);

@@ -146,6 +146,9 @@ struct kvx_cache {
   // bf16 caches: maps of each group's pools (absent where no driver is loaded)
   CUtensorMap k_maps[KVX_MAX_GROUPS];
   CUtensorMap v_maps[KVX_MAX_GROUPS];
+  // the same, boxes of at most 32 tokens (window attention)
+  CUtensorMap k_boxes[KVX_MAX_GROUPS];
+  CUtensorMap v_boxes[KVX_MAX_GROUPS];
   bool have_maps;
   int32_t stall_block;  // kvx_cache_inject_stall
   uint32_t wait_ns;

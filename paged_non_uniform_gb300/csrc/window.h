@@ -29,6 +29,7 @@ __host__ __device__ inline int64_t q4_params(const CacheDev &c, int64_t row) {
 
 // ---- attention ------------------------------------------------------------
 constexpr int kWindowTile = 64;  // keys of a tile
+constexpr int kWindowBox = 32;   // of a stage of the tensor-core kernels, and of a load at most
 
 struct WindowParams : TreeParams {
   const int32_t *sinks, *window;  // [Hkv], or null: no sinks, everything visible
@@ -49,9 +50,21 @@ struct WindowShape {
   size_t row_ml, split_row, scores, total;
 };
 
-cudaError_t launch_window_simt(const WindowParams &p, int dtype, int blocks, cudaStream_t st);
-int window_simt_rows();           // query rows of a row group
-int window_simt_blocks_per_sm();  // resident blocks
+// Tensor-core kernels' parameters.
+struct alignas(128) WindowMmaParams {
+  CUtensorMap tmK[KVX_MAX_GROUPS];  // bf16 caches
+  CUtensorMap tmV[KVX_MAX_GROUPS];
+  WindowParams w;
+};
+
+// fp32 caches: CUDA cores; bf16 and 4-bit caches: tensor cores.
+cudaError_t launch_window_simt(const WindowParams &p, int blocks, cudaStream_t st);
+cudaError_t launch_window_bf16(const WindowMmaParams &p, int blocks, cudaStream_t st);
+cudaError_t launch_window_q4(const WindowMmaParams &p, int blocks, cudaStream_t st);
+int window_simt_rows();  // query rows of a row group
+// of the tensor-core kernels, where a head has `rows` in all: one instance each
+constexpr int window_mma_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+constexpr int kWindowBlocksPerSm = 2;
 cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st);
 
 // ---- rows of 4-bit caches, rows read back ----------------------------------

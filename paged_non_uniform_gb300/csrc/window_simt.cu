@@ -1,10 +1,10 @@
 // window_simt.cu -- attention with a sliding window and sink tokens over a paged
-// cache, on the CUDA cores, and its accumulated weights.
+// fp32 cache, on the CUDA cores.
 //
 // out[row] = sum_t softmax(scale * <q_row, k_t>)_t v_t over the keys that the row sees
 // (window_split.cuh), in one pass over the visited tiles of 64 keys per group of 32 query
 // rows (running maximum and sum in fp32). K and V tiles are gathered from their
-// pages into shared memory as fp32; each thread computes a 4 x 4 block of scores and
+// pages into shared memory; each thread computes a 4 x 4 block of scores and
 // accumulates 4 rows x D/16 dims of the output. A tile that some row sees only in part
 // takes a separate path that skips what a row does not see instead of multiplying
 // it by zero, so that NaN and infinities in unseen rows, and padding, have no influence.
@@ -31,39 +31,13 @@ struct Smem {
   TreeRange range;
 };
 
-// Elements 4c .. 4c + 3 of a pool's row.
-template <int D, int kDtype>
-__device__ __forceinline__ float4 load4(const CacheDev &cd, const char *pool, int64_t row, int c) {
-  if constexpr (kDtype == KVX_F32) {
-    return *(const float4 *)(pool + row * (D * 4) + c * 16);
-  } else if constexpr (kDtype == KVX_BF16) {
-    const uint2 x = *(const uint2 *)(pool + row * (D * 2) + c * 8);
-    const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-  } else {
-    const int w = c >> 1, at = D == 128 ? 2 * (w & 7) + (w >> 3) : w;
-    const uint32_t x = *(const uint16_t *)(pool + q4_codes(cd, row) + at * 4 + (c & 1) * 2);
-    const float2 p = unpack_bf16(*(const uint32_t *)(pool + q4_params(cd, row) + (w >> 3) * 4));
-    return make_float4(fmaf(p.x, (float)(x & 15), p.y), fmaf(p.x, (float)(x >> 4 & 15), p.y),
-                       fmaf(p.x, (float)(x >> 8 & 15), p.y), fmaf(p.x, (float)(x >> 12), p.y));
-  }
-}
-template <int D, int kDtype>
-__device__ __forceinline__ float4 load_q(const char *row, int c) {
-  if constexpr (kDtype == KVX_F32) return *(const float4 *)(row + c * 16);
-  const uint2 x = *(const uint2 *)(row + c * 8);
-  const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-
-template <int D, int kDtype>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D>
+__global__ void __launch_bounds__(kThreads, kWindowBlocksPerSm)
     window_simt_kernel(const __grid_constant__ WindowParams p) {
   extern __shared__ float4 smem_raw[];
   Smem<D> &sm = *(Smem<D> *)smem_raw;
   constexpr int CPR = D / 4;  // 4-element chunks of a row
   constexpr int ND = D / 64;
-  constexpr int kItem = kDtype == KVX_F32 ? 4 : 2;  // bytes of a query element
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_launch_dependents();
   pdl_wait();
@@ -86,8 +60,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
         const int nr = tree_div_g(p, r), j = r - nr * g;
-        x = load_q<D, kDtype>(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
-                                  ((size_t)hd.h * g + j) * (D * kItem), c);
+        x = *(const float4 *)(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride +
+                              ((size_t)hd.h * g + j) * (D * 4) + c * 16);
       }
       *(float4 *)&sm.q[r][c * 4] = x;
     }
@@ -110,9 +84,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int tok = t0 + t;
           const int page = table[tok >> p.c.lgP];
           if (page >= 0 && page < grp.pages) {
-            const int64_t at = pool_row(p.c, grp, page, rank, tok & (P - 1));
-            dk = load4<D, kDtype>(p.c, grp.k, at, c);
-            dv = load4<D, kDtype>(p.c, grp.v, at, c);
+            const int64_t at = pool_row(p.c, grp, page, rank, tok & (P - 1)) * (D * 4) + c * 16;
+            dk = *(const float4 *)(grp.k + at);
+            dv = *(const float4 *)(grp.v + at);
           } else if (c == 0) {
             atomicOr(p.status, KVX_DEV_BAD_PAGE);
           }
@@ -263,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) tree_describe(p, range, any ? &it : nullptr);
 }
 
-template <int D, int kDtype>
+template <int D>
 cudaError_t launch_d(const WindowParams &p, int blocks, cudaStream_t st) {
   const int bytes = (int)sizeof(Smem<D>);
   static int8_t done[64];
-  cudaError_t e = raise_smem_limit(done, (const void *)window_simt_kernel<D, kDtype>, bytes);
+  cudaError_t e = raise_smem_limit(done, (const void *)window_simt_kernel<D>, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -279,24 +253,16 @@ cudaError_t launch_d(const WindowParams &p, int blocks, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, window_simt_kernel<D, kDtype>, p);
+  e = cudaLaunchKernelEx(&cfg, window_simt_kernel<D>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_t(const WindowParams &p, int dtype, int blocks, cudaStream_t st) {
-  if (dtype == KVX_F32) return launch_d<D, KVX_F32>(p, blocks, st);
-  if (dtype == KVX_BF16) return launch_d<D, KVX_BF16>(p, blocks, st);
-  return launch_d<D, KVX_Q4>(p, blocks, st);
 }
 
 }  // namespace
 
 int window_simt_rows() { return kRows; }
-int window_simt_blocks_per_sm() { return 2; }
 
-cudaError_t launch_window_simt(const WindowParams &p, int dtype, int blocks, cudaStream_t st) {
-  return p.c.D == 128 ? launch_t<128>(p, dtype, blocks, st) : launch_t<64>(p, dtype, blocks, st);
+cudaError_t launch_window_simt(const WindowParams &p, int blocks, cudaStream_t st) {
+  return p.c.D == 128 ? launch_d<128>(p, blocks, st) : launch_d<64>(p, blocks, st);
 }
 
 }  // namespace kvx
