@@ -143,7 +143,7 @@ int window_shape(const kvx_cache *c, int max_q, bool weigh, WindowShape *t) {
   if (rc != KVX_OK) return rc;
   const int g = c->dev.g;
   t->blocks = sms * kWindowBlocksPerSm;
-  t->rows = c->shape.dtype == KVX_F32 ? window_simt_rows() : window_mma_rows(max_q * g);
+  t->rows = c->shape.dtype == KVX_F32 ? window_simt_rows() : window_mma_rows(max_q * g, c->shape.dtype == KVX_Q4);
   t->tokens = t->rows / g;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);

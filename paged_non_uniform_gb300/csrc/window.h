@@ -63,7 +63,9 @@ cudaError_t launch_window_bf16(const WindowMmaParams &p, int blocks, cudaStream_
 cudaError_t launch_window_q4(const WindowMmaParams &p, int blocks, cudaStream_t st);
 int window_simt_rows();  // query rows of a row group
 // of the tensor-core kernels, where a head has `rows` in all: one instance each
-constexpr int window_mma_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+constexpr int window_mma_rows(int rows, bool q4) {
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || q4 ? 16 : 32;
+}
 constexpr int kWindowBlocksPerSm = 2;
 cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st);
 
