@@ -161,16 +161,21 @@ int window_shape(const kvx_cache *c, int max_q, bool weigh, WindowShape *t) {
   return KVX_OK;
 }
 
-// Units of an eviction, at most: every chunk that the page tables have room for.
-int64_t evict_units(const kvx_cache *c) {
-  int64_t n = 0;
-  for (int h = 0; h < c->dev.Hkv; ++h)
-    n += (int64_t)c->dev.B *
-         ((c->dev.grp[c->dev.head_grp[h]].tokens + (int64_t)kEvictChunk - 1) / kEvictChunk);
+// Chunks of all heads' page tables, and the workspace of an eviction.
+int64_t evict_shape(const kvx_cache *c, EvictParams *p, EvictWs *w) {
+  int64_t seq = 0;
+  for (int h = 0; h < c->dev.Hkv; ++h) {
+    if (p) p->chunk_off[h] = (int32_t)seq;
+    seq += (c->dev.grp[c->dev.head_grp[h]].tokens + (int64_t)kEvictChunk - 1) / kEvictChunk;
+  }
+  const int64_t n = seq * c->dev.B;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  w->read_done = KVX_WS_HEADER_BYTES + up(n * sizeof(EvictUnit));
+  w->rank = w->read_done + up(n * sizeof(uint32_t));
+  w->source = w->rank + up(n * sizeof(int32_t));
+  w->total = w->source + up(n * kEvictChunk * sizeof(int32_t));
+  if (p) p->chunks = n, p->chunks_seq = seq;
   return n;
-}
-size_t evict_flags(const kvx_cache *c) {  // where the units' flags are in the workspace
-  return KVX_WS_HEADER_BYTES + (size_t)evict_units(c) * sizeof(EvictUnit);
 }
 
 }  // namespace
@@ -548,7 +553,9 @@ extern "C" int kvx_window_attn(const kvx_cache *c, const void *q, int64_t q_stri
 
 extern "C" int kvx_evict_workspace_bytes(const kvx_cache *c, size_t *bytes) {
   if (!c || !bytes) return KVX_EINVAL;
-  *bytes = evict_flags(c) + ((size_t)evict_units(c) * sizeof(uint32_t) + 255) / 256 * 256;
+  EvictWs w;
+  if (evict_shape(c, nullptr, &w) >= (int64_t)UINT32_MAX) return KVX_ERANGE;
+  *bytes = w.total;
   return KVX_OK;
 }
 
@@ -559,11 +566,11 @@ extern "C" int kvx_evict(const kvx_cache *c, const int32_t *kv_len, const int32_
   if (!c || !kv_len || !budget || !weights || !weights_out || !kv_len_out) return KVX_EINVAL;
   if (sinks < 0 || recent < 0) return KVX_EINVAL;
   if (!aligned_ints({kv_len, budget, kv_len_out})) return KVX_EINVAL;
-  size_t need = 0;
-  kvx_evict_workspace_bytes(c, &need);
-  if (!workspace_ok(workspace, workspace_bytes, need)) return KVX_EINVAL;
   EvictParams p;
   std::memset(&p, 0, sizeof(p));
+  EvictWs w;
+  if (evict_shape(c, &p, &w) >= (int64_t)UINT32_MAX) return KVX_ERANGE;
+  if (!workspace_ok(workspace, workspace_bytes, w.total)) return KVX_EINVAL;
   p.c = c->dev;
   p.kv_len = kv_len;
   p.budget = budget;
@@ -571,22 +578,23 @@ extern "C" int kvx_evict(const kvx_cache *c, const int32_t *kv_len, const int32_
   p.sinks = sinks;
   p.recent = recent;
   p.q4 = c->shape.dtype == KVX_Q4;
+  int same = 0;
   for (int gi = 0; gi < c->dev.G; ++gi) {
-    if (!weights[gi] || !weights_out[gi] || !aligned(weights[gi], 4) || !aligned(weights_out[gi], 4))
+    if (!weights[gi] || !weights_out[gi] || !aligned_ints({weights[gi], weights_out[gi]}))
       return KVX_EINVAL;
     p.weights[gi] = weights[gi];
     p.weights_out[gi] = weights_out[gi];
-    p.copy_weights |= weights[gi] != weights_out[gi];
+    same += weights[gi] == weights_out[gi];
   }
-  // all in place or all elsewhere
-  for (int gi = 0; gi < c->dev.G; ++gi)
-    if (p.copy_weights && weights[gi] == weights_out[gi]) return KVX_EINVAL;
+  if (same != 0 && same != c->dev.G) return KVX_EINVAL;  // all in place, or all elsewhere
+  p.copy_weights = same == 0;
   char *ws = (char *)workspace;
   p.status = (uint32_t *)ws;
   p.counters = (uint32_t *)ws + 16;
   p.units = (EvictUnit *)(ws + KVX_WS_HEADER_BYTES);
-  p.read_done = (uint32_t *)(ws + evict_flags(c));
-  p.max_units = evict_units(c);
+  p.read_done = (uint32_t *)(ws + w.read_done);
+  p.rank = (int32_t *)(ws + w.rank);
+  p.source = (int32_t *)(ws + w.source);
   p.wait_ns = c->wait_ns;
   const cudaError_t e = launch_evict(p, (cudaStream_t)stream);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);

@@ -7,10 +7,10 @@
 // First launch: a cluster of blocks per head, each with a run of the head's tokens. Weights
 // become 32-bit keys of the same order; four passes of 8-bit digits find the cut (histograms
 // of the cluster's blocks are added through distributed shared memory), counts of the
-// runs give every 64-token chunk its place. It leaves a list of units: chunk, tokens that
-// stay, where they go.
+// runs give every kept token its place. It leaves the list of kept tokens, how many stay
+// before every chunk of 64, and a list of units: 64 places of a head.
 // Second launch: blocks take units by ticket. A unit reads its rows, says so, waits until
-// the units that hold its targets have read theirs (rows move towards the front, so those are
+// the units that read its places have done so (rows move towards the front, so those are
 // earlier units of the head, which running blocks have taken before, and no unit waits
 // before it has read), and writes. So a head moves on all SMs at once, in place, with
 // one read and one write of every row that moves.
@@ -23,10 +23,7 @@
 namespace kvx {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kChunk = kEvictChunk;
-constexpr int kKeys = 8192;  // keys of a block's run that are kept in shared memory
-static_assert(kThreads == 4 * kChunk, "a step of the placing pass is four chunks");
 
 // Order-preserving key: larger weight, larger key; -0 as 0; NaN below everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -57,19 +54,24 @@ __device__ __forceinline__ Head load_head(const EvictParams &p, int bh, bool rep
   return hd;
 }
 
+// kThreads threads, kKeys keys of a block's run kept in shared memory (a longer run reads the
+// others again in every pass).
+template <int kThreads, int kKeys>
 struct SelectSmem {
   uint32_t keys[kKeys];
   uint32_t hist[2][256];
-  uint32_t total[256];
-  uint32_t warp_sum[8];
-  uint32_t count[2];  // keys of this block's run above the cut, equal to it
-  uint32_t cut, left;  // digits found; keys still to take among those that share them
-  uint32_t start;      // rank 0: the head's first unit
-  uint32_t words[2][8];
+  uint32_t warp_sum[2][kThreads / 32];
+  uint32_t count[2];     // keys of this block's run that stay for certain, and equal to the cut
+  uint32_t cut, left;    // digits found; keys still to take among those that share them
+  uint32_t start;        // rank 0: the head's first unit
+  uint32_t above[kKeys / 32], equal[kKeys / 32];
 };
 
+template <int kThreads, int kKeys>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ SelectSmem sm;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ uint4 smem_raw[];
+  SelectSmem<kThreads, kKeys> &sm = *(SelectSmem<kThreads, kKeys> *)smem_raw;
   pdl_launch_dependents();
   pdl_wait();
   uint32_t C;
@@ -85,55 +87,79 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const int chunks = (hd.n + kChunk - 1) / kChunk, per = (chunks + (int)C - 1) / (int)C;
   const int c_lo = min(chunks, (int)rank * per), c_hi = min(chunks, c_lo + per);
   const int t_lo = c_lo * kChunk, t_hi = min(hd.n, c_hi * kChunk);
-  const int first_chunk = p.copy_weights ? 0 : hd.first / kChunk;
-  const int units = hd.evict || p.copy_weights ? max(0, chunks - first_chunk) : 0;
+  const int first_unit = p.copy_weights ? 0 : hd.first / kChunk;
+  const int units = hd.evict || p.copy_weights ? max(0, (hd.m + kChunk - 1) / kChunk - first_unit) : 0;
+  const int64_t base = (int64_t)hd.b * p.chunks_seq + p.chunk_off[hd.h];  // of the head's chunks
 
-  auto load_key = [&](int t) -> uint32_t {
-    const int page = table[t >> p.c.lgP];
+  auto load_key = [&](int t, int page) -> uint32_t {
     if (page < 0 || page >= grp.pages) return 0u;
     return weight_key(weights[pool_row(p.c, grp, page, row, t & (p.c.P - 1))]);
   };
   auto key = [&](int t) -> uint32_t {
-    return t - t_lo < kKeys ? sm.keys[t - t_lo] : load_key(t);
+    return t - t_lo < kKeys ? sm.keys[t - t_lo] : load_key(t, table[t >> p.c.lgP]);
   };
   const int a_lo = max(t_lo, hd.first), a_hi = min(t_hi, hd.last);  // this run's part that competes
-  if (rank == 0 && tid == 0) {
-    sm.start = units ? atomicAdd(p.counters, (uint32_t)units) : 0u;
-    sm.cut = 0;
-  }
+  if (rank == 0 && tid == 0) sm.start = units ? atomicAdd(p.counters, (uint32_t)units) : 0u;
+  // All blocks of the head have written what the others read next.
+  auto meet = [&]() {
+    __syncthreads();
+    if (C > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
+  };
   uint32_t prefix = 0, left = 0;  // found digits; keys to take among those that share them
   if (hd.evict) {
     left = (uint32_t)(hd.m - hd.first - (hd.n - hd.last));
-    for (int t = t_lo + tid; t < min(t_hi, t_lo + kKeys); t += kThreads) sm.keys[t - t_lo] = load_key(t);
+    const int end = min(t_hi, t_lo + kKeys);
+    for (int t0 = t_lo + tid; t0 < end; t0 += 8 * kThreads) {  // eight in flight
+      int page[8];
+      uint32_t k[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) page[u] = t0 + u * kThreads < end ? table[(t0 + u * kThreads) >> p.c.lgP] : -1;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k[u] = load_key(t0 + u * kThreads, page[u]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t0 + u * kThreads < end) sm.keys[t0 + u * kThreads - t_lo] = k[u];
+    }
   }
-  // left = 0: nothing of the middle stays (no key passes the cut)
+  // (left = 0: nothing of the middle stays)
   for (int pass = 0; pass < 4 && hd.evict && left; ++pass) {
     uint32_t *hist = sm.hist[pass & 1];
-    hist[tid] = 0;
+    if (tid < 256) hist[tid] = 0;
     __syncthreads();
     const int shift = 24 - 8 * pass;
-    for (int t = a_lo + tid; t < a_hi; t += kThreads) {
-      const uint32_t k = key(t);
-      if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[k >> shift & 255u], 1u);
+    for (int t0 = a_lo + 32 * warp; t0 < a_hi; t0 += kThreads) {
+      const int t = t0 + lane;
+      const uint32_t k = t < a_hi ? key(t) : 0u;
+      const bool in = t < a_hi && (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+      const uint32_t digit = in ? k >> shift & 255u : 256u;
+      // Weights share a few leading digits: one add for the lanes of a digit.
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], (uint32_t)__popc(same));
     }
-    __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    meet();
     // bin 255 - tid of all blocks, and the keys in higher bins
-    uint32_t own = 0;
-    const uint32_t at = smem_u32(&hist[255 - tid]);
-    for (uint32_t r = 0; r < C; ++r) own += ld_cluster_u32(mapa_shared(at, r));
-    uint32_t x = own;
+    uint32_t own = 0, x = 0;
+    if (tid < 256) {
+      const uint32_t at = smem_u32(&hist[255 - tid]);
+      if (C == 1)
+        own = hist[255 - tid];
+      else
+        for (uint32_t r = 0; r < C; ++r) own += ld_cluster_u32(mapa_shared(at, r));
+      x = own;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (lane == 31) sm.warp_sum[0][warp] = x;
     }
-    if (lane == 31) sm.warp_sum[warp] = x;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) x += sm.warp_sum[w];
-    if (x >= left && x - own < left) {
+    if (tid < 256)
+      for (int w = 0; w < warp; ++w) x += sm.warp_sum[0][w];
+    if (tid < 256 && x >= left && x - own < left) {
       sm.cut = prefix | (uint32_t)(255 - tid) << shift;
       sm.left = left - (x - own);
     }
@@ -142,79 +168,89 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     left = sm.left;
     __syncthreads();
   }
-  const bool none = hd.evict && left == 0;
+  const bool some = hd.evict && left > 0;
   // Kept are: the front, the tail, keys above the cut, and the first `left` keys equal to it.
-  auto above = [&](int t) {
-    return t < hd.n && (!hd.evict || t < hd.first || t >= hd.last || (!none && key(t) > prefix));
-  };
-  auto equal = [&](int t) {
-    return hd.evict && !none && t >= hd.first && t < hd.last && key(t) == prefix;
-  };
+  // Bits of the words of 32 tokens from t0 on, kKeys tokens at most; counts of both kinds.
   uint32_t na = 0, ne = 0;
-  for (int t = t_lo + tid; t < t_hi; t += kThreads) {
-    na += above(t);
-    ne += equal(t);
-  }
+  auto mark = [&](int t0) {
+    for (int w0 = warp; w0 < kKeys / 32 && t0 + 32 * w0 < t_hi; w0 += kThreads / 32) {
+      const int t = t0 + 32 * w0 + lane;
+      const bool in = t < t_hi, mid = in && hd.evict && t >= hd.first && t < hd.last;
+      const uint32_t k = mid && some ? key(t) : 0u;
+      const uint32_t ab = __ballot_sync(0xffffffffu, in && (!mid || (some && k > prefix)));
+      const uint32_t eq = __ballot_sync(0xffffffffu, mid && some && k == prefix);
+      if (lane == 0) {
+        sm.above[w0] = ab;
+        sm.equal[w0] = eq;
+      }
+      na += __popc(ab);
+      ne += __popc(eq);
+    }
+  };
   if (tid < 2) sm.count[tid] = 0;
   __syncthreads();
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    na += __shfl_xor_sync(0xffffffffu, na, d);
-    ne += __shfl_xor_sync(0xffffffffu, ne, d);
-  }
+  for (int t0 = t_lo; t0 < t_hi; t0 += kKeys) mark(t0);
   if (lane == 0) {
     atomicAdd(&sm.count[0], na);
     atomicAdd(&sm.count[1], ne);
   }
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-  uint32_t before = 0, equals = 0;  // kept, and keys equal to the cut, in the runs before
+  meet();
+  uint32_t before = 0, equals = 0;  // kept for certain, and equal to the cut, in the runs before
   for (uint32_t r = 0; r < rank; ++r) {
     before += ld_cluster_u32(mapa_shared(smem_u32(&sm.count[0]), r));
     equals += ld_cluster_u32(mapa_shared(smem_u32(&sm.count[1]), r));
   }
-  before += min(equals, left);
-  const uint32_t start = ld_cluster_u32(mapa_shared(smem_u32(&sm.start), 0));
+  const uint32_t start = C == 1 ? sm.start : ld_cluster_u32(mapa_shared(smem_u32(&sm.start), 0));
   if (rank == 0 && tid == 0)  // (all blocks of the head have read its length)
     p.kv_out[bh] = hd.n ? hd.m : p.kv_len[bh];
-  if (units)
-    for (int c0 = c_lo; c0 < c_hi; c0 += kThreads / kChunk) {
-      const int t = c0 * kChunk + tid;
-      const bool in = t < t_hi, ab = in && above(t), eq = in && equal(t);
-      const uint32_t eb = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) sm.words[0][warp] = __popc(eb);
+  for (int i = (int)rank * kThreads + tid; i < units; i += (int)C * kThreads) {
+    p.units[start + i] = {bh, first_unit + i};
+    p.read_done[start + i] = 0;
+  }
+  // Places: exclusive sums over the words of a segment of kKeys tokens.
+  static_assert(kKeys / 32 <= kThreads, "a thread a word");
+  for (int t0 = t_lo; t0 < t_hi && units; t0 += kKeys) {
+    if (t_hi - t_lo > kKeys) {  // (else the words are still there)
       __syncthreads();
-      uint32_t e = equals, e_all = 0;
-      for (int w = 0; w < 8; ++w) {
-        if (w < warp) e += sm.words[0][w];
-        e_all += sm.words[0][w];
-      }
-      const bool keep = ab || (eq && e + __popc(eb & ((1u << lane) - 1u)) < left);
-      const uint32_t bits = __ballot_sync(0xffffffffu, keep);
-      if (lane == 0) sm.words[1][warp] = bits;
-      __syncthreads();
-      if (tid < kThreads / kChunk && c0 + tid < c_hi && c0 + tid >= first_chunk) {
-        uint32_t k = before;
-        for (int w = 0; w < 2 * tid; ++w) k += __popc(sm.words[1][w]);
-        const uint32_t u = start + (uint32_t)(c0 + tid - first_chunk);
-        EvictUnit un;
-        un.bh = bh;
-        un.chunk = c0 + tid;
-        un.first = (int)k;
-        un.first_chunk = first_chunk;
-        un.keep[0] = sm.words[1][2 * tid];
-        un.keep[1] = sm.words[1][2 * tid + 1];
-        un.pad[0] = un.pad[1] = 0;
-        p.units[u] = un;
-        p.read_done[u] = 0;
-      }
-      for (int w = 0; w < 8; ++w) before += __popc(sm.words[1][w]);
-      equals += e_all;
-      __syncthreads();
+      mark(t0);
     }
-  cluster_arrive();  // nobody leaves while its shared memory may be read
-  cluster_wait();
+    __syncthreads();
+    const bool in = tid < kKeys / 32 && t0 + 32 * tid < t_hi;
+    const uint32_t ab = in ? sm.above[tid] : 0u, eq = in ? sm.equal[tid] : 0u;
+    uint32_t xa = __popc(ab), xe = __popc(eq);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t ya = __shfl_up_sync(0xffffffffu, xa, d), ye = __shfl_up_sync(0xffffffffu, xe, d);
+      if (lane >= d) xa += ya, xe += ye;
+    }
+    if (lane == 31) sm.warp_sum[0][warp] = xa, sm.warp_sum[1][warp] = xe;
+    __syncthreads();
+    uint32_t all_a = 0, all_e = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t sa = sm.warp_sum[0][w], se = sm.warp_sum[1][w];
+      if (w < warp) xa += sa, xe += se;
+      all_a += sa, all_e += se;
+    }
+    const uint32_t e0 = equals + xe - __popc(eq);  // equal keys before this word
+    uint32_t keep = ab, take = min(left > e0 ? left - e0 : 0u, (uint32_t)__popc(eq));
+    for (uint32_t rest = eq; take; --take, rest &= rest - 1) keep |= rest & (0u - rest);
+    const uint32_t at = before + xa - __popc(ab) + min(e0, left);  // kept before this word
+    __syncthreads();  // (the words and sums have been read)
+    if (in) {
+      sm.above[tid] = keep;
+      sm.equal[tid] = at;
+      if ((tid & 1) == 0) p.rank[base + (t0 >> 6) + (tid >> 1)] = (int)at;
+    }
+    before += all_a;
+    equals += all_e;
+    __syncthreads();
+    for (int w = warp; w < kKeys / 32 && t0 + 32 * w < t_hi; w += kWarps) {
+      const uint32_t k = sm.above[w];
+      if (k >> lane & 1u)
+        p.source[base * kChunk + sm.equal[w] + __popc(k & ((1u << lane) - 1u))] = t0 + 32 * w + lane;
+    }
+  }
+  meet();  // nobody leaves while its shared memory may be read
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
@@ -226,90 +262,154 @@ __device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
   asm volatile("st.release.gpu.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// What is known of a unit before its rows are read.
+struct Places {
+  int64_t src[kChunk], dst[kChunk];  // pool rows; -1: a page outside the pool
+  int32_t bh, chunk, count, wait_from;  // wait_from: first chunk whose unit must have read
+  uint32_t unit, end;                   // end: no unit, nothing comes after it
+};
+constexpr int kMovers = 256, kScouts = kChunk;
+constexpr int kRing = 3;  // units whose places are known: written, read, looked up
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Named barriers: a ring slot's places are there (1 ..), the slot is free (4 ..), movers (7).
+constexpr int kFull = 1, kFree = kFull + kRing, kMove = kFree + kRing;
+
 // kPieces pieces of type V make a row's K, as many its V. 4-bit rows: the last piece is the
-// row's parameters.
+// row's parameters. Two warps look up the places of the units to come; the others read unit
+// i + 1 before they wait for the units before unit i and write it, so that a unit is
+// read long before another one needs that.
 template <class V, int kPieces, bool kQ4>
-__global__ void __launch_bounds__(kThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kRow = 2 * kPieces;
-  constexpr int kEach = (kChunk * kRow + kThreads - 1) / kThreads;  // pieces of a thread
-  __shared__ int64_t src[kChunk], dst[kChunk];  // pool rows; dst -1: stays where it is
+  constexpr int kEach = (kChunk * kRow + kMovers - 1) / kMovers;  // pieces of a thread
+  __shared__ Places ring[kRing];
   __shared__ uint32_t ticket;
-  __shared__ int ok_all;
-  pdl_wait();
+  __shared__ int failed;
   const int tid = threadIdx.x;
-  const uint32_t total = p.counters[0];
-  for (;;) {
-    __syncthreads();  // the unit before is done
-    if (tid == 0) ticket = atomicAdd(p.counters + 1, 1u);
-    __syncthreads();
-    const uint32_t u = ticket;
-    if (u >= total) break;
-    const EvictUnit un = p.units[u];
-    const int b = un.bh / p.c.Hkv, h = un.bh - b * p.c.Hkv;
-    const int gi = p.c.head_grp[h], row = p.c.head_row[h];
-    const CacheGroup &grp = p.c.grp[gi];
-    const int n0 = __popc(un.keep[0]), cnt = n0 + __popc(un.keep[1]);
-    float w = 0.f;
-    int64_t w_to = -1;
-    if (tid < kChunk && (un.keep[tid >> 5] >> (tid & 31) & 1u)) {
-      const int32_t *table = grp.table + (size_t)b * grp.stride;
-      const int j = (tid >> 5 ? n0 : 0) + __popc(un.keep[tid >> 5] & ((1u << (tid & 31)) - 1u));
-      const int from = un.chunk * kChunk + tid, to = un.first + j;
-      const int pf = table[from >> p.c.lgP], pt = table[to >> p.c.lgP];
-      const bool have = pf >= 0 && pf < grp.pages && pt >= 0 && pt < grp.pages;
-      if (!have) atomicOr(p.status, KVX_DEV_BAD_PAGE);
-      src[j] = have ? pool_row(p.c, grp, pf, row, from & (p.c.P - 1)) : 0;
-      const int64_t at = have ? pool_row(p.c, grp, pt, row, to & (p.c.P - 1)) : -1;
-      dst[j] = from == to ? -1 : at;
-      if (have && (p.copy_weights || from != to)) {
-        w_to = at;
-        w = p.weights[gi][src[j]];
+  if (tid == 0) failed = 0;
+  __syncthreads();
+  pdl_wait();
+  if (tid >= kMovers) {
+    const int j = tid - kMovers;  // the unit's row
+    const uint32_t total = p.counters[0];
+    for (int i = 0;; ++i) {
+      Places &m = ring[i % kRing];
+      if (i >= kRing) bar_sync(kFree + i % kRing, kMovers + kScouts);
+      if (j == 0) ticket = atomicAdd(p.counters + 1, 1u);
+      bar_sync(kMove + 1, kScouts);
+      const uint32_t u = ticket;
+      bar_sync(kMove + 1, kScouts);
+      if (u < total) {
+        const EvictUnit un = p.units[u];
+        const int b = un.bh / p.c.Hkv, h = un.bh - b * p.c.Hkv, row = p.c.head_row[h];
+        const CacheGroup &grp = p.c.grp[p.c.head_grp[h]];
+        const int64_t base = (int64_t)b * p.chunks_seq + p.chunk_off[h];
+        const int32_t *table = grp.table + (size_t)b * grp.stride;
+        // (checked by the launch before; where kv_out is kv_len, that is the number of kept tokens)
+        const int kept = min(p.kv_len[un.bh], p.budget[un.bh]);
+        const int to = un.chunk * kChunk + j, count = min(kChunk, kept - un.chunk * kChunk);
+        int64_t src = -1, dst = -1;
+        if (j < count) {
+          const int from = p.source[base * kChunk + to];
+          const int pf = table[from >> p.c.lgP], pt = table[to >> p.c.lgP];
+          if (pf >= 0 && pf < grp.pages && pt >= 0 && pt < grp.pages) {
+            src = pool_row(p.c, grp, pf, row, from & (p.c.P - 1));
+            dst = pool_row(p.c, grp, pt, row, to & (p.c.P - 1));
+          } else {
+            atomicOr(p.status, KVX_DEV_BAD_PAGE);
+          }
+        }
+        m.src[j] = src;
+        m.dst[j] = dst;
+        if (j == 0) {
+          m.bh = un.bh;
+          m.chunk = un.chunk;
+          m.count = count;
+          m.wait_from = p.rank[base + un.chunk] / kChunk;
+          m.unit = u;
+        }
       }
+      if (j == 0) m.end = u >= total;
+      bar_arrive(kFull + i % kRing, kMovers + kScouts);
+      if (u >= total) break;
     }
-    if (tid == 0) ok_all = 1;
-    __syncthreads();
-    V x[kEach];
-    auto place = [&](int64_t r, int q) -> char * {
+  } else {
+    auto place = [&](const CacheGroup &grp, int64_t r, int q) -> char * {
       char *pool = q < kPieces ? grp.k : grp.v;
       const int i = q < kPieces ? q : q - kPieces;
       if constexpr (kQ4)
         return pool + (i < kPieces - 1 ? q4_codes(p.c, r) + i * (int)sizeof(V) : q4_params(p.c, r));
       return pool + (r * kPieces + i) * (int)sizeof(V);
     };
-    const int pieces = cnt * kRow;
+    auto moves = [&](const Places &m, int i) {
+      return i < m.count * kRow && m.dst[i / kRow] != m.src[i / kRow];
+    };
+    auto weighs = [&](const Places &m) {
+      return tid < m.count && m.dst[tid] >= 0 && (p.copy_weights || m.dst[tid] != m.src[tid]);
+    };
+    auto read = [&](const Places &m, V(&v)[kEach], float &wt) {
+      const int gi = p.c.head_grp[m.bh % p.c.Hkv];
+      const CacheGroup &grp = p.c.grp[gi];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = tid + e * kThreads;
-      if (i < pieces && dst[i / kRow] >= 0) x[e] = *(const V *)place(src[i / kRow], i % kRow);
-    }
-    __syncthreads();  // the block has read its rows and weights
-    if (tid == 0) st_release(p.read_done + u, 1u);
-    // The chunks before this one that hold targets of its rows.
-    const int lo = max(un.first_chunk, un.first / kChunk);
-    if (cnt) {
-      for (int c = lo + tid; c < un.chunk; c += kThreads) {
-        const uint32_t *flag = p.read_done + (u - (uint32_t)(un.chunk - c));
+      for (int e = 0; e < kEach; ++e) {
+        const int i = tid + e * kMovers;
+        if (moves(m, i)) v[e] = *(const V *)place(grp, m.src[i / kRow], i % kRow);
+      }
+      if (weighs(m)) wt = p.weights[gi][m.src[tid]];
+    };
+    auto write = [&](const Places &m, const V(&v)[kEach], float wt) {
+      // Units before this one that read what it overwrites.
+      for (int c = m.wait_from + tid; c < m.chunk; c += kMovers) {
+        const uint32_t *flag = p.read_done + (m.unit - (uint32_t)(m.chunk - c));
         if (ld_acquire(flag)) continue;
         const uint64_t t0 = globaltimer_ns();
         while (!ld_acquire(flag))
           if (globaltimer_ns() - t0 > p.wait_ns) {
             atomicOr(p.status, KVX_DEV_TIMEOUT);
-            ok_all = 0;
+            *(volatile int *)&failed = 1;
             break;
           }
       }
-    }
-    __syncthreads();
-    if (ok_all) {
+      bar_sync(kMove, kMovers);
+      if (*(volatile int *)&failed) return;
+      const int gi = p.c.head_grp[m.bh % p.c.Hkv];
+      const CacheGroup &grp = p.c.grp[gi];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int i = tid + e * kThreads;
-        if (i < pieces && dst[i / kRow] >= 0) *(V *)place(dst[i / kRow], i % kRow) = x[e];
+        const int i = tid + e * kMovers;
+        if (moves(m, i)) *(V *)place(grp, m.dst[i / kRow], i % kRow) = v[e];
       }
-      if (w_to >= 0) p.weights_out[gi][w_to] = w;
+      if (weighs(m)) p.weights_out[gi][m.dst[tid]] = wt;
+    };
+    // Reads unit i (false: there is none) and writes the unit before it, whose rows are in `prev`.
+    auto step = [&](int i, V(&mine)[kEach], float &w_mine, const V(&prev)[kEach], float w_prev) {
+      const Places &m = ring[i % kRing], &before = ring[(i + kRing - 1) % kRing];
+      bar_sync(kFull + i % kRing, kMovers + kScouts);
+      const bool more = !m.end;
+      if (more) {
+        read(m, mine, w_mine);
+        bar_sync(kMove, kMovers);  // the block has read its rows and weights
+        if (tid == 0) st_release(p.read_done + m.unit, 1u);
+      }
+      if (i > 0) {
+        write(before, prev, w_prev);
+        if (more) bar_arrive(kFree + (i + kRing - 1) % kRing, kMovers + kScouts);
+      }
+      return more;
+    };
+    V xa[kEach], xb[kEach];
+    float wa = 0.f, wb = 0.f;
+    for (int i = 0; step(i, xa, wa, xb, wb) && step(i + 1, xb, wb, xa, wa); i += 2) {
     }
   }
   __threadfence();
+  __syncthreads();
   // The last block to leave resets the counters for the next call.
   if (tid == 0 && atomicAdd(p.counters + 2, 1u) == gridDim.x - 1)
     p.counters[0] = p.counters[1] = p.counters[2] = 0;
@@ -318,8 +418,8 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(const __grid_const
 template <class V, int kPieces, bool kQ4>
 cudaError_t launch_move(const EvictParams &p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.max_units < 4 * 152 ? p.max_units : 4 * 152));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(p.chunks < 3 * 152 ? p.chunks : 3 * 152));
+  cfg.blockDim = dim3(kMovers + kScouts);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -330,15 +430,17 @@ cudaError_t launch_move(const EvictParams &p, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
-  const int heads = p.c.B * p.c.Hkv;
-  // A head's blocks: more where there are few heads to fill the GPU with.
-  const int C = heads <= 64 ? 8 : heads <= 256 ? 4 : heads <= 1024 ? 2 : 1;
+template <int kThreads, int kKeys>
+cudaError_t launch_select(const EvictParams &p, int C, cudaStream_t st) {
+  static int8_t done[64];
+  const int bytes = (int)sizeof(SelectSmem<kThreads, kKeys>);
+  const auto kernel = evict_select_kernel<kThreads, kKeys>;
+  cudaError_t e = raise_smem_limit(done, (const void *)kernel, bytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(heads * C));
+  cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * C));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -349,8 +451,20 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
+  // Short heads: a small block each, many to an SM. Long ones: a large block each where there are
+  // enough of them to fill half of the GPU, else clusters of up to eight.
+  const int heads = p.c.B * p.c.Hkv;
+  const int64_t longest = p.chunks / heads * kChunk;  // (their mean room)
+  int C = 1;
+  while (C < 8 && 2 * C * heads <= 152) C *= 2;
+  cudaError_t e = longest <= 4096 ? launch_select<256, 4096>(p, 1, st) : launch_select<1024, 32768>(p, C, st);
   if (e != cudaSuccess) return e;
   const bool wide = p.c.D == 128;
   if (p.q4) return wide ? launch_move<uint2, 9, true>(p, st) : launch_move<uint32_t, 9, true>(p, st);

@@ -2,8 +2,7 @@
 // cache, and rows of any cache read back from their slots.
 //
 // Quantisation of a group of 64 elements x: lo = min x (a bf16 number, so exact), step =
-// bf16((max x - lo) / 15), code = min(15, rint((x - lo) / step)) in fp32 with IEEE division;
-// codes 0 where step is 0. A group with a non-finite element, or whose range is not finite,
+// bf16((max x - lo) / 15), code = min(15, rint((x - lo) / step)) in fp32; codes 0 where step is 0. A group with a non-finite element, or whose range is not finite,
 // gets step 0 and lo NaN, so that all of it reads as NaN. Eight lanes hold a group,
 // eight elements (a 16-byte load, a 4-byte word of codes) each; minimum and maximum
 // meet in three shuffles. Memory bounds both kernels.
@@ -52,16 +51,46 @@ __device__ __forceinline__ Quantised quantise(const uint4 &x) {
   const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
   const float step = __bfloat162float(sb);
   uint32_t codes = 0;
-  if (step > 0.f)
+  if (step > 0.f) {
+    const float r = step >= 0x1p-120f ? __frcp_rn(step) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = fminf(15.f, rintf(__fdiv_rn(f[i] - lo, step)));
-      codes |= (uint32_t)c << (4 * i);
+      // rint(fl(d / step)) without the division: an estimate says between which two codes, and the sign
+      // of d - half * step, exact in one multiply-add, on which side of their middle `half`. Within half
+      // a unit in the last place of `half` the quotient would be rounded to it: ties to even.
+      const float d = f[i] - lo;
+      const float low = floorf(r > 0.f ? d * r : __fdiv_rn(d, step));
+      const float half = low + 0.5f, e = fmaf(-half, step, d);
+      const float ulp2 = __uint_as_float((__float_as_uint(half) & 0x7f800000u) - (24u << 23));
+      const uint32_t l = (uint32_t)low;
+      const uint32_t c = l + (fabsf(e) <= ulp2 * step ? l & 1u : e > 0.f ? 1u : 0u);
+      codes |= min(c, 15u) << (4 * i);
     }
+  }
   return {codes, pack_bf16(step, lo)};
 }
 
-// One lane per eight elements of a (row, head), K and V together.
+// Steps through the (row, head) pairs of a call, `step` pairs at a time, without dividing.
+struct Pairs {
+  int64_t rh;    // row * Hkv + head
+  int32_t r, h;  // (rows fit in 30 bits)
+  int32_t dr, dh;
+  int64_t step;
+  __device__ __forceinline__ Pairs(int64_t first, int64_t step_, int Hkv) : rh(first), step(step_) {
+    r = (int32_t)(first / Hkv);
+    h = (int32_t)(first - (int64_t)r * Hkv);
+    dr = (int32_t)(step_ / Hkv);
+    dh = (int32_t)(step_ - (int64_t)dr * Hkv);
+  }
+  __device__ __forceinline__ void next(int Hkv) {
+    rh += step;
+    r += dr;
+    h += dh;
+    if (h >= Hkv) h -= Hkv, ++r;
+  }
+};
+
+// One lane per eight elements of a (row, head), K and V together; two pairs in flight.
 template <int D>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;  // of a row
@@ -71,35 +100,45 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const __grid_consta
   if ((stated < 0 || stated > p.max_rows) && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   if (rows <= 0) return;
-  const int64_t total = (int64_t)rows * c.Hkv * kLanes;
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  // whole warps stay in the loop: lanes meet in shuffles
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31); i0 < total; i0 += step) {
-    const int64_t i = i0 + (threadIdx.x & 31);
-    const bool in = i < total;
-    const int64_t rh = in ? i / kLanes : 0;
-    const int w = (int)(threadIdx.x % kLanes);  // the row's word
-    const int64_t r = rh / c.Hkv;
-    const int h = (int)(rh - r * c.Hkv);
-    const int64_t slot = in ? p.slots[rh] : -1;
-    const int grp = c.head_grp[h];
-    const bool have = slot >= 0 && slot < pool_rows(c, grp);
-    if (!have && slot != -1 && w == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
-    uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-    if (have) {
-      const int64_t src = (int64_t)h * (D * 2) + w * 16;
-      kx = *(const uint4 *)(p.k + r * p.k_stride + src);
-      vx = *(const uint4 *)(p.v + r * p.v_stride + src);
+  const int64_t total = (int64_t)rows * c.Hkv;
+  const int w = (int)(threadIdx.x % kLanes);  // the row's word
+  const int at = D == 128 ? 2 * (w & 7) + (w >> 3) : w;
+  // (lanes meet in shuffles: whole warps stay in the loop, a warp's first pair decides)
+  const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
+  const int64_t lead = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / kLanes;
+  Pairs q(first, (int64_t)gridDim.x * (kThreads / kLanes), c.Hkv);
+  for (int64_t i = lead; i < total; i += 2 * q.step) {
+    int64_t slot[2];
+    int grp[2];
+    uint4 kx[2], vx[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool in = q.rh < total;
+      slot[u] = -1;
+      grp[u] = c.head_grp[q.h];
+      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+      if (in) {
+        slot[u] = p.slots[q.rh];
+        const int64_t src = (int64_t)q.h * (D * 2) + w * 16;
+        kx[u] = *(const uint4 *)(p.k + q.r * p.k_stride + src);
+        vx[u] = *(const uint4 *)(p.v + q.r * p.v_stride + src);
+      }
+      q.next(c.Hkv);
     }
-    const Quantised k = quantise(kx), v = quantise(vx);
-    if (!have) continue;
-    const int at = D == 128 ? 2 * (w & 7) + (w >> 3) : w;
-    const int64_t co = q4_codes(c, slot) + at * 4, po = q4_params(c, slot) + (w >> 3) * 4;
-    *(uint32_t *)(c.grp[grp].k + co) = k.codes;
-    *(uint32_t *)(c.grp[grp].v + co) = v.codes;
-    if ((w & 7) == 0) {
-      *(uint32_t *)(c.grp[grp].k + po) = k.params;
-      *(uint32_t *)(c.grp[grp].v + po) = v.params;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const Quantised k = quantise(kx[u]), v = quantise(vx[u]);
+      if (slot[u] < 0 || slot[u] >= pool_rows(c, grp[u])) {
+        if (slot[u] != -1 && w == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
+        continue;
+      }
+      const int64_t co = q4_codes(c, slot[u]) + at * 4, po = q4_params(c, slot[u]) + (w >> 3) * 4;
+      *(uint32_t *)(c.grp[grp[u]].k + co) = k.codes;
+      *(uint32_t *)(c.grp[grp[u]].v + co) = v.codes;
+      if ((w & 7) == 0) {
+        *(uint32_t *)(c.grp[grp[u]].k + po) = k.params;
+        *(uint32_t *)(c.grp[grp[u]].v + po) = v.params;
+      }
     }
   }
   __threadfence();
@@ -116,45 +155,56 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t params) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// out[r][h] = pool_h[slots[r][h]] for K and V; one lane per 16 bytes of a value row.
-template <bool kQ4>
+// out[r][h] = pool_h[slots[r][h]] for K and V; one lane per 16 bytes of a value row (kLanes a
+// row), two (row, head) pairs in flight.
+template <bool kQ4, int kLanes>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const CacheDev &c = p.c;
-  const int lanes = c.row_bytes >> 4;
   const int stated = p.q_start[c.B], rows = min(stated, p.max_rows);
   if ((stated < 0 || stated > p.max_rows) && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   if (rows <= 0) return;
-  const int64_t total = (int64_t)rows * c.Hkv * lanes;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kThreads) {
-    const int64_t rh = i / lanes;
-    const int w = (int)(i - rh * lanes);
-    const int64_t r = rh / c.Hkv;
-    const int h = (int)(rh - r * c.Hkv);
-    const int64_t slot = p.slots[rh];
-    const CacheGroup &g = c.grp[c.head_grp[h]];
-    if (slot < 0 || slot >= pool_rows(c, c.head_grp[h])) {
-      if (slot != -1 && w == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
-      continue;
+  const int64_t total = (int64_t)rows * c.Hkv;
+  const int w = (int)(threadIdx.x % kLanes);
+  const int at = kLanes == 16 ? 2 * (w & 7) + (w >> 3) : w;  // (4 bits: D / 8 lanes)
+  Pairs q(((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes,
+          (int64_t)gridDim.x * (kThreads / kLanes), c.Hkv);
+  while (q.rh < total) {
+    int64_t slot[2];
+    int32_t r[2], h[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      slot[u] = q.rh < total ? p.slots[q.rh] : -1;
+      r[u] = q.r;
+      h[u] = q.h;
+      q.next(c.Hkv);
     }
-    uint4 k, v;
-    if constexpr (kQ4) {
-      const int at = c.D == 128 ? 2 * (w & 7) + (w >> 3) : w;
-      const int64_t co = q4_codes(c, slot) + at * 4, po = q4_params(c, slot) + (w >> 3) * 4;
-      const uint32_t kc = *(const uint32_t *)(g.k + co), kp = *(const uint32_t *)(g.k + po);
-      const uint32_t vc = *(const uint32_t *)(g.v + co), vp = *(const uint32_t *)(g.v + po);
-      k = values8(kc, kp);
-      v = values8(vc, vp);
-    } else {
-      k = *(const uint4 *)(g.k + slot * c.row_bytes + w * 16);
-      v = *(const uint4 *)(g.v + slot * c.row_bytes + w * 16);
+    uint4 k[2], v[2];
+    uint32_t kp[2], vp[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const CacheGroup &g = c.grp[c.head_grp[h[u]]];
+      if (slot[u] < 0 || slot[u] >= pool_rows(c, c.head_grp[h[u]])) {
+        if (slot[u] != -1 && w == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
+        slot[u] = -1;
+      } else if constexpr (kQ4) {
+        const int64_t co = q4_codes(c, slot[u]) + at * 4, po = q4_params(c, slot[u]) + (w >> 3) * 4;
+        k[u].x = *(const uint32_t *)(g.k + co), kp[u] = *(const uint32_t *)(g.k + po);
+        v[u].x = *(const uint32_t *)(g.v + co), vp[u] = *(const uint32_t *)(g.v + po);
+      } else {
+        k[u] = *(const uint4 *)(g.k + slot[u] * (kLanes * 16) + w * 16);
+        v[u] = *(const uint4 *)(g.v + slot[u] * (kLanes * 16) + w * 16);
+      }
     }
-    const int64_t dst = (int64_t)h * c.row_bytes + w * 16;
-    *(uint4 *)(p.k + r * p.k_stride + dst) = k;
-    *(uint4 *)(p.v + r * p.v_stride + dst) = v;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (slot[u] < 0) continue;
+      const int64_t dst = (int64_t)h[u] * (kLanes * 16) + w * 16;
+      *(uint4 *)(p.k + r[u] * p.k_stride + dst) = kQ4 ? values8(k[u].x, kp[u]) : k[u];
+      *(uint4 *)(p.v + r[u] * p.v_stride + dst) = kQ4 ? values8(v[u].x, vp[u]) : v[u];
+    }
   }
 }
 
@@ -187,7 +237,13 @@ cudaError_t launch_q4_append(const AppendParams &p, cudaStream_t st) {
 cudaError_t launch_read(const ReadParams &p, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
   const int64_t lanes = (int64_t)p.max_rows * p.c.Hkv * (p.c.row_bytes >> 4);
-  return p.q4 ? launch(read_kernel<true>, p, lanes, st) : launch(read_kernel<false>, p, lanes, st);
+  if (p.q4)
+    return p.c.D == 128 ? launch(read_kernel<true, 16>, p, lanes, st) : launch(read_kernel<true, 8>, p, lanes, st);
+  switch (p.c.row_bytes) {
+    case 512: return launch(read_kernel<false, 32>, p, lanes, st);
+    case 256: return launch(read_kernel<false, 16>, p, lanes, st);
+    default: return launch(read_kernel<false, 8>, p, lanes, st);
+  }
 }
 
 }  // namespace kvx

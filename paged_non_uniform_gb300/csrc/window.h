@@ -83,30 +83,35 @@ struct ReadParams {
 cudaError_t launch_read(const ReadParams &p, cudaStream_t st);
 
 // ---- eviction ---------------------------------------------------------------
-// One unit of the move: `kChunk` source tokens of a head.
+// A unit of the move: kEvictChunk target places of a head. A head's arrays hold a number per
+// chunk of the tokens that its page table has room for, heads one after the other.
 constexpr int kEvictChunk = 64;
 struct EvictUnit {
-  int32_t bh, chunk;
-  int32_t first;      // tokens kept before the chunk: where its own go
-  int32_t first_chunk;  // of the head's units
-  uint32_t keep[2];   // tokens of the chunk that stay
-  int32_t pad[2];
+  int32_t bh, chunk;  // head, place / kEvictChunk
 };
 struct EvictParams {
   CacheDev c;
   const int32_t *kv_len, *budget;
   int32_t *kv_out;
   int32_t sinks, recent;
-  int32_t q4;                       // 4-bit rows
-  int32_t copy_weights;             // weights_out is not weights
+  int32_t q4;            // 4-bit rows
+  int32_t copy_weights;  // weights_out is not weights
   const float *weights[KVX_MAX_GROUPS];
   float *weights_out[KVX_MAX_GROUPS];
   uint32_t *status;
-  uint32_t *counters;               // [0] units, [1] tickets
-  EvictUnit *units;
-  uint32_t *read_done;              // [units] the unit's rows have been read
-  int64_t max_units;
+  uint32_t *counters;   // [0] units, [1] tickets, [2] blocks done
+  EvictUnit *units;     // [chunks]
+  uint32_t *read_done;  // [chunks] the unit's rows have been read
+  int32_t *rank;        // per head and chunk: tokens kept before the chunk's first
+  int32_t *source;      // per head and kept token: the token that it was
+  int64_t chunks;       // of all heads
+  int64_t chunks_seq;   // of a sequence's heads
+  int32_t chunk_off[KVX_MAX_KV_HEADS];  // where a KV head's begin among them
   uint32_t wait_ns;
+};
+// Workspace: header | units | read_done | rank | source.
+struct EvictWs {
+  size_t read_done, rank, source, total;
 };
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 
