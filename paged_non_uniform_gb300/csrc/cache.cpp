@@ -171,8 +171,7 @@ int64_t evict_shape(const kvx_cache *c, EvictParams *p, EvictWs *w) {
   const int64_t n = seq * c->dev.B;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w->read_done = KVX_WS_HEADER_BYTES + up(n * sizeof(EvictUnit));
-  w->rank = w->read_done + up(n * sizeof(uint32_t));
-  w->source = w->rank + up(n * sizeof(int32_t));
+  w->source = w->read_done + up(n * sizeof(uint32_t));
   w->total = w->source + up(n * kEvictChunk * sizeof(int32_t));
   if (p) p->chunks = n, p->chunks_seq = seq;
   return n;
@@ -593,7 +592,6 @@ extern "C" int kvx_evict(const kvx_cache *c, const int32_t *kv_len, const int32_
   p.counters = (uint32_t *)ws + 16;
   p.units = (EvictUnit *)(ws + KVX_WS_HEADER_BYTES);
   p.read_done = (uint32_t *)(ws + w.read_done);
-  p.rank = (int32_t *)(ws + w.rank);
   p.source = (int32_t *)(ws + w.source);
   p.wait_ns = c->wait_ns;
   const cudaError_t e = launch_evict(p, (cudaStream_t)stream);

@@ -5,10 +5,10 @@
 // in their order; kept token number i becomes token i.
 //
 // First launch: a cluster of blocks per head, each with a run of the head's tokens. Weights
-// become 32-bit keys of the same order; four passes of 8-bit digits find the cut (histograms
+// become 32-bit keys of the same order; three passes of 11, 11 and 10 bits find the cut (histograms
 // of the cluster's blocks are added through distributed shared memory), counts of the
-// runs give every kept token its place. It leaves the list of kept tokens, how many stay
-// before every chunk of 64, and a list of units: 64 places of a head.
+// runs give every kept token its place. It leaves the list of kept tokens and a list of units:
+// 64 places of a head each, with how many tokens stay before token 64 k of the head.
 // Second launch: blocks take units by ticket. A unit reads its rows, says so, waits until
 // the units that read its places have done so (rows move towards the front, so those are
 // earlier units of the head, which running blocks have taken before, and no unit waits
@@ -24,6 +24,7 @@ namespace kvx {
 namespace {
 
 constexpr int kChunk = kEvictChunk;
+constexpr int kBins = 2048;  // of a histogram: 11 bits of a key
 
 // Order-preserving key: larger weight, larger key; -0 as 0; NaN below everything.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -59,7 +60,7 @@ __device__ __forceinline__ Head load_head(const EvictParams &p, int bh, bool rep
 template <int kThreads, int kKeys>
 struct SelectSmem {
   uint32_t keys[kKeys];
-  uint32_t hist[2][256];
+  uint32_t hist[2][kBins];
   uint32_t warp_sum[2][kThreads / 32];
   uint32_t count[2];     // keys of this block's run that stay for certain, and equal to the cut
   uint32_t cut, left;    // digits found; keys still to take among those that share them
@@ -84,16 +85,22 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const CacheGroup &grp = p.c.grp[gi];
   const int32_t *table = grp.table + (size_t)hd.b * grp.stride;
   const float *weights = p.weights[gi];
+  // place of token t of page `page` in a pool of weights (pool_row, in fewer operations)
+  const int page_step = grp.size << p.c.lgP, tok_step = p.c.token_major ? grp.size : 1;
+  const int first_at = p.c.token_major ? row : row << p.c.lgP;
+  auto place = [&](int page, int t) {
+    return (int64_t)page * page_step + ((t & (p.c.P - 1)) * tok_step + first_at);
+  };
   const int chunks = (hd.n + kChunk - 1) / kChunk, per = (chunks + (int)C - 1) / (int)C;
   const int c_lo = min(chunks, (int)rank * per), c_hi = min(chunks, c_lo + per);
   const int t_lo = c_lo * kChunk, t_hi = min(hd.n, c_hi * kChunk);
-  const int first_unit = p.copy_weights ? 0 : hd.first / kChunk;
-  const int units = hd.evict || p.copy_weights ? max(0, (hd.m + kChunk - 1) / kChunk - first_unit) : 0;
+  const int first_unit = hd.first / kChunk;
+  const int units = hd.evict ? max(0, (hd.m + kChunk - 1) / kChunk - first_unit) : 0;
   const int64_t base = (int64_t)hd.b * p.chunks_seq + p.chunk_off[hd.h];  // of the head's chunks
 
   auto load_key = [&](int t, int page) -> uint32_t {
     if (page < 0 || page >= grp.pages) return 0u;
-    return weight_key(weights[pool_row(p.c, grp, page, row, t & (p.c.P - 1))]);
+    return weight_key(weights[place(page, t)]);
   };
   auto key = [&](int t) -> uint32_t {
     return t - t_lo < kKeys ? sm.keys[t - t_lo] : load_key(t, table[t >> p.c.lgP]);
@@ -125,43 +132,58 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     }
   }
   // (left = 0: nothing of the middle stays)
-  for (int pass = 0; pass < 4 && hd.evict && left; ++pass) {
+  for (int pass = 0; pass < 3 && hd.evict && left; ++pass) {
     uint32_t *hist = sm.hist[pass & 1];
-    if (tid < 256) hist[tid] = 0;
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
-    const int shift = 24 - 8 * pass;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     for (int t0 = a_lo + 32 * warp; t0 < a_hi; t0 += kThreads) {
       const int t = t0 + lane;
-      const uint32_t k = t < a_hi ? key(t) : 0u;
-      const bool in = t < a_hi && (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
-      const uint32_t digit = in ? k >> shift & 255u : 256u;
-      // Weights share a few leading digits: one add for the lanes of a digit.
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], (uint32_t)__popc(same));
+      const uint32_t k = t < a_hi ? key(t) : 0u, digit = k >> shift & ((1u << bits) - 1u);
+      if (pass == 0) {
+        // Weights share leading digits: one add for all lanes of a digit (adds to one address go
+        // one after the other).
+        const uint32_t same = __match_any_sync(0xffffffffu, t < a_hi ? digit : (uint32_t)kBins);
+        if (t < a_hi && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], (uint32_t)__popc(same));
+      } else if (t < a_hi && (k >> (shift + bits)) == (prefix >> (shift + bits))) {
+        atomicAdd(&hist[digit], 1u);
+      }
     }
     meet();
-    // bin 255 - tid of all blocks, and the keys in higher bins
-    uint32_t own = 0, x = 0;
-    if (tid < 256) {
-      const uint32_t at = smem_u32(&hist[255 - tid]);
-      if (C == 1)
-        own = hist[255 - tid];
-      else
-        for (uint32_t r = 0; r < C; ++r) own += ld_cluster_u32(mapa_shared(at, r));
-      x = own;
+    // Bins from the last down, kEach to a thread, of all blocks; the keys in higher bins.
+    constexpr int kEach = kBins / kThreads;
+    uint32_t own[kEach], x = 0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+    for (int e = 0; e < kEach; ++e) own[e] = 0;
+    for (uint32_t r = 0; r < C; ++r)
+#pragma unroll
+      for (int e = 0; e < kEach; e += 4) {  // four bins a load, the highest last
+        const uint32_t at = smem_u32(&hist[kBins - 4 - (tid * kEach + e)]);
+        const float4 v = ld_cluster_f4(C == 1 ? at : mapa_shared(at, r));
+        own[e] += __float_as_uint(v.w);
+        own[e + 1] += __float_as_uint(v.z);
+        own[e + 2] += __float_as_uint(v.y);
+        own[e + 3] += __float_as_uint(v.x);
       }
-      if (lane == 31) sm.warp_sum[0][warp] = x;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) x += own[e];
+    const uint32_t mine = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
     }
+    if (lane == 31) sm.warp_sum[0][warp] = x;
     __syncthreads();
-    if (tid < 256)
-      for (int w = 0; w < warp; ++w) x += sm.warp_sum[0][w];
-    if (tid < 256 && x >= left && x - own < left) {
-      sm.cut = prefix | (uint32_t)(255 - tid) << shift;
-      sm.left = left - (x - own);
+    x -= mine;
+    for (int w = 0; w < warp; ++w) x += sm.warp_sum[0][w];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (x < left && x + own[e] >= left) {
+        sm.cut = prefix | (uint32_t)(kBins - 1 - (tid * kEach + e)) << shift;
+        sm.left = left - x;
+      }
+      x += own[e];
     }
     __syncthreads();
     prefix = sm.cut;
@@ -203,13 +225,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const uint32_t start = C == 1 ? sm.start : ld_cluster_u32(mapa_shared(smem_u32(&sm.start), 0));
   if (rank == 0 && tid == 0)  // (all blocks of the head have read its length)
     p.kv_out[bh] = hd.n ? hd.m : p.kv_len[bh];
-  for (int i = (int)rank * kThreads + tid; i < units; i += (int)C * kThreads) {
-    p.units[start + i] = {bh, first_unit + i};
-    p.read_done[start + i] = 0;
-  }
   // Places: exclusive sums over the words of a segment of kKeys tokens.
   static_assert(kKeys / 32 <= kThreads, "a thread a word");
-  for (int t0 = t_lo; t0 < t_hi && units; t0 += kKeys) {
+  for (int t0 = t_lo; t0 < t_hi && (units || p.copy_weights); t0 += kKeys) {
     if (t_hi - t_lo > kKeys) {  // (else the words are still there)
       __syncthreads();
       mark(t0);
@@ -239,15 +257,48 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     if (in) {
       sm.above[tid] = keep;
       sm.equal[tid] = at;
-      if ((tid & 1) == 0) p.rank[base + (t0 >> 6) + (tid >> 1)] = (int)at;
+      const int c = (t0 >> 6) + (tid >> 1);
+      if ((tid & 1) == 0 && c >= first_unit && c < first_unit + units) {
+        p.units[start + (c - first_unit)] = {bh, c, min(kChunk, hd.m - c * kChunk), (int)at / kChunk};
+        p.read_done[start + (c - first_unit)] = 0;
+      }
     }
     before += all_a;
     equals += all_e;
     __syncthreads();
-    for (int w = warp; w < kKeys / 32 && t0 + 32 * w < t_hi; w += kWarps) {
-      const uint32_t k = sm.above[w];
-      if (k >> lane & 1u)
-        p.source[base * kChunk + sm.equal[w] + __popc(k & ((1u << lane) - 1u))] = t0 + 32 * w + lane;
+    const int words = min(kKeys / 32, (t_hi - t0 + 31) / 32);
+    for (int w0 = warp; w0 < words; w0 += 8 * kWarps) {  // eight words in flight
+      int from[8], to[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int w = w0 + u * kWarps;
+        const uint32_t k = w < words ? sm.above[w] : 0u;
+        from[u] = t0 + 32 * w + lane;
+        to[u] = -1;
+        if (k >> lane & 1u) {
+          to[u] = (int)(sm.equal[w] + __popc(k & ((1u << lane) - 1u)));
+          p.source[base * kChunk + to[u]] = from[u];
+        }
+      }
+      if (!p.copy_weights) continue;  // (in place, weights move with their rows)
+      int pf[8], pt[8];
+      float wt[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        pf[u] = to[u] >= 0 ? table[from[u] >> p.c.lgP] : 0;
+        pt[u] = to[u] >= 0 ? table[to[u] >> p.c.lgP] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (to[u] >= 0 && (pf[u] < 0 || pf[u] >= grp.pages || pt[u] < 0 || pt[u] >= grp.pages)) {
+          atomicOr(p.status, KVX_DEV_BAD_PAGE);
+          to[u] = -1;
+        }
+        if (to[u] >= 0) wt[u] = weights[place(pf[u], from[u])];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (to[u] >= 0) p.weights_out[gi][place(pt[u], to[u])] = wt[u];
     }
   }
   meet();  // nobody leaves while its shared memory may be read
@@ -265,8 +316,8 @@ __device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
 // What is known of a unit before its rows are read.
 struct Places {
   int64_t src[kChunk], dst[kChunk];  // pool rows; -1: a page outside the pool
-  int32_t bh, chunk, count, wait_from;  // wait_from: first chunk whose unit must have read
-  uint32_t unit, end;                   // end: no unit, nothing comes after it
+  EvictUnit un;
+  uint32_t unit, end;  // end: no unit, nothing comes after it
 };
 constexpr int kMovers = 256, kScouts = kChunk;
 constexpr int kRing = 3;  // units whose places are known: written, read, looked up
@@ -283,7 +334,7 @@ constexpr int kFull = 1, kFree = kFull + kRing, kMove = kFree + kRing;
 // kPieces pieces of type V make a row's K, as many its V. 4-bit rows: the last piece is the
 // row's parameters. Two warps look up the places of the units to come; the others read unit
 // i + 1 before they wait for the units before unit i and write it, so that a unit is
-// read long before another one needs that.
+// read long before another one needs that (said only after unit i is written: 132 -> 175 us).
 template <class V, int kPieces, bool kQ4>
 __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kRow = 2 * kPieces;
@@ -298,26 +349,33 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
   if (tid >= kMovers) {
     const int j = tid - kMovers;  // the unit's row
     const uint32_t total = p.counters[0];
-    for (int i = 0;; ++i) {
-      Places &m = ring[i % kRing];
-      if (i >= kRing) bar_sync(kFree + i % kRing, kMovers + kScouts);
-      if (j == 0) ticket = atomicAdd(p.counters + 1, 1u);
+    // The ticket is taken two units ahead, the unit read one ahead.
+    auto take = [&]() { return j == 0 ? atomicAdd(p.counters + 1, 1u) : 0u; };
+    auto tell = [&](uint32_t t) {
+      if (j == 0) ticket = t;
       bar_sync(kMove + 1, kScouts);
       const uint32_t u = ticket;
       bar_sync(kMove + 1, kScouts);
+      return u;
+    };
+    uint32_t u = tell(take()), u1 = tell(take());
+    EvictUnit un = {}, un1 = {};
+    if (u < total) un = p.units[u];
+    for (int i = 0;; ++i) {
+      Places &m = ring[i % kRing];
+      const uint32_t t2 = take();
+      if (u1 < total) un1 = p.units[u1];
+      if (i >= kRing) bar_sync(kFree + i % kRing, kMovers + kScouts);
       if (u < total) {
-        const EvictUnit un = p.units[u];
         const int b = un.bh / p.c.Hkv, h = un.bh - b * p.c.Hkv, row = p.c.head_row[h];
         const CacheGroup &grp = p.c.grp[p.c.head_grp[h]];
         const int64_t base = (int64_t)b * p.chunks_seq + p.chunk_off[h];
         const int32_t *table = grp.table + (size_t)b * grp.stride;
-        // (checked by the launch before; where kv_out is kv_len, that is the number of kept tokens)
-        const int kept = min(p.kv_len[un.bh], p.budget[un.bh]);
-        const int to = un.chunk * kChunk + j, count = min(kChunk, kept - un.chunk * kChunk);
+        const int to = un.chunk * kChunk + j;
         int64_t src = -1, dst = -1;
-        if (j < count) {
+        if (j < un.count) {
           const int from = p.source[base * kChunk + to];
-          const int pf = table[from >> p.c.lgP], pt = table[to >> p.c.lgP];
+          const int pt = table[to >> p.c.lgP], pf = table[from >> p.c.lgP];
           if (pf >= 0 && pf < grp.pages && pt >= 0 && pt < grp.pages) {
             src = pool_row(p.c, grp, pf, row, from & (p.c.P - 1));
             dst = pool_row(p.c, grp, pt, row, to & (p.c.P - 1));
@@ -328,16 +386,16 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
         m.src[j] = src;
         m.dst[j] = dst;
         if (j == 0) {
-          m.bh = un.bh;
-          m.chunk = un.chunk;
-          m.count = count;
-          m.wait_from = p.rank[base + un.chunk] / kChunk;
+          m.un = un;
           m.unit = u;
         }
       }
       if (j == 0) m.end = u >= total;
       bar_arrive(kFull + i % kRing, kMovers + kScouts);
       if (u >= total) break;
+      u = u1;
+      un = un1;
+      u1 = tell(t2);
     }
   } else {
     auto place = [&](const CacheGroup &grp, int64_t r, int q) -> char * {
@@ -348,13 +406,13 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
       return pool + (r * kPieces + i) * (int)sizeof(V);
     };
     auto moves = [&](const Places &m, int i) {
-      return i < m.count * kRow && m.dst[i / kRow] != m.src[i / kRow];
+      return i < m.un.count * kRow && m.dst[i / kRow] != m.src[i / kRow];
     };
     auto weighs = [&](const Places &m) {
-      return tid < m.count && m.dst[tid] >= 0 && (p.copy_weights || m.dst[tid] != m.src[tid]);
+      return !p.copy_weights && tid < m.un.count && m.dst[tid] != m.src[tid];
     };
     auto read = [&](const Places &m, V(&v)[kEach], float &wt) {
-      const int gi = p.c.head_grp[m.bh % p.c.Hkv];
+      const int gi = p.c.head_grp[m.un.bh % p.c.Hkv];
       const CacheGroup &grp = p.c.grp[gi];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
@@ -365,8 +423,8 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
     };
     auto write = [&](const Places &m, const V(&v)[kEach], float wt) {
       // Units before this one that read what it overwrites.
-      for (int c = m.wait_from + tid; c < m.chunk; c += kMovers) {
-        const uint32_t *flag = p.read_done + (m.unit - (uint32_t)(m.chunk - c));
+      for (int c = m.un.wait_from + tid; c < m.un.chunk; c += kMovers) {
+        const uint32_t *flag = p.read_done + (m.unit - (uint32_t)(m.un.chunk - c));
         if (ld_acquire(flag)) continue;
         const uint64_t t0 = globaltimer_ns();
         while (!ld_acquire(flag))
@@ -378,7 +436,7 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
       }
       bar_sync(kMove, kMovers);
       if (*(volatile int *)&failed) return;
-      const int gi = p.c.head_grp[m.bh % p.c.Hkv];
+      const int gi = p.c.head_grp[m.un.bh % p.c.Hkv];
       const CacheGroup &grp = p.c.grp[gi];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
@@ -458,13 +516,14 @@ cudaError_t launch_select(const EvictParams &p, int C, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
-  // Short heads: a small block each, many to an SM. Long ones: a large block each where there are
-  // enough of them to fill half of the GPU, else clusters of up to eight.
+  // Short heads: a small block each, many to an SM. Long ones: as many blocks (two to an SM) as
+  // their keys fill, and more where there are few heads; the longest head bounds the launch.
   const int heads = p.c.B * p.c.Hkv;
   const int64_t longest = p.chunks / heads * kChunk;  // (their mean room)
   int C = 1;
-  while (C < 8 && 2 * C * heads <= 152) C *= 2;
-  cudaError_t e = longest <= 4096 ? launch_select<256, 4096>(p, 1, st) : launch_select<1024, 32768>(p, C, st);
+  while (C < 8 && (C * heads < 2 * 152 || C * 16384 < longest)) C *= 2;
+  cudaError_t e = longest <= 4096 && heads >= 152 ? launch_select<256, 4096>(p, 1, st)
+                                                  : launch_select<512, 16384>(p, C, st);
   if (e != cudaSuccess) return e;
   const bool wide = p.c.D == 128;
   if (p.q4) return wide ? launch_move<uint2, 9, true>(p, st) : launch_move<uint32_t, 9, true>(p, st);

@@ -20,52 +20,56 @@ __device__ __forceinline__ int64_t pool_rows(const CacheDev &c, int grp) {
   return c.grp[grp].pages * c.grp[grp].size * c.P;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
-  const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y), c = unpack_bf16(x.z), d = unpack_bf16(x.w);
-  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
-}
-
 struct Quantised {
   uint32_t codes, params;  // (lo << 16 | step, of the group)
 };
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *(const __nv_bfloat162 *)&x; }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *(const uint32_t *)&x; }
 // This lane's eight elements of its group; eight neighbouring lanes hold one.
 __device__ __forceinline__ Quantised quantise(const uint4 &x) {
-  float f[8];
-  unpack8(x, f);
-  float lo = f[0], hi = f[0];
-  bool finite = true;
+  // (least, -greatest) of the group; NaN stays NaN
+  __nv_bfloat162 a = __hmin2_nan(__hmin2_nan(as_bf2(x.x), as_bf2(x.y)), __hmin2_nan(as_bf2(x.z), as_bf2(x.w)));
+  __nv_bfloat162 b = __hmax2_nan(__hmax2_nan(as_bf2(x.x), as_bf2(x.y)), __hmax2_nan(as_bf2(x.z), as_bf2(x.w)));
+  b = __hneg2(b);
+  a = __hmin2_nan(__lows2bfloat162(a, b), __highs2bfloat162(a, b));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, f[i]);
-    hi = fmaxf(hi, f[i]);
-    finite = finite && isfinite(f[i]);
-  }
-#pragma unroll
-  for (int w = 1; w < 8; w <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, w));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, w));
-    finite = __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, w) && finite;
-  }
-  const float range = hi - lo;
-  if (!finite || !isfinite(range)) return {0u, 0x7fc00000u};
+  for (int w = 1; w < 8; w <<= 1) a = __hmin2_nan(a, as_bf2(__shfl_xor_sync(0xffffffffu, as_u32(a), w)));
+  const float lo = __low2float(a), range = -__high2float(a) - lo;
+  if (!isfinite(range)) return {0u, 0x7fc00000u};
   const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
   const float step = __bfloat162float(sb);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack_bf16(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w);
+    f[2 * i] = v.x - lo;
+    f[2 * i + 1] = v.y - lo;
+  }
   uint32_t codes = 0;
-  if (step > 0.f) {
-    const float r = step >= 0x1p-120f ? __frcp_rn(step) : 0.f;
+  if (step >= 0x1p-120f) {
+    // rint(fl(d / step)) without the division: c, the nearest integer to an estimate of the
+    // quotient, and e = d - c * step, exact in one multiply-add. Where 2 |e| is below step, c it
+    // is. Else d lies past the middle between c and its neighbour on e's side (the estimate was
+    // off), or so near it that the quotient would be rounded to it: then the even one of the two.
+    const float r = __frcp_rn(step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // rint(fl(d / step)) without the division: an estimate says between which two codes, and the sign
-      // of d - half * step, exact in one multiply-add, on which side of their middle `half`. Within half
-      // a unit in the last place of `half` the quotient would be rounded to it: ties to even.
-      const float d = f[i] - lo;
-      const float low = floorf(r > 0.f ? d * r : __fdiv_rn(d, step));
-      const float half = low + 0.5f, e = fmaf(-half, step, d);
-      const float ulp2 = __uint_as_float((__float_as_uint(half) & 0x7f800000u) - (24u << 23));
-      const uint32_t l = (uint32_t)low;
-      const uint32_t c = l + (fabsf(e) <= ulp2 * step ? l & 1u : e > 0.f ? 1u : 0u);
-      codes |= min(c, 15u) << (4 * i);
+      float c = fmaf(f[i], r, 12582912.f) - 12582912.f;  // 1.5 * 2^23
+      const float e = fmaf(-c, step, f[i]), past = fmaf(2.f, fabsf(e), -step);
+      if (past > -0x1p-20f * step) {
+        const float middle = c + copysignf(0.5f, e);
+        // half a unit in the last place of the middle, twice
+        const float near = __uint_as_float((__float_as_uint(middle) & 0x7f800000u) - (23u << 23)) * step;
+        if (past > near || (past >= -near && ((int)c & 1))) c = 2.f * middle - c;
+      }
+      f[i] = c;
     }
+    const float l = fmaf(fmaf(fmaf(f[3], 16.f, f[2]), 16.f, f[1]), 16.f, f[0]);
+    const float h = fmaf(fmaf(fmaf(f[7], 16.f, f[6]), 16.f, f[5]), 16.f, f[4]);
+    codes = __byte_perm(__float_as_uint(l + 8388608.f), __float_as_uint(h + 8388608.f), 0x5410);
+  } else if (step > 0.f) {
+    for (int i = 0; i < 8; ++i)
+      codes |= (uint32_t)fminf(15.f, rintf(__fdiv_rn(f[i], step))) << (4 * i);
   }
   return {codes, pack_bf16(step, lo)};
 }

@@ -86,8 +86,10 @@ cudaError_t launch_read(const ReadParams &p, cudaStream_t st);
 // A unit of the move: kEvictChunk target places of a head. A head's arrays hold a number per
 // chunk of the tokens that its page table has room for, heads one after the other.
 constexpr int kEvictChunk = 64;
-struct EvictUnit {
-  int32_t bh, chunk;  // head, place / kEvictChunk
+struct alignas(16) EvictUnit {
+  int32_t bh, chunk;  // head, first place / kEvictChunk
+  int32_t count;      // places
+  int32_t wait_from;  // first chunk whose unit reads what this one overwrites
 };
 struct EvictParams {
   CacheDev c;
@@ -102,16 +104,15 @@ struct EvictParams {
   uint32_t *counters;   // [0] units, [1] tickets, [2] blocks done
   EvictUnit *units;     // [chunks]
   uint32_t *read_done;  // [chunks] the unit's rows have been read
-  int32_t *rank;        // per head and chunk: tokens kept before the chunk's first
   int32_t *source;      // per head and kept token: the token that it was
   int64_t chunks;       // of all heads
   int64_t chunks_seq;   // of a sequence's heads
   int32_t chunk_off[KVX_MAX_KV_HEADS];  // where a KV head's begin among them
   uint32_t wait_ns;
 };
-// Workspace: header | units | read_done | rank | source.
+// Workspace: header | units | read_done | source.
 struct EvictWs {
-  size_t read_done, rank, source, total;
+  size_t read_done, source, total;
 };
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 

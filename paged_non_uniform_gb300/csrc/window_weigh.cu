@@ -3,8 +3,8 @@
 // w_t = (t < n ? w_t : 0) + sum over the rows r (new rows and query heads of the KV head) of
 // 2^(x_rt - M_r) / L_r, from the scores x that the attention launch left and the row's
 // maximum and sum, which are only known when all of a head's pieces are merged: hence
-// the stored scores and a launch of its own. A thread owns a token and adds its rows in
-// order, so nothing depends on timing. Blocks take equal parts of all heads' visited tiles.
+// the stored scores and a launch of its own. A token's rows are added in a fixed order, so
+// nothing depends on timing. Blocks take equal parts of all heads' visited tiles.
 #include <math.h>
 
 #include "window_split.cuh"
@@ -20,11 +20,15 @@ struct Smem {
   TreeRange range;
 };
 
+// kLanes lanes share a token: four rows of every row group each (a 16-byte load), so that a
+// token's scores are one stretch of memory to neighbouring lanes; kBatch tokens in flight.
+template <int kLanes>
 __global__ void __launch_bounds__(kThreads) weigh_kernel(const __grid_constant__ WindowParams p,
                                                          int group_tokens) {
+  constexpr int kBatch = 4, kTokens = kThreads / kLanes;  // tokens of a block's step
   __shared__ Smem sm;
   extern __shared__ float2 row[];  // the head's rows: (maximum, 1 / sum)
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, sub = tid % kLanes;
   pdl_launch_dependents();
   pdl_wait();
   // (the params count a head as one row group here; group_tokens are the attention launch's)
@@ -42,30 +46,56 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const __grid_constant__
       row[r] = make_float2(ml.x, ml.y == 0.f ? 0.f : 1.f / ml.y);
     }
     __syncthreads();
-    const int per = group_tokens * p.c.g;
-    for (int i = it.t0 * kTile + tid; i < it.t1 * kTile; i += kThreads) {
-      const int t = window_tile(hd, i / kTile) * kTile + i % kTile;
-      if (t >= hd.n + hd.T) continue;
-      float w = 0.f;
-      for (int r0 = 0, group = 0; r0 < rows; r0 += per, ++group) {
-        const float *x = window_scores(p, hd, group, i);
-        const int k = min(per, rows - r0);
-        for (int r = 0; r < k; ++r) {
-          const float xr = __ldcg(x + r);
-          if (xr != -INFINITY) w += ex2(xr - row[r0 + r].x) * row[r0 + r].y;
+    const int per = group_tokens * p.c.g, end = it.t1 * kTile;
+    // (warps stay whole: lanes of a token meet in shuffles)
+    for (int i0 = it.t0 * kTile; i0 < end; i0 += kBatch * kTokens) {
+      int t[kBatch];
+      float w[kBatch], old[kBatch];
+      float *at[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * kTokens + tid / kLanes;
+        t[b] = i < end ? window_tile(hd, i / kTile) * kTile + i % kTile : INT32_MAX;
+        w[b] = 0.f;
+        at[b] = nullptr;
+        if (t[b] < hd.n + hd.T && sub == 0) {
+          const int page = table[t[b] >> p.c.lgP];
+          // (a page outside the pool was reported by the attention launch)
+          if (page >= 0 && page < grp.pages)
+            at[b] = p.weights[gi] + pool_row(p.c, grp, page, rank, t[b] & (p.c.P - 1));
         }
       }
-      const int page = table[t >> p.c.lgP];
-      if (page < 0 || page >= grp.pages) continue;  // (reported by the attention launch)
-      float *at = p.weights[gi] + pool_row(p.c, grp, page, rank, t & (p.c.P - 1));
-      *at = t < hd.n ? *at + w : w;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) old[b] = at[b] && t[b] < hd.n ? *at[b] : 0.f;
+      for (int r0 = 0, group = 0; r0 < rows; r0 += per, ++group) {
+        const int k = min(per, rows - r0) - 4 * sub;  // rows left from this lane's first
+        const float2 *rw = row + r0 + 4 * sub;
+        float4 x[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (k > 0 && t[b] < hd.n + hd.T)
+            x[b] = __ldcg((const float4 *)(window_scores(p, hd, group, i0 + b * kTokens + tid / kLanes) + 4 * sub));
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (k <= 0 || t[b] >= hd.n + hd.T) continue;
+          const float v[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < k && v[e] != -INFINITY) w[b] = fmaf(ex2(v[e] - rw[e].x), rw[e].y, w[b]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+        for (int sh = 1; sh < kLanes; sh <<= 1) w[b] += __shfl_xor_sync(0xffffffffu, w[b], sh);
+        if (at[b]) *at[b] = old[b] + w[b];
+      }
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st) {
+template <int kLanes>
+cudaError_t launch_lanes(const WindowParams &p, int blocks, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
@@ -78,8 +108,18 @@ cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st) {
   cfg.numAttrs = 1;
   WindowParams w = p;
   w.group_tokens = p.max_q;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, weigh_kernel, w, (int)p.group_tokens);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weigh_kernel<kLanes>, w, (int)p.group_tokens);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st) {
+  const int n = p.score_rows / 4;  // lanes with work
+  if (n <= 1) return launch_lanes<1>(p, 2 * blocks, st);
+  if (n <= 2) return launch_lanes<2>(p, 2 * blocks, st);
+  if (n <= 4) return launch_lanes<4>(p, 2 * blocks, st);
+  return launch_lanes<8>(p, 2 * blocks, st);
 }
 
 }  // namespace kvx
