@@ -45,32 +45,35 @@ namespace wmma {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
-// NB: column blocks of 8 query rows. kDup: at most 4 rows, repeated (NB = 1).
-template <int D, bool kQ4, int NB, bool kDup>
+// kRows: query rows of a row group, 4 to 32. NB: column blocks of 8 that one warp takes; kCols:
+// warps that share a stage, each with its own columns (32 rows in one warp left no registers for
+// independent work: up to 8 drafts 413 us). kDup: 4 rows, repeated.
+template <int D, bool kQ4, int kRows_>
 struct Cfg {
-  static constexpr int kRows = kDup ? 4 : 8 * NB;  // query rows of a row group
+  static constexpr int kRows = kRows_;
+  static constexpr bool kDup = kRows == 4;
+  static constexpr int kCols = kQ4 || kRows <= 8 ? 1 : 2;
+  static constexpr int NB = kRows <= 8 ? 1 : kRows / 8 / kCols;
   static constexpr int kTokens = kQ4 ? 64 : 32;  // of a stage
   static constexpr int kBox = kWindowBox;        // of a bf16 load, at most
   static constexpr int kTokenBytes = kQ4 ? q4_row_bytes(D) : 2 * D;
   static constexpr int kTile = kTokens * kTokenBytes;  // K (or V) bytes of a stage
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kCons = kQ4 ? (NB == 1 ? 4 : 2) : NB == 1 ? 3 : 2;
-  static constexpr int kSteps = NB > 2 ? 1 : 2;  // 16-token steps computed together
-  static constexpr int kStages = 2 * kCons;
+  static constexpr int kTeams = kQ4 ? (NB == 1 ? 4 : 2) : kCols == 1 ? 3 : 2;  // takers of stages
+  static constexpr int kCons = kTeams * kCols;                                 // consumer warps
+  static constexpr int kSteps = NB > 1 && !kQ4 ? 1 : 2;  // 16-token steps computed together
+  static constexpr int kStages = 2 * kTeams;
   static constexpr int kProd = kQ4 ? 2 : 1;   // producer warps: K and V, or both in one
   static constexpr int kBatch = kQ4 ? 4 : 1;  // stages that a producer handles at once
   static constexpr int kThreads = 32 * (kCons + kProd);
-  static constexpr int kMS = D + 4;  // floats of a row of a warp's record
+  static constexpr int kMS = D + 4;  // floats of a row of a team's record
   static constexpr int kRec = kRows * kMS;
   static constexpr int kRing = kStages * kStage;
-  static constexpr bool kQShared = NB > 2;  // query fragments in shared memory
-  static constexpr int kQBytes = kQShared ? NB * (D / 16) * 32 * 8 : 0;
-  // ring | records | (max, sum) [kCons][kRows] | weights [kRows][8] | queries | barriers, flag
-  static constexpr int kSmem = 1024 + kRing + 4 * kCons * kRec + 8 * kCons * kRows + 32 * kRows +
-                               kQBytes + 16 * kStages + 16;
+  // ring | records | (max, sum) [kTeams][kRows] | weights [kRows][8] | barriers, flag
+  static constexpr int kSmem =
+      1024 + kRing + 4 * kTeams * kRec + 8 * kTeams * kRows + 32 * kRows + 16 * kStages + 16;
   static_assert(kSmem + 2048 <= 227 * 1024 / kWindowBlocksPerSm, "resident blocks per SM");
-  static_assert(kStages % kCons == 0, "each ring slot belongs to one consumer warp");
-  static_assert(kCons <= 7, "a row's eighth weight is 1 / sum");
+  static_assert(kTeams <= 7, "a row's eighth weight is 1 / sum");
 };
 
 __device__ __forceinline__ float bf_low(uint32_t x) { return __uint_as_float(x << 16); }
@@ -182,11 +185,11 @@ __device__ __forceinline__ int stage_token(const TreeItem &it, int st) {
 }
 
 // ---- producer ----------------------------------------------------------------
-template <int D, bool kQ4, int NB, bool kDup>
+template <int D, bool kQ4, int kRows>
 __device__ __forceinline__ void produce(const WindowMmaParams &mp, const TreeRange &range,
                                         uint32_t ring, uint32_t full0, uint32_t empty0,
                                         volatile int *abort_flag, int which, int lane) {
-  using C = Cfg<D, kQ4, NB, kDup>;
+  using C = Cfg<D, kQ4, kRows>;
   const WindowParams &p = mp.w;
   const int P = p.c.P, box = min(P, kQ4 ? C::kTokens : C::kBox), lb = 31 - __clz(box);
   const uint32_t box_bytes = (uint32_t)box * C::kTokenBytes;
@@ -298,23 +301,20 @@ struct State {
   float z[NG][NB][2], vscale, vtop;
 };
 
-// Query fragments: registers, or shared memory where there are many.
-template <int D, int NB, bool kShared>
+// Query fragments.
+template <int D, int NB>
 struct Queries {
-  uint32_t f[kShared ? 1 : NB][kShared ? 1 : D / 16][2];
-  const uint8_t *at;  // shared: this lane's fragments
-  __device__ __forceinline__ uint2 get(int nb, int j) const {
-    if constexpr (kShared) return *(const uint2 *)(at + (nb * (D / 16) + j) * 256);
-    return make_uint2(f[nb][j][0], f[nb][j][1]);
-  }
+  uint32_t f[NB][D / 16][2];
+  __device__ __forceinline__ uint2 get(int nb, int j) const { return make_uint2(f[nb][j][0], f[nb][j][1]); }
 };
 
 // What the rows of an item see.
-template <int NB>
 struct View {
   Window win;
-  int n, i0, i1;   // cached tokens, first and last new row of the item
-  int pos[NB][2];  // positions of this lane's query rows (-1: none)
+  int n, i0, i1, rows;  // cached tokens, first and last new row, query rows of the item
+  int recip_g;
+  // position of query row r, -1 where there is none
+  __device__ __forceinline__ int pos(int r) const { return r < rows ? n + i0 + ((r * recip_g) >> 16) : -1; }
 };
 
 // Scores of kSteps * 16 tokens, not yet scaled; `tile`: their first token's rows of K.
@@ -406,20 +406,22 @@ constexpr float kNoRef = -3e38f;  // of a row that has seen nothing
 // x[mt][nb][e]: token mt * 16 + r (+ 8 for e >= 2), query row 8 nb + 2c + (e & 1). Masks and
 // scales the scores, stores them where weights want them, and makes them weights. seen (kEdge):
 // bit (mt * NB + nb) * 4 + e.
-template <int D, bool kQ4, int NB, int kSteps, bool kEdge>
-__device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (&scale)[NB][2],
-                                        const View<NB> &vw, int t0, State<D, kQ4, NB> &s,
-                                        uint32_t &seen, float *scores, int score_rows, int lane) {
+template <int D, bool kQ4, int NB, int kSteps, bool kDup, bool kEdge>
+__device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (&scale)[kQ4 ? NB : 1][2],
+                                        const View &vw, int t0, State<D, kQ4, NB> &s,
+                                        uint32_t &seen, float *scores, int score_rows, int row0, int lane) {
   const int r = lane >> 2, c = lane & 3;
   seen = 0;
+  auto sc = [&](int nb, int k) { return scale[kQ4 ? nb : 0][k]; };
   if constexpr (kEdge) {
 #pragma unroll
-    for (int mt = 0; mt < kSteps; ++mt)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int mt = 0; mt < kSteps; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool see = window_sees(vw.win, vw.pos[nb][e & 1], t0 + mt * 16 + r + ((e >> 1) << 3));
+          const int q = row0 + 8 * nb + 2 * c + (e & 1);
+          const bool see = window_sees(vw.win, vw.pos(kDup ? q & 3 : q), t0 + mt * 16 + r + ((e >> 1) << 3));
           seen |= (see ? 1u : 0u) << ((mt * NB + nb) * 4 + e);
           x[mt][nb][e] = see ? x[mt][nb][e] : -INFINITY;
         }
@@ -429,11 +431,11 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
     for (int mt = 0; mt < kSteps; ++mt)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        if (8 * nb + 2 * c < score_rows) {
-          float *at = scores + (size_t)(mt * 16 + r) * score_rows + 8 * nb + 2 * c;
-          *(float2 *)at = make_float2(x[mt][nb][0] * scale[nb][0], x[mt][nb][1] * scale[nb][1]);
+        if (row0 + 8 * nb + 2 * c < score_rows) {
+          float *at = scores + (size_t)(mt * 16 + r) * score_rows + row0 + 8 * nb + 2 * c;
+          *(float2 *)at = make_float2(x[mt][nb][0] * sc(nb, 0), x[mt][nb][1] * sc(nb, 1));
           *(float2 *)(at + 8 * score_rows) =
-              make_float2(x[mt][nb][2] * scale[nb][0], x[mt][nb][3] * scale[nb][1]);
+              make_float2(x[mt][nb][2] * sc(nb, 0), x[mt][nb][3] * sc(nb, 1));
         }
   }
   float y[kSteps][NB][4];  // relative to the reference
@@ -446,7 +448,7 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const float2 v = fma2(make_float2(x[mt][nb][e], x[mt][nb][e + 1]),
-                                make_float2(scale[nb][0], scale[nb][1]),
+                                make_float2(sc(nb, 0), sc(nb, 1)),
                                 make_float2(-s.ref[nb][0], -s.ref[nb][1]));
           y[mt][nb][e] = v.x, y[mt][nb][e + 1] = v.y;
           top = fmaxf(top, fmaxf(v.x, v.y));
@@ -463,7 +465,7 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
         for (int mt = 0; mt < kSteps; ++mt) mx = fmaxf(mx, fmaxf(x[mt][nb][k], x[mt][nb][k + 2]));
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, sh));
-        const float ref = fmaxf(s.ref[nb][k], mx * scale[nb][k]), f = ex2(s.ref[nb][k] - ref);
+        const float ref = fmaxf(s.ref[nb][k], mx * sc(nb, k)), f = ex2(s.ref[nb][k] - ref);
         s.ref[nb][k] = ref;
         s.l[nb][k] *= f;
 #pragma unroll
@@ -492,15 +494,14 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
 }
 
 // Whether some row of the item sees token t.
-template <int NB>
-__device__ __forceinline__ bool any_sees(const View<NB> &vw, int t) {
+__device__ __forceinline__ bool any_sees(const View &vw, int t) {
   return t <= vw.n + vw.i1 &&
          (t < vw.win.sinks || (t > vw.n + vw.i0 - vw.win.width && vw.win.width > 0));
 }
 
 template <int D, int NB, int kSteps, bool kDup, bool kEdge, class S>
 __device__ __forceinline__ void values_bf16(uint32_t tile, const float (&x)[kSteps][NB][4],
-                                            const View<NB> &vw, int t0, S &s, uint32_t seen, int lane) {
+                                            const View &vw, int t0, S &s, uint32_t seen, int lane) {
   const int c = lane & 3, mi = lane >> 3, lr = lane & 7;
   // P^T as the B operand (inner dimension tokens), in parts; repeated rows: the first two parts
   // in one operand, the third and zeros in another.
@@ -589,26 +590,26 @@ __device__ __forceinline__ void values_bf16(uint32_t tile, const float (&x)[kSte
         }
       }
     }
+    float acc[NB][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float acc[4];
+    for (int k = kParts - 1; k >= 0; --k)  // small parts first; the column blocks side by side
 #pragma unroll
-      for (int k = kParts - 1; k >= 0; --k)  // small parts first
+      for (int mt = 0; mt < kSteps; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < kSteps; ++mt)
+        for (int nb = 0; nb < NB; ++nb)
           if (k == kParts - 1 && mt == 0)
-            mma<false, true>(acc, a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[k][mt][nb][0], b[k][mt][nb][1]);
+            mma<false, true>(acc[nb], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[k][mt][nb][0], b[k][mt][nb][1]);
           else
-            mma<false, false>(acc, a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[k][mt][nb][0], b[k][mt][nb][1]);
-      add4(s.o[dm][nb], acc);
-    }
+            mma<false, false>(acc[nb], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[k][mt][nb][0], b[k][mt][nb][1]);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) add4(s.o[dm][nb], acc[nb]);
   }
 }
 
 template <int D, int NB, int kSteps, bool kDup, bool kEdge, class S>
 __device__ __forceinline__ void values_q4(const uint8_t *codes, const uint8_t *params,
                                           const float (&x)[kSteps][NB][4],
-                                          const View<NB> &vw, int t0, S &s, uint32_t seen, int lane) {
+                                          const View &vw, int t0, S &s, uint32_t seen, int lane) {
   constexpr int NG = D / 64, kCode = q4_code_bytes(D), kParam = q4_param_bytes(D);
   const int r = lane >> 2, c = lane & 3;
   // Words r of tokens 2c, 2c + 1 of each half step; lanes with odd c read the odd one first, so
@@ -763,14 +764,15 @@ __device__ __forceinline__ void values_q4(const uint8_t *codes, const uint8_t *p
 }
 
 // One stage. kEdge: some row does not see all of it.
-template <int D, bool kQ4, int NB, bool kDup, bool kEdge, class Q, class S>
-__device__ __forceinline__ void consume(const uint8_t *kt, const uint8_t *vt, const View<NB> &vw, int t0,
-                                        const Q &q, const float (&qs)[kQ4 ? D / 64 : 1][NB][2],
+template <int D, bool kQ4, int kRows, bool kEdge, int NB>
+__device__ __forceinline__ void consume(const uint8_t *kt, const uint8_t *vt, const View &vw, int t0,
+                                        const Queries<D, NB> &q, const float (&qs)[kQ4 ? D / 64 : 1][NB][2],
                                         const float (&qe)[kQ4 ? D / 64 : 1][NB][2],
-                                        const float (&scale)[NB][2], S &s, float *scores, int score_rows,
-                                        int lane) {
-  using C = Cfg<D, kQ4, NB, kDup>;
+                                        const float (&scale)[kQ4 ? NB : 1][2], State<D, kQ4, NB> &s,
+                                        float *scores, int score_rows, int row0, int lane) {
+  using C = Cfg<D, kQ4, kRows>;
   constexpr int kSteps = C::kSteps;
+  constexpr bool kDup = C::kDup;
 #pragma unroll 1
   for (int h = 0; h < C::kTokens; h += 16 * kSteps) {
     float x[kSteps][NB][4];
@@ -780,8 +782,8 @@ __device__ __forceinline__ void consume(const uint8_t *kt, const uint8_t *vt, co
       scores_q4<D, NB, kSteps>(kt + h * kCode, kt + C::kTokens * kCode + h * kParam, q, qs, qe, x, lane);
     else
       scores_bf16<D, NB, kSteps>(smem_u32(kt) + h * (2 * D), q, x, lane);
-    softmax<D, kQ4, NB, kSteps, kEdge>(x, scale, vw, t0 + h, s, seen, scores ? scores + h * score_rows : nullptr,
-                                       score_rows, lane);
+    softmax<D, kQ4, NB, kSteps, kDup, kEdge>(x, scale, vw, t0 + h, s, seen, scores ? scores + h * score_rows : nullptr,
+                                       score_rows, row0, lane);
     if constexpr (kQ4)
       values_q4<D, NB, kSteps, kDup, kEdge>(vt + h * kCode, vt + C::kTokens * kCode + h * kParam, x, vw, t0 + h, s,
                                             seen, lane);
@@ -797,21 +799,25 @@ __device__ __forceinline__ int query_dim(int j, int e, int c) {
   return kQ4 ? 64 * (j >> 2) + 8 * (2 * c + ((j >> 1) & 1)) + 2 * (j & 1) + e : 16 * j + 2 * c + 8 * e;
 }
 
-template <int D, bool kQ4, int NB, bool kDup>
-__global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBlocksPerSm)
+template <int D, bool kQ4, int kRows>
+__global__ void __launch_bounds__((Cfg<D, kQ4, kRows>::kThreads), kWindowBlocksPerSm)
     window_mma_kernel(const __grid_constant__ WindowMmaParams mp) {
-  using C = Cfg<D, kQ4, NB, kDup>;
-  constexpr int NK = D / 16, NG = kQ4 ? D / 64 : 1, kCons = C::kCons;
+  using C = Cfg<D, kQ4, kRows>;
+  constexpr int NK = D / 16, NG = kQ4 ? D / 64 : 1, NB = C::NB, kCons = C::kCons, kTeams = C::kTeams;
+  constexpr bool kDup = C::kDup;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kCons + C::kProd];
   __shared__ TreeRange range_s;
+  // Each consumer warp's place in the block's items, and its item: not worth registers.
+  __shared__ alignas(16) uint8_t cur_s[kCons][sizeof(TreeCursor<kWindowTile>)];
+  __shared__ TreeItem item_s[kCons];
+  __shared__ View view_s[kCons];
   const WindowParams &p = mp.w;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float *rec = (float *)(smem + C::kRing);
-  float2 *ml = (float2 *)(rec + kCons * C::kRec);
-  float *wgt = (float *)(ml + kCons * C::kRows);
-  uint8_t *qsm = (uint8_t *)(wgt + 8 * C::kRows);
-  uint64_t *bars = (uint64_t *)(qsm + C::kQBytes);
+  float2 *ml = (float2 *)(rec + kTeams * C::kRec);
+  float *wgt = (float *)(ml + kTeams * kRows);
+  uint64_t *bars = (uint64_t *)(wgt + 8 * kRows);
   volatile int *abort_flag = (volatile int *)(bars + 2 * C::kStages);
   const uint32_t ring = smem_u32(smem), full0 = smem_u32(bars), empty0 = smem_u32(bars + C::kStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -819,7 +825,7 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full0 + 8 * i, C::kProd);
-      mbar_init(empty0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, C::kCols);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -831,34 +837,53 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
   pdl_wait();
   const TreeRange range = tree_range<C::kThreads, kWindowTile>(p, 1, warp_sum, &range_s);
   if (warp >= kCons) {
-    produce<D, kQ4, NB, kDup>(mp, range, ring, full0, empty0, abort_flag, warp - kCons, lane);
+    produce<D, kQ4, kRows>(mp, range, ring, full0, empty0, abort_flag, warp - kCons, lane);
     return;
   }
   const int r = lane >> 2, c = lane & 3, g = p.c.g;
-  TreeCursor<kWindowTile> cur(p, range);
-  TreeItem it;
+  const int team = warp / C::kCols, row0 = warp % C::kCols * (8 * NB);  // this warp's first row
+  using Cursor = TreeCursor<kWindowTile>;
+  Cursor &cur = *(Cursor *)cur_s[warp];
+  const TreeItem &it = item_s[warp];
+  const View &vw = view_s[warp];
+  {
+    const Cursor first(p, range);
+    if (lane == 0) cur = first;
+    __syncwarp();
+  }
   bool any = false, dead = false;
   int gs = 0;
-  while (cur.next(p, it)) {
+  for (;;) {
+    {
+      Cursor c1 = cur;
+      TreeItem i1;
+      const bool more = c1.next(p, i1);
+      __syncwarp();
+      if (!more) break;
+      if (lane == 0) {
+        cur = c1;
+        item_s[warp] = i1;
+        View v;
+        v.win = window_of(p, i1.head.h);
+        v.n = i1.head.n;
+        v.i0 = tree_first(p, i1);
+        v.rows = tree_rows(p, i1);
+        v.i1 = v.i0 + tree_div_g(p, v.rows - 1);
+        v.recip_g = p.recip_g;
+        view_s[warp] = v;
+      }
+      __syncwarp();
+    }
     any = true;
     const TreeHead &hd = it.head;
     const int i0 = tree_first(p, it), rows = tree_rows(p, it);
-    View<NB> vw;
-    vw.win = window_of(p, hd.h);
-    vw.n = hd.n;
-    vw.i0 = i0;
-    vw.i1 = i0 + tree_div_g(p, rows - 1);
     // queries: column n = lane / 4 of each block; scale: of the scores of columns 2c, 2c + 1
-    Queries<D, NB, C::kQShared> q;
-    float qs[NG][NB][2], qe[NG][NB][2], scale[NB][2];
-    if constexpr (C::kQShared) {
-      consumer_sync(kCons * 32);  // the item before has read its queries
-      q.at = qsm + lane * 8;
-    }
+    Queries<D, NB> q;
+    float qs[NG][NB][2], qe[NG][NB][2], scale[kQ4 ? NB : 1][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      if (!C::kQShared || nb % kCons == warp) {  // (shared: the warps share the work)
-        const int row = kDup ? r & 3 : 8 * nb + r;
+      {
+        const int row = kDup ? r & 3 : row0 + 8 * nb + r;
         const int nr = tree_div_g(p, row), j0 = row - nr * g;
         const uint16_t *src = (const uint16_t *)(p.q + (size_t)(hd.q0 + i0 + nr) * p.q_stride) +
                               ((size_t)hd.h * g + j0) * D;
@@ -915,22 +940,12 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
         }
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
-          if constexpr (C::kQShared) {
-            *(uint2 *)(qsm + ((nb * NK + j) * 32 + lane) * 8) = make_uint2(f[j][0], f[j][1]);
-          } else {
-            q.f[nb][j][0] = f[j][0];
-            q.f[nb][j][1] = f[j][1];
-          }
+          q.f[nb][j][0] = f[j][0];
+          q.f[nb][j][1] = f[j][1];
         }
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int own = kDup ? (2 * c + k) & 3 : 8 * nb + 2 * c + k;
-        vw.pos[nb][k] = own < rows ? hd.n + i0 + tree_div_g(p, own) : -1;
-        if constexpr (!kQ4) scale[nb][k] = p.scale_log2;
-      }
     }
-    if constexpr (C::kQShared) consumer_sync(kCons * 32);
+    if constexpr (!kQ4) scale[0][0] = scale[0][1] = p.scale_log2;
     State<D, kQ4, NB> s;
     s.vscale = 0x1p60f;
     s.vtop = 0.f;
@@ -947,9 +962,9 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
       }
     }
     const int nst = item_stages<C::kTokens>(it);
-    // this warp's stages: gs = warp (mod kCons)
-    int st = (warp - gs) % kCons;
-    for (st += st < 0 ? kCons : 0; st < nst && !dead; st += kCons) {
+    // this warp's stages: gs = team (mod kTeams)
+    int st = (team - gs) % kTeams;
+    for (st += st < 0 ? kTeams : 0; st < nst && !dead; st += kTeams) {
       const int at = gs + st, slot = at % C::kStages;
       bool ok = !*abort_flag;
       if (ok) ok = mbar_wait(full0 + 8 * slot, (at / C::kStages) & 1, p.wait_ns);
@@ -965,16 +980,18 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
       float *scores = p.scores ? window_scores(p, hd, it.group, (int64_t)it.t0 * kWindowTile + st * C::kTokens)
                                : nullptr;
       const uint8_t *kt = smem + slot * C::kStage, *vt = kt + C::kTile;
-      if (window_all_seen(vw.win, hd.n, vw.i0, vw.i1, t0, C::kTokens))
-        consume<D, kQ4, NB, kDup, false>(kt, vt, vw, t0, q, qs, qe, scale, s, scores, p.score_rows, lane);
-      else
-        consume<D, kQ4, NB, kDup, true>(kt, vt, vw, t0, q, qs, qe, scale, s, scores, p.score_rows, lane);
+      if (row0 >= rows) {  // few rows: none for this warp
+      } else if (window_all_seen(vw.win, hd.n, vw.i0, vw.i1, t0, C::kTokens)) {
+        consume<D, kQ4, kRows, false>(kt, vt, vw, t0, q, qs, qe, scale, s, scores, p.score_rows, row0, lane);
+      } else {
+        consume<D, kQ4, kRows, true>(kt, vt, vw, t0, q, qs, qe, scale, s, scores, p.score_rows, row0, lane);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * slot);
     }
     gs += nst;
     // ---- the consumer warps' states of this item meet
-    float *mw = rec + warp * C::kRec;
+    float *mw = rec + team * C::kRec + row0 * C::kMS;
     const float back = kQ4 ? 0.5f / s.vscale : 1.f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -1010,7 +1027,7 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
       if (r == 0 && (!kDup || c < 2))
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          ml[warp * C::kRows + 8 * nb + 2 * c + k] = make_float2(s.ref[nb][k], s.l[nb][k]);
+          ml[team * kRows + row0 + 8 * nb + 2 * c + k] = make_float2(s.ref[nb][k], s.l[nb][k]);
     }
     consumer_sync(kCons * 32);
     const bool whole = tree_whole(it);
@@ -1018,10 +1035,10 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
     if (tid < rows) {
       float M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kCons; ++w) M = fmaxf(M, ml[w * C::kRows + tid].x);
+      for (int w = 0; w < kTeams; ++w) M = fmaxf(M, ml[w * kRows + tid].x);
 #pragma unroll
-      for (int w = 0; w < kCons; ++w) {
-        const float2 v = ml[w * C::kRows + tid];
+      for (int w = 0; w < kTeams; ++w) {
+        const float2 v = ml[w * kRows + tid];
         const float f = v.x == v.x ? tree_weight(v.x, M) : v.x;
         wgt[tid * 8 + w] = f;
         L = fmaf(f, v.y, L);
@@ -1037,7 +1054,7 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
       const int row = i / (D / 4), d4 = 4 * (i - row * (D / 4));
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kCons; ++w) {
+      for (int w = 0; w < kTeams; ++w) {
         const float f = wgt[row * 8 + w];
         const float4 v = *(const float4 *)(rec + w * C::kRec + row * C::kMS + d4);
         O.x = fmaf(f, v.x, O.x);
@@ -1058,11 +1075,11 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, NB, kDup>::kThreads), kWindowBloc
   if (tid == 0) tree_describe(p, range, any ? &it : nullptr);
 }
 
-template <int D, bool kQ4, int NB, bool kDup>
+template <int D, bool kQ4, int kRows>
 cudaError_t launch_one(const WindowMmaParams &p, int blocks, cudaStream_t st) {
-  using C = Cfg<D, kQ4, NB, kDup>;
+  using C = Cfg<D, kQ4, kRows>;
   static int8_t done[64];
-  const auto kernel = window_mma_kernel<D, kQ4, NB, kDup>;
+  const auto kernel = window_mma_kernel<D, kQ4, kRows>;
   cudaError_t e = raise_smem_limit(done, (const void *)kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1082,12 +1099,12 @@ cudaError_t launch_one(const WindowMmaParams &p, int blocks, cudaStream_t st) {
 template <int D, bool kQ4>
 cudaError_t launch_rows(const WindowMmaParams &p, int blocks, cudaStream_t st) {
   switch (p.w.group_rows) {  // window_mma_rows
-    case 4: return launch_one<D, kQ4, 1, true>(p, blocks, st);
-    case 8: return launch_one<D, kQ4, 1, false>(p, blocks, st);
-    case 16: return launch_one<D, kQ4, 2, false>(p, blocks, st);
+    case 4: return launch_one<D, kQ4, 4>(p, blocks, st);
+    case 8: return launch_one<D, kQ4, 8>(p, blocks, st);
+    case 16: return launch_one<D, kQ4, 16>(p, blocks, st);
     default:
-      if constexpr (kQ4) return cudaErrorInvalidValue;
-      else return launch_one<D, kQ4, 4, false>(p, blocks, st);
+      if constexpr (kQ4) return cudaErrorInvalidValue;  // unreachable
+      else return launch_one<D, kQ4, 32>(p, blocks, st);
   }
 }
 
