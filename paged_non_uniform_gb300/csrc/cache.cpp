@@ -142,8 +142,9 @@ int window_shape(const kvx_cache *c, int max_q, bool weigh, WindowShape *t) {
   const int rc = kvx_device_sm_count(&sms);
   if (rc != KVX_OK) return rc;
   const int g = c->dev.g;
-  t->blocks = sms * kWindowBlocksPerSm;
-  t->rows = c->shape.dtype == KVX_F32 ? window_simt_rows() : window_mma_rows(max_q * g, c->shape.dtype == KVX_Q4);
+  const bool f32 = c->shape.dtype == KVX_F32;
+  t->rows = f32 ? window_simt_rows() : window_mma_rows(max_q * g, c->shape.dtype == KVX_Q4);
+  t->blocks = sms * (f32 ? kWindowBlocksPerSm : window_mma_blocks_per_sm(t->rows));
   t->tokens = t->rows / g;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t slots = (size_t)2 * t->blocks, row = (size_t)c->shape.D * sizeof(float);

@@ -67,6 +67,7 @@ constexpr int window_mma_rows(int rows, bool q4) {
   return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 || q4 ? 16 : 32;
 }
 constexpr int kWindowBlocksPerSm = 2;
+constexpr int window_mma_blocks_per_sm(int rows) { return rows == 32 ? 3 : 2; }
 cudaError_t launch_weigh(const WindowParams &p, int blocks, cudaStream_t st);
 
 // ---- rows of 4-bit caches, rows read back ----------------------------------

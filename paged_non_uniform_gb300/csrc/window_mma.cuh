@@ -52,17 +52,18 @@ template <int D, bool kQ4, int kRows_>
 struct Cfg {
   static constexpr int kRows = kRows_;
   static constexpr bool kDup = kRows == 4;
-  static constexpr int kCols = kQ4 || kRows <= 8 ? 1 : 2;
+  static constexpr int kCols = kQ4 || kRows <= 8 ? 1 : kRows / 8;
   static constexpr int NB = kRows <= 8 ? 1 : kRows / 8 / kCols;
   static constexpr int kTokens = kQ4 ? 64 : 32;  // of a stage
   static constexpr int kBox = kWindowBox;        // of a bf16 load, at most
   static constexpr int kTokenBytes = kQ4 ? q4_row_bytes(D) : 2 * D;
   static constexpr int kTile = kTokens * kTokenBytes;  // K (or V) bytes of a stage
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kTeams = kQ4 ? (NB == 1 ? 4 : 2) : kCols == 1 ? 3 : 2;  // takers of stages
+  static constexpr int kTeams = kQ4 ? (NB == 1 ? 4 : 2) : kCols == 1 ? 3 : kCols == 2 ? 2 : 1;  // takers of stages
   static constexpr int kCons = kTeams * kCols;                                 // consumer warps
-  static constexpr int kSteps = NB > 1 && !kQ4 ? 1 : 2;  // 16-token steps computed together
-  static constexpr int kStages = 2 * kTeams;
+  static constexpr int kBlocks = window_mma_blocks_per_sm(kRows);
+  static constexpr int kSteps = 2;  // 16-token steps computed together
+  static constexpr int kStages = kTeams == 1 ? 3 : 2 * kTeams;
   static constexpr int kProd = kQ4 ? 2 : 1;   // producer warps: K and V, or both in one
   static constexpr int kBatch = kQ4 ? 4 : 1;  // stages that a producer handles at once
   static constexpr int kThreads = 32 * (kCons + kProd);
@@ -72,7 +73,7 @@ struct Cfg {
   // ring | records | (max, sum) [kTeams][kRows] | weights [kRows][8] | barriers, flag
   static constexpr int kSmem =
       1024 + kRing + 4 * kTeams * kRec + 8 * kTeams * kRows + 32 * kRows + 16 * kStages + 16;
-  static_assert(kSmem + 2048 <= 227 * 1024 / kWindowBlocksPerSm, "resident blocks per SM");
+  static_assert(kSmem + 2048 <= 227 * 1024 / kBlocks, "resident blocks per SM");
   static_assert(kTeams <= 7, "a row's eighth weight is 1 / sum");
 };
 
@@ -800,7 +801,7 @@ __device__ __forceinline__ int query_dim(int j, int e, int c) {
 }
 
 template <int D, bool kQ4, int kRows>
-__global__ void __launch_bounds__((Cfg<D, kQ4, kRows>::kThreads), kWindowBlocksPerSm)
+__global__ void __launch_bounds__((Cfg<D, kQ4, kRows>::kThreads), (Cfg<D, kQ4, kRows>::kBlocks))
     window_mma_kernel(const __grid_constant__ WindowMmaParams mp) {
   using C = Cfg<D, kQ4, kRows>;
   constexpr int NK = D / 16, NG = kQ4 ? D / 64 : 1, NB = C::NB, kCons = C::kCons, kTeams = C::kTeams;
