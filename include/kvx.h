@@ -719,8 +719,9 @@ void kvx_cache_destroy(kvx_cache *cache);
 
 /* Failure-detection test hook (no effect unless called), as kvx_plan_inject_stall: block
  * `block` of kvx_tree_attn's tensor-core kernel waits for one arrival more than its first
- * K tile gets, so that the wait runs out after wait_limit_ns (1 ms .. 4 s; every
- * pipeline wait of later calls with this cache uses this limit, 2 s by default). The
+ * K tile gets (of kvx_window_attn's: for loads of its first tile that it leaves out), so that
+ * the wait runs out after wait_limit_ns (1 ms .. 4 s; every pipeline wait of later calls with
+ * this cache, and every wait of kvx_evict's, uses this limit, 2 s by default). The
  * call then finishes with KVX_DEV_TIMEOUT in its status word; its output is undefined,
  * the CUDA context stays usable. block < 0 turns the stall off (the limit stays as
  * given). Errors: KVX_EINVAL, KVX_ERANGE. */
@@ -947,7 +948,8 @@ int kvx_window_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
  * sequence, as for kvx_build_tables.
  * Launch: two kernels; pages are written by the second, which lets its dependents start
  * only when all is written. In it, waits for rows that have yet to be read by another block give
- * up after 2 s (KVX_DEV_TIMEOUT; the rows in question are not written).
+ * up after the cache's limit (kvx_cache_inject_stall, 2 s by default: KVX_DEV_TIMEOUT; the
+ * rows in question are not written, and the workspace must be cleared before the next call).
  * Errors: KVX_EINVAL, KVX_ECUDA.
  * ------------------------------------------------------------------------- */
 int kvx_evict_workspace_bytes(const kvx_cache *cache, size_t *bytes);
