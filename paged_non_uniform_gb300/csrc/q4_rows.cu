@@ -3,9 +3,9 @@
 //
 // Quantisation of a group of 64 elements x: lo = min x (a bf16 number, so exact), step =
 // bf16((max x - lo) / 15), code = min(15, rint((x - lo) / step)) in fp32; codes 0 where step is 0. A group with a non-finite element, or whose range is not finite,
-// gets step 0 and lo NaN, so that all of it reads as NaN. Eight lanes hold a group,
-// eight elements (a 16-byte load, a 4-byte word of codes) each; minimum and maximum
-// meet in three shuffles. Memory bounds both kernels.
+// gets step 0 and lo NaN, so that all of it reads as NaN. Four lanes hold a group,
+// sixteen elements (32 bytes in, two 4-byte words of codes out) each; minimum and maximum
+// meet in two shuffles. Memory bounds both kernels.
 #include <math.h>
 
 #include "ptx.cuh"
@@ -21,57 +21,78 @@ __device__ __forceinline__ int64_t pool_rows(const CacheDev &c, int grp) {
 }
 
 struct Quantised {
-  uint32_t codes, params;  // (lo << 16 | step, of the group)
+  uint32_t codes[2], params;  // two words; (lo << 16 | step, of the group)
 };
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *(const __nv_bfloat162 *)&x; }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *(const uint32_t *)&x; }
-// This lane's eight elements of its group; eight neighbouring lanes hold one.
-__device__ __forceinline__ Quantised quantise(const uint4 &x) {
+// fl(range / 15) to bf16: the product with a rounded 1 / 15 is within two units in the last place of
+// the quotient, which matters only next to the middle of two bf16 numbers.
+__device__ __forceinline__ __nv_bfloat16 step_of(float range) {
+  float q = range * (1.f / 15.f);
+  if (((__float_as_uint(q) + 4u) & 0xffffu) - 0x8000u <= 8u || q < 0x1p-100f) q = __fdiv_rn(range, 15.f);
+  return __float2bfloat16_rn(q);
+}
+// Settles an element whose estimated code c leaves e, half a step or nearly (quantise).
+__device__ __noinline__ float settle(float c, float e, float past, float step) {
+  const float middle = c + copysignf(0.5f, e);
+  // half a unit in the last place of the middle, twice
+  const float near = __uint_as_float((__float_as_uint(middle) & 0x7f800000u) - (23u << 23)) * step;
+  return past > near || (past >= -near && ((int)c & 1)) ? 2.f * middle - c : c;
+}
+
+// This lane's sixteen elements of its group; four neighbouring lanes hold one.
+__device__ __forceinline__ Quantised quantise(const uint4 (&x)[2]) {
   // (least, -greatest) of the group; NaN stays NaN
-  __nv_bfloat162 a = __hmin2_nan(__hmin2_nan(as_bf2(x.x), as_bf2(x.y)), __hmin2_nan(as_bf2(x.z), as_bf2(x.w)));
-  __nv_bfloat162 b = __hmax2_nan(__hmax2_nan(as_bf2(x.x), as_bf2(x.y)), __hmax2_nan(as_bf2(x.z), as_bf2(x.w)));
+  __nv_bfloat162 a = as_bf2(x[0].x), b = a;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a = __hmin2_nan(__hmin2_nan(a, as_bf2(x[i].x)), as_bf2(x[i].y));
+    a = __hmin2_nan(__hmin2_nan(a, as_bf2(x[i].z)), as_bf2(x[i].w));
+    b = __hmax2_nan(__hmax2_nan(b, as_bf2(x[i].x)), as_bf2(x[i].y));
+    b = __hmax2_nan(__hmax2_nan(b, as_bf2(x[i].z)), as_bf2(x[i].w));
+  }
   b = __hneg2(b);
   a = __hmin2_nan(__lows2bfloat162(a, b), __highs2bfloat162(a, b));
 #pragma unroll
-  for (int w = 1; w < 8; w <<= 1) a = __hmin2_nan(a, as_bf2(__shfl_xor_sync(0xffffffffu, as_u32(a), w)));
+  for (int w = 1; w < 4; w <<= 1) a = __hmin2_nan(a, as_bf2(__shfl_xor_sync(0xffffffffu, as_u32(a), w)));
   const float lo = __low2float(a), range = -__high2float(a) - lo;
-  if (!isfinite(range)) return {0u, 0x7fc00000u};
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
+  if (!isfinite(range)) return {{0u, 0u}, 0x7fc00000u};
+  const __nv_bfloat16 sb = step_of(range);
   const float step = __bfloat162float(sb);
-  float f[8];
+  Quantised q = {{0u, 0u}, pack_bf16(step, lo)};
+  // rint(fl(d / step)) without the division: c, the nearest integer to an estimate of the
+  // quotient, and e = d - c * step, exact in one multiply-add. Where 2 |e| is below step, c it
+  // is. Else d lies past the middle between c and its neighbour on e's side (the estimate was
+  // off), or so near it that the quotient would be rounded to it: then the even one of the two.
+  const bool usual = step >= 0x1p-120f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(step));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = unpack_bf16(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w);
-    f[2 * i] = v.x - lo;
-    f[2 * i + 1] = v.y - lo;
-  }
-  uint32_t codes = 0;
-  if (step >= 0x1p-120f) {
-    // rint(fl(d / step)) without the division: c, the nearest integer to an estimate of the
-    // quotient, and e = d - c * step, exact in one multiply-add. Where 2 |e| is below step, c it
-    // is. Else d lies past the middle between c and its neighbour on e's side (the estimate was
-    // off), or so near it that the quotient would be rounded to it: then the even one of the two.
-    const float r = __frcp_rn(step);
+  for (int k = 0; k < 2; ++k) {
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float c = fmaf(f[i], r, 12582912.f) - 12582912.f;  // 1.5 * 2^23
-      const float e = fmaf(-c, step, f[i]), past = fmaf(2.f, fabsf(e), -step);
-      if (past > -0x1p-20f * step) {
-        const float middle = c + copysignf(0.5f, e);
-        // half a unit in the last place of the middle, twice
-        const float near = __uint_as_float((__float_as_uint(middle) & 0x7f800000u) - (23u << 23)) * step;
-        if (past > near || (past >= -near && ((int)c & 1))) c = 2.f * middle - c;
-      }
-      f[i] = c;
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack_bf16(i == 0 ? x[k].x : i == 1 ? x[k].y : i == 2 ? x[k].z : x[k].w);
+      f[2 * i] = v.x - lo;
+      f[2 * i + 1] = v.y - lo;
     }
-    const float l = fmaf(fmaf(fmaf(f[3], 16.f, f[2]), 16.f, f[1]), 16.f, f[0]);
-    const float h = fmaf(fmaf(fmaf(f[7], 16.f, f[6]), 16.f, f[5]), 16.f, f[4]);
-    codes = __byte_perm(__float_as_uint(l + 8388608.f), __float_as_uint(h + 8388608.f), 0x5410);
-  } else if (step > 0.f) {
-    for (int i = 0; i < 8; ++i)
-      codes |= (uint32_t)fminf(15.f, rintf(__fdiv_rn(f[i], step))) << (4 * i);
+    if (usual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float c = fmaf(f[i], r, 12582912.f) - 12582912.f;  // 1.5 * 2^23
+        const float e = fmaf(-c, step, f[i]), past = fmaf(2.f, fabsf(e), -step);
+        if (past > -0x1p-20f * step) c = settle(c, e, past, step);
+        f[i] = c;
+      }
+      const float l = fmaf(fmaf(fmaf(f[3], 16.f, f[2]), 16.f, f[1]), 16.f, f[0]);
+      const float h = fmaf(fmaf(fmaf(f[7], 16.f, f[6]), 16.f, f[5]), 16.f, f[4]);
+      q.codes[k] = __byte_perm(__float_as_uint(l + 8388608.f), __float_as_uint(h + 8388608.f), 0x5410);
+    } else if (step > 0.f) {
+      for (int i = 0; i < 8; ++i)
+        q.codes[k] |= (uint32_t)fminf(15.f, rintf(__fdiv_rn(f[i], step))) << (4 * i);
+    }
   }
-  return {codes, pack_bf16(step, lo)};
+  return q;
 }
 
 // Steps through the (row, head) pairs of a call, `step` pairs at a time, without dividing.
@@ -94,10 +115,11 @@ struct Pairs {
   }
 };
 
-// One lane per eight elements of a (row, head), K and V together; two pairs in flight.
+// One lane per sixteen elements of a (row, head), K and V together (with eight, what a lane does
+// once took as long as its elements).
 template <int D>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 8;  // of a row
+  constexpr int kLanes = D / 16;  // of a row
   pdl_wait();
   const CacheDev &c = p.c;
   const int stated = p.q_start[c.B], rows = min(stated, p.max_rows);
@@ -105,44 +127,36 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const __grid_consta
     atomicOr(p.status, KVX_DEV_BAD_LENGTH);
   if (rows <= 0) return;
   const int64_t total = (int64_t)rows * c.Hkv;
-  const int w = (int)(threadIdx.x % kLanes);  // the row's word
-  const int at = D == 128 ? 2 * (w & 7) + (w >> 3) : w;
+  const int l = (int)(threadIdx.x % kLanes);  // words 2l and 2l + 1 of the row
+  const int at = D == 128 ? 4 * (l & 3) + (l >> 2) : 2 * l, next = D == 128 ? 2 : 1;
   // (lanes meet in shuffles: whole warps stay in the loop, a warp's first pair decides)
   const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   const int64_t lead = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / kLanes;
   Pairs q(first, (int64_t)gridDim.x * (kThreads / kLanes), c.Hkv);
-  for (int64_t i = lead; i < total; i += 2 * q.step) {
-    int64_t slot[2];
-    int grp[2];
-    uint4 kx[2], vx[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool in = q.rh < total;
-      slot[u] = -1;
-      grp[u] = c.head_grp[q.h];
-      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-      if (in) {
-        slot[u] = p.slots[q.rh];
-        const int64_t src = (int64_t)q.h * (D * 2) + w * 16;
-        kx[u] = *(const uint4 *)(p.k + q.r * p.k_stride + src);
-        vx[u] = *(const uint4 *)(p.v + q.r * p.v_stride + src);
-      }
-      q.next(c.Hkv);
+  for (int64_t i = lead; i < total; i += q.step, q.next(c.Hkv)) {
+    uint4 kx[2] = {}, vx[2] = {};
+    int64_t slot = -1;
+    if (q.rh < total) {
+      slot = p.slots[q.rh];
+      const int64_t src = (int64_t)q.h * (D * 2) + l * 32;
+      const uint4 *ks = (const uint4 *)(p.k + q.r * p.k_stride + src);
+      const uint4 *vs = (const uint4 *)(p.v + q.r * p.v_stride + src);
+      kx[0] = ks[0], kx[1] = ks[1], vx[0] = vs[0], vx[1] = vs[1];
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const Quantised k = quantise(kx[u]), v = quantise(vx[u]);
-      if (slot[u] < 0 || slot[u] >= pool_rows(c, grp[u])) {
-        if (slot[u] != -1 && w == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
-        continue;
-      }
-      const int64_t co = q4_codes(c, slot[u]) + at * 4, po = q4_params(c, slot[u]) + (w >> 3) * 4;
-      *(uint32_t *)(c.grp[grp[u]].k + co) = k.codes;
-      *(uint32_t *)(c.grp[grp[u]].v + co) = v.codes;
-      if ((w & 7) == 0) {
-        *(uint32_t *)(c.grp[grp[u]].k + po) = k.params;
-        *(uint32_t *)(c.grp[grp[u]].v + po) = v.params;
-      }
+    const Quantised k = quantise(kx), v = quantise(vx);
+    const CacheGroup &g = c.grp[c.head_grp[q.h]];
+    if (slot < 0 || slot >= pool_rows(c, c.head_grp[q.h])) {
+      if (slot != -1 && l == 0) atomicOr(p.status, KVX_DEV_BAD_BLOCK);
+      continue;
+    }
+    const int64_t co = q4_codes(c, slot) + at * 4, po = q4_params(c, slot) + (l >> 2) * 4;
+    *(uint32_t *)(g.k + co) = k.codes[0];
+    *(uint32_t *)(g.k + co + next * 4) = k.codes[1];
+    *(uint32_t *)(g.v + co) = v.codes[0];
+    *(uint32_t *)(g.v + co + next * 4) = v.codes[1];
+    if ((l & 3) == 0) {
+      *(uint32_t *)(g.k + po) = k.params;
+      *(uint32_t *)(g.v + po) = v.params;
     }
   }
   __threadfence();
@@ -233,7 +247,7 @@ cudaError_t launch(void (*kernel)(Params), const Params &p, int64_t lanes, cudaS
 
 cudaError_t launch_q4_append(const AppendParams &p, cudaStream_t st) {
   if (p.max_rows == 0) return cudaSuccess;
-  const int64_t lanes = (int64_t)p.max_rows * p.c.Hkv * (p.c.D / 8);
+  const int64_t lanes = (int64_t)p.max_rows * p.c.Hkv * (p.c.D / 16);
   return p.c.D == 128 ? launch(q4_append_kernel<128>, p, lanes, st)
                       : launch(q4_append_kernel<64>, p, lanes, st);
 }

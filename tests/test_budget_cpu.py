@@ -140,7 +140,7 @@ def test_page_writers_hold_their_dependents_back():
     rows, evict = kernels("q4_rows.cu"), kernels("evict.cu")
     assert set(rows) == {"q4_append_kernel", "read_kernel"}
     assert set(evict) == {"evict_select_kernel", "evict_move_kernel"}
-    for body, last in ((rows["q4_append_kernel"], ".v + po) ="), (evict["evict_move_kernel"], "write(before,")):
+    for body, last in ((rows["q4_append_kernel"], "g.v + po) ="), (evict["evict_move_kernel"], "write(before,")):
         assert "pdl_launch_dependents" not in body
         assert "__threadfence();" in body[body.rindex(last):]
     assert "grp.k" not in evict["evict_select_kernel"] and "grp.v" not in evict["evict_select_kernel"]
