@@ -35,17 +35,36 @@ struct TreeHead {
   int q0, T;     // first new row, new rows (0: nothing to do)
   int n;         // cached tokens
   int tiles, groups;
-  int lead, gap;  // windows (window_split.cuh): tiles before the gap, tiles left out
+  // windows (window_split.cuh): tiles before the gap, tiles left out, and the head's window
+  int lead, gap, sinks, width;
 };
+
+// The lengths of a head as they are in memory: loaded ahead of their use.
+struct TreeRaw {
+  int q0, q1, n, sinks, width;
+};
+__device__ __forceinline__ void tree_raw_window(const TreeParams &, int, TreeRaw &) {}
+template <class Prm>
+__device__ __forceinline__ TreeRaw tree_raw(const Prm &p, int hd) {
+  TreeRaw r = {0, 0, 0, 0, 0};
+  if (hd < p.c.B * p.c.Hkv) {
+    const int b = hd / p.c.Hkv;
+    r.q0 = p.q_start[b];
+    r.q1 = p.q_start[b + 1];
+    r.n = p.kv_len[hd];
+    tree_raw_window(p, hd - b * p.c.Hkv, r);
+  }
+  return r;
+}
 
 // What a tile and an item cost, by the kind of attention.
 __device__ __forceinline__ constexpr int tile_cost(const TreeParams &) { return kTileCost; }
 __device__ __forceinline__ constexpr int item_cost(const TreeParams &) { return kItemCost; }
 // A head's tiles: all of its keys.
 template <int kTile>
-__device__ __forceinline__ void tree_tiles(const TreeParams &, TreeHead &t) {
+__device__ __forceinline__ void tree_tiles(const TreeParams &, const TreeRaw &, TreeHead &t) {
   t.tiles = t.T > 0 ? (t.n + t.T + kTile - 1) / kTile : 0;
-  t.lead = t.gap = 0;
+  t.lead = t.gap = t.sinks = t.width = 0;
 }
 
 // Cost of a row group, and of the head.
@@ -56,21 +75,6 @@ __device__ __forceinline__ int tree_seg(const Prm &p, const TreeHead &t) {
 template <class Prm>
 __device__ __forceinline__ int64_t tree_cost(const Prm &p, const TreeHead &t) {
   return (int64_t)tree_seg(p, t) * t.groups;
-}
-
-// The lengths of a head as they are in memory: loaded ahead of their use.
-struct TreeRaw {
-  int q0, q1, n;
-};
-__device__ __forceinline__ TreeRaw tree_raw(const TreeParams &p, int hd) {
-  TreeRaw r = {0, 0, 0};
-  if (hd < p.c.B * p.c.Hkv) {
-    const int b = hd / p.c.Hkv;
-    r.q0 = p.q_start[b];
-    r.q1 = p.q_start[b + 1];
-    r.n = p.kv_len[hd];
-  }
-  return r;
 }
 
 // Head `hd` from its lengths; lengths that do not fit their arrays give T = 0
@@ -91,7 +95,7 @@ __device__ __forceinline__ TreeHead tree_head(const Prm &p, int hd, const TreeRa
     if (report) atomicOr(p.status, KVX_DEV_BAD_LENGTH);
     t.T = t.n = 0;
   }
-  tree_tiles<kTile>(p, t);
+  tree_tiles<kTile>(p, r, t);
   t.groups = t.T <= p.group_tokens ? 1 : (t.T + p.group_tokens - 1) / p.group_tokens;
   return t;
 }

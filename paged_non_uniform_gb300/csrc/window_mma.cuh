@@ -865,7 +865,7 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, kRows>::kThreads), (Cfg<D, kQ4, k
         cur = c1;
         item_s[warp] = i1;
         View v;
-        v.win = window_of(p, i1.head.h);
+        v.win = window_of(i1.head);
         v.n = i1.head.n;
         v.i0 = tree_first(p, i1);
         v.rows = tree_rows(p, i1);

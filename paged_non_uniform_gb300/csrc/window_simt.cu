@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, kWindowBlocksPerSm)
     any = true;
     const TreeHead &hd = it.head;
     const CacheGroup &grp = p.c.grp[p.c.head_grp[hd.h]];
-    const Window win = window_of(p, hd.h);
+    const Window win = window_of(hd);
     const int rank = p.c.head_row[hd.h], g = p.c.g, P = p.c.P;
     const int32_t *table = grp.table + (size_t)hd.b * grp.stride;
     const int i0 = tree_first(p, it), rows = tree_rows(p, it);

@@ -20,22 +20,25 @@ __device__ __forceinline__ constexpr int item_cost(const WindowParams &) { retur
 struct Window {
   int sinks, width;
 };
-__device__ __forceinline__ Window window_of(const WindowParams &p, int h) {
-  return {p.sinks ? max(0, p.sinks[h]) : 0, p.window ? max(0, p.window[h]) : INT32_MAX};
+__device__ __forceinline__ void tree_raw_window(const WindowParams &p, int h, TreeRaw &r) {
+  r.sinks = p.sinks ? p.sinks[h] : 0;
+  r.width = p.window ? p.window[h] : INT32_MAX;
 }
+__device__ __forceinline__ Window window_of(const TreeHead &t) { return {t.sinks, t.width}; }
 // Whether the row at position pos sees key t.
 __device__ __forceinline__ bool window_sees(const Window &w, int pos, int t) {
   return t <= pos && (t < w.sinks || t > pos - w.width);
 }
 
 template <int kTile>
-__device__ __forceinline__ void tree_tiles(const WindowParams &p, TreeHead &t) {
+__device__ __forceinline__ void tree_tiles(const WindowParams &, const TreeRaw &r, TreeHead &t) {
+  t.sinks = max(0, r.sinks);
+  t.width = max(0, r.width);
   t.tiles = t.lead = t.gap = 0;
   if (t.T <= 0) return;
-  const Window w = window_of(p, t.h);
   const int all = (t.n + t.T + kTile - 1) / kTile;
-  const int from = max(0, min(t.n, t.n - w.width + 1)) / kTile;
-  t.lead = min(all, w.sinks / kTile + (w.sinks % kTile ? 1 : 0));
+  const int from = max(0, min(t.n, t.n - t.width + 1)) / kTile;
+  t.lead = min(all, t.sinks / kTile + (t.sinks % kTile ? 1 : 0));
   t.gap = max(0, from - t.lead);
   t.tiles = all - t.gap;
 }
