@@ -98,14 +98,20 @@ __device__ __forceinline__ void codes_k(uint32_t w, uint32_t (&o)[4]) {
     o[2 * i + 1] = hsub2(both, low);
   }
 }
+// (a & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+  return d;
+}
 // 2 * code - 15 of the four nibbles of both 16-bit halves, exact: a code's bits one place up, with
 // a one below them, under the exponent of 1024 are 1024 + 2 code + 1, or 16 times that.
 __device__ __forceinline__ void codes_v(uint32_t y, uint32_t (&o)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t s = i ? y >> 7 : y << 1;
-    o[2 * i] = hsub2((s & 0x001e001eu) | 0x64016401u, 0x64106410u);  // 1040
-    o[2 * i + 1] = hfma2((s & 0x01e001e0u) | 0x64106410u, __float2half2_rn(0.0625f), __float2half2_rn(-80.f));
+    o[2 * i] = hsub2(and_or(s, 0x001e001eu, 0x64016401u), 0x64106410u);  // 1040
+    o[2 * i + 1] = hfma2(and_or(s, 0x01e001e0u, 0x64106410u), __float2half2_rn(0.0625f), __float2half2_rn(-80.f));
   }
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -496,8 +502,7 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
 
 // Whether some row of the item sees token t.
 __device__ __forceinline__ bool any_sees(const View &vw, int t) {
-  return t <= vw.n + vw.i1 &&
-         (t < vw.win.sinks || (t > vw.n + vw.i0 - vw.win.width && vw.win.width > 0));
+  return window_any_sees(vw.win, vw.n, vw.i0, vw.i1, t);
 }
 
 template <int D, int NB, int kSteps, bool kDup, bool kEdge, class S>

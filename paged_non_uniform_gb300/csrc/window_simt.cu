@@ -5,9 +5,10 @@
 // (window_split.cuh), in one pass over the visited tiles of 64 keys per group of 32 query
 // rows (running maximum and sum in fp32). K and V tiles are gathered from their
 // pages into shared memory; each thread computes a 4 x 4 block of scores and
-// accumulates 4 rows x D/16 dims of the output. A tile that some row sees only in part
-// takes a separate path that skips what a row does not see instead of multiplying
-// it by zero, so that NaN and infinities in unseen rows, and padding, have no influence.
+// accumulates 4 rows x D/16 dims of the output. Keys that no row of the item sees are not read.
+// In a tile that some row sees only in part, unseen scores become -inf; where such a tile's V is
+// not all finite, a separate path skips what a row does not see instead of multiplying it by
+// zero, so that NaN and infinities in unseen rows have no influence.
 #include <math.h>
 
 #include "window_split.cuh"
@@ -76,17 +77,20 @@ __global__ void __launch_bounds__(kThreads, kWindowBlocksPerSm)
     for (int tile = it.t0; tile < it.t1; ++tile) {
       const int t0 = window_tile(hd, tile) * kTile, valid = min(kTile, hd.n + hd.T - t0);
       const bool edge = !window_all_seen(win, hd.n, i0, i1, t0, kTile);
-      __syncthreads();  // the tile before is consumed
+      bool odd = false;  // infinities or NaN in V (or sums past fp32's range)
+      __syncthreads();   // the tile before is consumed
       for (int i = tid; i < kTile * CPR; i += kThreads) {
         const int t = i / CPR, c = i - t * CPR;
         float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-        if (t < valid) {
-          const int tok = t0 + t;
+        const int tok = t0 + t;
+        // (what no row sees is not read)
+        if (t < valid && (!edge || window_any_sees(win, hd.n, i0, i1, tok))) {
           const int page = table[tok >> p.c.lgP];
           if (page >= 0 && page < grp.pages) {
             const int64_t at = pool_row(p.c, grp, page, rank, tok & (P - 1)) * (D * 4) + c * 16;
             dk = *(const float4 *)(grp.k + at);
             dv = *(const float4 *)(grp.v + at);
+            odd |= !(fabsf(dv.x) + fabsf(dv.y) + fabsf(dv.z) + fabsf(dv.w) < INFINITY);
           } else if (c == 0) {
             atomicOr(p.status, KVX_DEV_BAD_PAGE);
           }
@@ -98,15 +102,10 @@ __global__ void __launch_bounds__(kThreads, kWindowBlocksPerSm)
         // visible keys of row r, word w: bits [32w, 32w + 32) of the tile
         const int r = tid >> 1, w = tid & 1;
         uint32_t bits = 0;
-        if (r < rows) {
-          const int pos = hd.n + i0 + tree_div_g(p, r);
-#pragma unroll 4
-          for (int e = 0; e < 32; ++e)
-            bits |= (window_sees(win, pos, t0 + 32 * w + e) ? 1u : 0u) << e;
-        }
+        if (r < rows) bits = window_bits(win, hd.n + i0 + tree_div_g(p, r), t0 + 32 * w);
         sm.seen[r][w] = bits;
       }
-      __syncthreads();
+      const bool skip = __syncthreads_or(edge && odd);
       float s[4][4];
 #pragma unroll
       for (int a = 0; a < 4; ++a)
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, kWindowBlocksPerSm)
         }
       }
       __syncwarp();  // a row's scores are written and read by one half-warp
-      if (!edge) {
+      if (!skip) {
 #pragma unroll 2
         for (int t = 0; t < kTile; t += 4) {
           float pa[4][4];

@@ -53,6 +53,17 @@ __device__ __forceinline__ bool window_all_seen(const Window &w, int n, int i0, 
   return t0 + len - 1 <= n + i0 && (t0 + len <= w.sinks || t0 > n + i1 - w.width);
 }
 
+// Whether one of the rows [i0, i1] sees key t.
+__device__ __forceinline__ bool window_any_sees(const Window &w, int n, int i0, int i1, int t) {
+  return t <= n + i1 && (t < w.sinks || (t > n + i0 - w.width && w.width > 0));
+}
+// The keys base .. base + 31 that the row at position pos sees, as bits.
+__device__ __forceinline__ uint32_t window_bits(const Window &w, int pos, int base) {
+  auto ones = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+  const int from = max(0, pos - w.width + 1);
+  return ones(pos + 1 - base) & (ones(w.sinks - base) | ~ones(from - base));
+}
+
 // Scores of an item's visited key `key` (tile * kTile + place): one row group's.
 __device__ __forceinline__ float *window_scores(const WindowParams &p, const TreeHead &t, int group,
                                                 int64_t key) {
