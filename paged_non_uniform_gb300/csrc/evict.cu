@@ -33,6 +33,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
+// The weight that a key other than 0 was made of (-0 as 0).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
 struct Head {
   int b, h, n, m, first, last;  // cached, kept; tokens kept at the front and from `last` on
   bool evict;
@@ -102,10 +107,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     if (page < 0 || page >= grp.pages) return 0u;
     return weight_key(weights[place(page, t)]);
   };
-  auto key = [&](int t) -> uint32_t {
-    return t - t_lo < kKeys ? sm.keys[t - t_lo] : load_key(t, table[t >> p.c.lgP]);
-  };
   const int a_lo = max(t_lo, hd.first), a_hi = min(t_hi, hd.last);  // this run's part that competes
+  const int k_hi = min(t_hi, t_lo + kKeys);                         // keys in shared memory
   if (rank == 0 && tid == 0) sm.start = units ? atomicAdd(p.counters, (uint32_t)units) : 0u;
   // All blocks of the head have written what the others read next.
   auto meet = [&]() {
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   uint32_t prefix = 0, left = 0;  // found digits; keys to take among those that share them
   if (hd.evict) {
     left = (uint32_t)(hd.m - hd.first - (hd.n - hd.last));
-    const int end = min(t_hi, t_lo + kKeys);
+    const int end = k_hi;
     for (int t0 = t_lo + tid; t0 < end; t0 += 8 * kThreads) {  // eight in flight
       int page[8];
       uint32_t k[8];
@@ -137,17 +140,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int t0 = a_lo + 32 * warp; t0 < a_hi; t0 += kThreads) {
-      const int t = t0 + lane;
-      const uint32_t k = t < a_hi ? key(t) : 0u, digit = k >> shift & ((1u << bits) - 1u);
+    auto count = [&](bool in, uint32_t k) {
+      const uint32_t digit = k >> shift & ((1u << bits) - 1u);
       if (pass == 0) {
         // Weights share leading digits: one add for all lanes of a digit (adds to one address go
         // one after the other).
-        const uint32_t same = __match_any_sync(0xffffffffu, t < a_hi ? digit : (uint32_t)kBins);
-        if (t < a_hi && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], (uint32_t)__popc(same));
-      } else if (t < a_hi && (k >> (shift + bits)) == (prefix >> (shift + bits))) {
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : (uint32_t)kBins);
+        if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[digit], (uint32_t)__popc(same));
+      } else if (in && (k >> (shift + bits)) == (prefix >> (shift + bits))) {
         atomicAdd(&hist[digit], 1u);
       }
+    };
+    const int split = min(a_hi, max(a_lo, k_hi));
+    for (int t0 = a_lo + 32 * warp; t0 < split; t0 += kThreads) {
+      const int t = t0 + lane;
+      count(t < split, t < split ? sm.keys[t - t_lo] : 0u);
+    }
+    for (int t0 = split + 32 * warp; t0 < a_hi; t0 += kThreads) {
+      const int t = t0 + lane;
+      count(t < a_hi, t < a_hi ? load_key(t, table[t >> p.c.lgP]) : 0u);
     }
     meet();
     // Bins from the last down, kEach to a thread, of all blocks; the keys in higher bins.
@@ -198,7 +209,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     for (int w0 = warp; w0 < kKeys / 32 && t0 + 32 * w0 < t_hi; w0 += kThreads / 32) {
       const int t = t0 + 32 * w0 + lane;
       const bool in = t < t_hi, mid = in && hd.evict && t >= hd.first && t < hd.last;
-      const uint32_t k = mid && some ? key(t) : 0u;
+      const uint32_t k = !mid || !some ? 0u
+                         : t0 == t_lo  ? sm.keys[t - t_lo]
+                                       : load_key(t, table[t >> p.c.lgP]);
       const uint32_t ab = __ballot_sync(0xffffffffu, in && (!mid || (some && k > prefix)));
       const uint32_t eq = __ballot_sync(0xffffffffu, mid && some && k == prefix);
       if (lane == 0) {
@@ -283,18 +296,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       if (!p.copy_weights) continue;  // (in place, weights move with their rows)
       int pf[8], pt[8];
       float wt[8];
+      bool look[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        pf[u] = to[u] >= 0 ? table[from[u] >> p.c.lgP] : 0;
+        const uint32_t k = to[u] >= 0 && hd.evict && t0 == t_lo ? sm.keys[from[u] - t_lo] : 0u;
+        wt[u] = key_weight(k);
         pt[u] = to[u] >= 0 ? table[to[u] >> p.c.lgP] : 0;
+        // (key 0: not in shared memory, NaN, or a page outside the pool)
+        look[u] = to[u] >= 0 && k == 0u;
+        pf[u] = look[u] ? table[from[u] >> p.c.lgP] : 0;
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        if (to[u] >= 0 && (pf[u] < 0 || pf[u] >= grp.pages || pt[u] < 0 || pt[u] >= grp.pages)) {
+        const bool ok = pt[u] >= 0 && pt[u] < grp.pages && pf[u] >= 0 && pf[u] < grp.pages;
+        if (!ok) {
           atomicOr(p.status, KVX_DEV_BAD_PAGE);
           to[u] = -1;
         }
-        if (to[u] >= 0) wt[u] = weights[place(pf[u], from[u])];
+        if (ok && look[u]) wt[u] = weights[place(pf[u], from[u])];
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
