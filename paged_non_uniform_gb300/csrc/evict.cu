@@ -535,13 +535,14 @@ cudaError_t launch_select(const EvictParams &p, int C, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
-  // Short heads: a small block each, many to an SM. Long ones: as many blocks (two to an SM) as
-  // their keys fill, and more where there are few heads. 128 heads of 8k to 32k tokens: one block a
-  // head (of 1024 threads) 74 us, two 58, four 62, eight 105 (cluster barriers).
+  // Many short heads: a small block each, many to an SM. Else two blocks to an SM, and a head's
+  // blocks as many as its keys fill, or, where heads are few, as give each 4096 of them. 128 heads of
+  // 8k to 32k tokens: one block a head (of 1024 threads) 74 us, two 58, four 62, eight 105
+  // (cluster barriers).
   const int heads = p.c.B * p.c.Hkv;
   const int64_t longest = p.chunks / heads * kChunk;  // (their mean room)
   int C = 1;
-  while (C < 8 && (C * heads < 152 || C * 16384 < longest)) C *= 2;
+  while (C < 8 && ((C * heads < 152 && C * 4096 < longest) || C * 16384 < longest)) C *= 2;
   cudaError_t e = longest <= 4096 && heads >= 152 ? launch_select<256, 4096>(p, 1, st)
                                                   : launch_select<512, 16384>(p, C, st);
   if (e != cudaSuccess) return e;
