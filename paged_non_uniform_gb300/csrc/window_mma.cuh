@@ -2,15 +2,17 @@
 // cache, on warp-level tensor-core MMAs; bf16 and 4-bit caches.
 //
 // The keys that a head visits come in tiles of 64 (window_split.cuh), its query rows in
-// groups of 8 * NB columns (or 4, below). Blocks take equal parts of all (row group, tile)
-// units, found on the device from the lengths. In a block one producer warp walks the items and
-// loads stages of 32 tokens (K and V) into a ring in shared memory; each consumer warp takes
-// every kCons-th stage and holds its own running maximum, sum and output, which meet in
-// shared memory at an item's end. Per stage a warp computes S^T = K Q^T (m16n8k16: 16 tokens x
-// 8 query rows), the softmax on the accumulators (column maxima by shuffles), turns P into
-// the B operand with movmatrix, and O^T = V^T P^T in fresh accumulators that are then added to
-// the output in fp32: the tensor cores truncate their sums, and a chain of two 16-token
-// steps keeps that below the rounding of P.
+// groups of 4, 8, 16 or 32 (Cfg). Blocks take equal parts of all (row group, tile) units, found on
+// the device from the lengths. In a block the producer warps walk the items and load stages of 32
+// tokens (4 bits: 64) of K and V into a ring in shared memory; teams of one or more consumer
+// warps, each warp with 8 of the group's rows, take the stages in turn. A team holds its own
+// reference, sum and output, which meet in shared memory at an item's end. Per stage a warp computes
+// S^T = K Q^T (m16n8k16: 16 tokens x 8 query rows), the softmax on the accumulators, turns P into the
+// B operand with movmatrix, and O^T = V^T P^T in fresh accumulators that are then added to the
+// output in fp32: the tensor cores truncate their sums, and a chain of two 16-token steps keeps
+// that below the rounding of P. (mma.sync, not tcgen05: a decode step has 4 to 8 rows of the 128
+// that an operand of tcgen05 has, and what it waits for is memory; and three parts of P beside S
+// and O are more than tensor memory holds for two blocks an SM.)
 // P is split into three bf16 parts (24 bits), 4-bit caches: two fp16 parts (22). With at most
 // four query rows (a decode step of up to four heads a KV head) the columns 4 .. 7 repeat
 // the rows 0 .. 3, so that one MMA multiplies two parts: high in the first four columns, next in
@@ -19,7 +21,7 @@
 // bf16 stages: bulk-tensor boxes of up to 32 tokens of one head, [8-token group][64-dim
 // half][8 rows][128 B] with 128-byte swizzle. Tensor-core operands by ldmatrix.
 //
-// 4-bit stages: bulk copies of the codes and parameters of up to 32 tokens (window.h). Codes become
+// 4-bit stages: bulk copies of the codes and parameters of up to 64 tokens (window.h). Codes become
 // fp16 in registers, two at a time: bits put under the exponent of 1024, and one subtraction
 // or multiply-add (codes_k, codes_v). They go to the MMAs unscaled:
 //   S = sum_g step_g sum_{d in g} q_d c_d + lo_g sum_{d in g} q_d
@@ -31,6 +33,20 @@
 // permute of their words brings equal elements side by side. The MMAs' inner dimension has no order
 // of its own, so a lane takes the elements that its loads bring: eight neighbours of both
 // groups of a row for V, sixteen for K.
+//
+// Measured on one GB300 (a call in a graph):
+//  * bf16, 16 sequences of 8k to 32k, one token, two of eight heads unlimited, the others with
+//    windows of 4096: 88 us for 526 MB (6.0 TB/s; the copy rate in the middle, about 10 us of
+//    ramp, last output and merge). 8 x 122k: 587 us for 4.0 GB (6.8 TB/s).
+//  * bf16, up to 8 drafts of 5 query heads, windows of 1000 in half of the heads: 206 us for 676 MB.
+//    Latency bounds it: 12 consumer warps an SM (128 registers) issue on 38 % of the cycles, the
+//    tensor pipe is 38 % busy. 32 rows in one warp took 413, 16 in one of two warps 254.
+//  * 4 bits, 16 sequences of 8k to 32k: 48 us for 121 MB; 8 x 122k 270 us for 1.13 GB (4.2 TB/s).
+//    Instructions bound it: about 760 for 32 tokens, 330 of them on the half-rate integer pipe, most to
+//    make fp16 of codes. Without any of that work the loads take 177 us; one load at a time, in
+//    the producer's own latency, took 560.
+// Tried and slower: 4-bit stages for six or seven consumer warps of 128 registers (334), single 16-token
+// steps (297), f32 pairs only in scalar form (+3 %); for 32 rows four blocks an SM (219).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -39,9 +55,7 @@
 #include "window_split.cuh"
 
 namespace kvx {
-
 namespace wmma {
-
 
 constexpr uint32_t kAll = 0xffffffffu;
 

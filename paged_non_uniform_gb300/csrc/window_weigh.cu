@@ -5,6 +5,9 @@
 // maximum and sum, which are only known when all of a head's pieces are merged: hence
 // the stored scores and a launch of its own. A token's rows are added in a fixed order, so
 // nothing depends on timing. Blocks take equal parts of all heads' visited tiles.
+// Recomputing the scores instead would read K again, 256 bytes a token where a decode step of
+// four query heads stores and reads 32. Measured on one GB300, the launch alone: 16 sequences of 8k to
+// 32k, one row of 4 heads, about 10 us of the call's 87; 4 sequences, 32 rows (200 MB of scores) 60 us.
 #include <math.h>
 
 #include "window_split.cuh"
