@@ -15,8 +15,8 @@
 // before it has read), and writes. So a head moves on all SMs at once, in place, with
 // one read and one write of every row that moves.
 // Measured on one GB300 (a call in a graph): 128 heads of 8k to 32k tokens cut to 10 to 50 % (a quarter
-// keep all), 419 MB, 128 us: 50 of it the first launch (instructions: loads, three passes and
-// the places of 2.4 M keys), 80 the second (356 MB, 4.4 TB/s: two blocks an SM, each with two units
+// keep all), 419 MB, 128 us: 50 of it the first launch (latency of
+// the loads and the three passes), 80 the second (356 MB, 4.4 TB/s: two blocks an SM, each with two units
 // of 32 KB under way, are bound by the latency of a unit's steps). 512 short heads, half of them
 // cut to an eighth, 61 MB, 36 us: latency.
 #include <math.h>
@@ -357,7 +357,7 @@ constexpr int kFull = 1, kFree = kFull + kRing, kMove = kFree + kRing;
 // kPieces pieces of type V make a row's K, as many its V. 4-bit rows: the last piece is the
 // row's parameters. Two warps look up the places of the units to come; the others read unit
 // i + 1 before they wait for the units before unit i and write it, so that a unit is
-// read long before another one needs that (said only after unit i is written: 132 -> 175 us).
+// read long before another one needs that (said only after unit i is written, a call took 228 us instead of 183).
 template <class V, int kPieces, bool kQ4>
 __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kRow = 2 * kPieces;
@@ -541,8 +541,8 @@ cudaError_t launch_select(const EvictParams &p, int C, cudaStream_t st) {
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
   // Many short heads: a small block each, many to an SM. Else two blocks to an SM, and a head's
   // blocks as many as its keys fill, or, where heads are few, as give each 4096 of them. 128 heads of
-  // 8k to 32k tokens: one block a head (of 1024 threads) 74 us, two 58, four 62, eight 105
-  // (cluster barriers).
+  // 8k to 32k tokens: one block a head 122 us (keys past its shared memory are read in every
+  // pass), two 50, four 56, eight 98.
   const int heads = p.c.B * p.c.Hkv;
   const int64_t longest = p.chunks / heads * kChunk;  // (their mean room)
   int C = 1;

@@ -42,11 +42,11 @@
 //    Latency bounds it: 12 consumer warps an SM (128 registers) issue on 38 % of the cycles, the
 //    tensor pipe is 38 % busy. 32 rows in one warp took 413, 16 in one of two warps 254.
 //  * 4 bits, 16 sequences of 8k to 32k: 48 us for 121 MB; 8 x 122k 270 us for 1.13 GB (4.2 TB/s).
-//    Instructions bound it: about 760 for 32 tokens, 330 of them on the half-rate integer pipe, most to
-//    make fp16 of codes. Without any of that work the loads take 177 us; one load at a time, in
-//    the producer's own latency, took 560.
-// Tried and slower: 4-bit stages for six or seven consumer warps of 128 registers (334), single 16-token
-// steps (297), f32 pairs only in scalar form (+3 %); for 32 rows four blocks an SM (219).
+//    Instructions bound it: about 760 for 32 tokens, 325 of them on the half-rate integer pipe. Without
+//    any of that work the loads take 177 us, in batches of four stages; stage by stage they took 559.
+// Tried and slower: with 4 bits (288 at that time) six consumer warps on stages of 32 tokens (334, 342
+// in single 16-token steps), on as many stages of 64 as warps (505), four on stages of 32 tokens
+// (298), single 16-token steps (297); for 32 rows four blocks an SM (209 -> 219).
 #pragma once
 
 #include <cuda_fp16.h>
