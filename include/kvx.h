@@ -904,12 +904,15 @@ int kvx_read_kv(const kvx_cache *cache, const int32_t *q_start, const int64_t *s
  *                      w_t = (t < n[b][h] ? w_t : 0) + sum of softmax_t
  *                  over the sequence's new rows and the g query heads: new tokens start at 0.
  *                  Weights of tokens that no row sees keep their value. Sums are made in
- *                  a fixed order (equal inputs give equal bits).
+ *                  a fixed order (equal inputs give equal bits). With weights a page belongs
+ *                  to one sequence, as for kvx_build_tables.
  *   workspace      >= kvx_window_attn_workspace_bytes(cache, max_q, weights != NULL). With
  *                  weights it holds a score for every query row and token that the page
  *                  tables have room for, 4 * max_q * g bytes a token of a head.
  *   q, max_q, scale, out: as for kvx_tree_attn. 4-bit caches compute with lo + step * code
- *                  unrounded.
+ *                  unrounded; steps must not be negative (kvx_append_kv makes none that are). A
+ *                  token's weight times its step of V is off by at most 2^-22 of itself or 2^-36 of the
+ *                  head's largest step, and K's steps and lo have to stay below 2^90 in magnitude.
  * The same lengths are out of range, page ids outside a pool read as zero rows
  * (KVX_DEV_BAD_PAGE; their weights are lost), and so much work that (tiles + 1) over all
  * heads and groups of query rows pass 2^31 is refused whole (KVX_DEV_BAD_LENGTH).

@@ -50,6 +50,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include "window_split.cuh"
@@ -422,7 +423,7 @@ __device__ __forceinline__ void scores_q4(const uint8_t *codes, const uint8_t *p
 // then need neither the columns' maxima nor a rescaled output. (4-bit caches: p * step stays
 // below 2^(12 + kSlack) in fp16.)
 constexpr float kSlack = 3.f;
-constexpr float kNoRef = -3e38f;  // of a row that has seen nothing
+constexpr float kNoRef = -FLT_MAX;  // of a row that has seen nothing
 
 // x[mt][nb][e]: token mt * 16 + r (+ 8 for e >= 2), query row 8 nb + 2c + (e & 1). Masks and
 // scales the scores, stores them where weights want them, and makes them weights. seen (kEdge):
@@ -468,8 +469,10 @@ __device__ __forceinline__ void softmax(float (&x)[kSteps][NB][4], const float (
       for (int mt = 0; mt < kSteps; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          const float2 v = fma2(make_float2(x[mt][nb][e], x[mt][nb][e + 1]),
-                                make_float2(sc(nb, 0), sc(nb, 1)),
+          // The product is rounded as the reference was: one multiply-add would leave the reference's
+          // rounding in all weights, which passes any number where scores are large. (A packed product
+          // and sum are joined into one by the assembler; __fmul_rn is not.)
+          const float2 v = add2(make_float2(__fmul_rn(x[mt][nb][e], sc(nb, 0)), __fmul_rn(x[mt][nb][e + 1], sc(nb, 1))),
                                 make_float2(-s.ref[nb][0], -s.ref[nb][1]));
           y[mt][nb][e] = v.x, y[mt][nb][e + 1] = v.y;
           top = fmaxf(top, fmaxf(v.x, v.y));
