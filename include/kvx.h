@@ -953,7 +953,8 @@ int kvx_window_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
  * only when all is written. In it, waits for rows that have yet to be read by another block give
  * up after the cache's limit (kvx_cache_inject_stall, 2 s by default: KVX_DEV_TIMEOUT; the
  * rows in question are not written, and the workspace must be cleared before the next call).
- * Errors: KVX_EINVAL, KVX_ECUDA.
+ * Errors: KVX_EINVAL, KVX_ERANGE (page tables of 2^32 - 1 chunks of 64 tokens or more, over all
+ * heads), KVX_ECUDA.
  * ------------------------------------------------------------------------- */
 int kvx_evict_workspace_bytes(const kvx_cache *cache, size_t *bytes);
 

@@ -2,8 +2,8 @@
 // cache, and rows of any cache read back from their slots.
 //
 // Quantisation of a group of 64 elements x: lo = min x (a bf16 number, so exact), step =
-// bf16((max x - lo) / 15), code = min(15, rint((x - lo) / step)) in fp32; codes 0 where step is 0. A group with a non-finite element, or whose range is not finite,
-// gets step 0 and lo NaN, so that all of it reads as NaN. Four lanes hold a group,
+// bf16((max x - lo) / 15), code = min(15, rint((x - lo) / step)) in fp32; codes 0 where step is
+// 0. A group with a non-finite element, or whose range is not finite, gets step 0 and lo NaN, so that all of it reads as NaN. Four lanes hold a group,
 // sixteen elements (32 bytes in, two 4-byte words of codes out) each; minimum and maximum
 // meet in two shuffles.
 // Measured on one GB300: 44k rows of 8 heads quantised in 75 us (230 MB; instructions bound it: with

@@ -29,7 +29,7 @@ __host__ __device__ inline int64_t q4_params(const CacheDev &c, int64_t row) {
 
 // ---- attention ------------------------------------------------------------
 constexpr int kWindowTile = 64;  // keys of a tile
-constexpr int kWindowBox = 32;   // of a stage of the tensor-core kernels, and of a load at most
+constexpr int kWindowBox = 32;   // of a stage of bf16 caches, and of a load at most
 
 struct WindowParams : TreeParams {
   const int32_t *sinks, *window;  // [Hkv], or null: no sinks, everything visible
