@@ -915,7 +915,8 @@ int kvx_read_kv(const kvx_cache *cache, const int32_t *q_start, const int64_t *s
  *                  head's largest step, and K's steps and lo have to stay below 2^90 in magnitude.
  * The same lengths are out of range, page ids outside a pool read as zero rows
  * (KVX_DEV_BAD_PAGE; their weights are lost), and so much work that (tiles + 1) over all
- * heads and groups of query rows pass 2^31 is refused whole (KVX_DEV_BAD_LENGTH).
+ * heads and groups of query rows pass 2^31 is refused whole (KVX_DEV_BAD_LENGTH). A call that
+ * ends with KVX_DEV_TIMEOUT in its status word leaves the weights as they were.
  * Launch: two kernels, with weights three.
  * Errors: KVX_EINVAL, KVX_ERANGE (max_q, max_rows), KVX_ECUDA.
  * ------------------------------------------------------------------------- */

@@ -37,6 +37,9 @@ __global__ void __launch_bounds__(kThreads, kLanes == 1 ? 4 : 3) weigh_kernel(co
   const int tid = threadIdx.x, sub = tid % kLanes;
   pdl_launch_dependents();
   pdl_wait();
+  // After a wait that ran out the scores of the stages left out are an earlier call's: the weights,
+  // which are the sum of all calls, stay as they are.
+  if (*(volatile const uint32_t *)p.status & KVX_DEV_TIMEOUT) return;
   // (the params count a head as one row group here; group_tokens are the attention launch's)
   const TreeRange range = tree_range<kThreads, kTile>(p, 1, sm.warp_sum, &sm.range);
   TreeCursor<kTile> cur(p, range);
