@@ -928,7 +928,10 @@ __global__ void __launch_bounds__((Cfg<D, kQ4, kRows>::kThreads), (Cfg<D, kQ4, k
               top = max(top, max((f[j][e] & 0x7fffu) << 16, f[j][e] & 0x7fff0000u));
           top = max(top, __shfl_xor_sync(kAll, top, 1));
           top = max(top, __shfl_xor_sync(kAll, top, 2));
-          const int ex = min(254, max(1, 268 - (int)(top >> 23)));
+          // (and no further than back, below, is a normal number: -inf times 0 would be NaN. Elements
+          // that this leaves too small for fp16 move no score by more than 2^-45, see the header's limits.)
+          const int most = min(254, (int)(__float_as_uint(p.scale_log2) >> 23) + 126);
+          const int ex = max(1, min(most, 268 - (int)(top >> 23)));
           const float mul = __uint_as_float((uint32_t)ex << 23);
           float sum[NG], even[NG];
 #pragma unroll
