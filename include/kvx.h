@@ -719,7 +719,8 @@ void kvx_cache_destroy(kvx_cache *cache);
 
 /* Failure-detection test hook (no effect unless called), as kvx_plan_inject_stall: block
  * `block` of kvx_tree_attn's tensor-core kernel waits for one arrival more than its first
- * K tile gets (of kvx_window_attn's: for loads of its first tile that it leaves out), so that
+ * K tile gets (of kvx_window_attn's: for loads of its first tile that it leaves out; of
+ * kvx_evict's second kernel: does not say that its first 64 rows have been read), so that
  * the wait runs out after wait_limit_ns (1 ms .. 4 s; every pipeline wait of later calls with
  * this cache, and every wait of kvx_evict's, uses this limit, 2 s by default). The
  * call then finishes with KVX_DEV_TIMEOUT in its status word; its output is undefined,
@@ -951,9 +952,11 @@ int kvx_window_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
  * as NaN, and a move from or to one is skipped (KVX_DEV_BAD_PAGE). A page belongs to one
  * sequence, as for kvx_build_tables.
  * Launch: two kernels; pages are written by the second, which lets its dependents start
- * only when all is written. In it, waits for rows that have yet to be read by another block give
- * up after the cache's limit (kvx_cache_inject_stall, 2 s by default: KVX_DEV_TIMEOUT; the
- * rows in question are not written, and the workspace must be cleared before the next call).
+ * only when all is written. It moves 64 places of a head at a time; waits for rows that have yet to
+ * be read by another block give up after the cache's limit (kvx_cache_inject_stall, 2 s by default:
+ * KVX_DEV_TIMEOUT). The 64 places that such a wait was for are not written (K, V and, in place, weights;
+ * a block that has given up once no longer waits), all others are, and kv_len_out holds the new
+ * lengths: the head has lost what was to move there. The workspace must be cleared before the next call.
  * Errors: KVX_EINVAL, KVX_ERANGE (page tables of 2^32 - 1 chunks of 64 tokens or more, over all
  * heads), KVX_ECUDA.
  * ------------------------------------------------------------------------- */

@@ -594,6 +594,7 @@ extern "C" int kvx_evict(const kvx_cache *c, const int32_t *kv_len, const int32_
   p.units = (EvictUnit *)(ws + KVX_WS_HEADER_BYTES);
   p.read_done = (uint32_t *)(ws + w.read_done);
   p.source = (int32_t *)(ws + w.source);
+  p.stall_block = c->stall_block;
   p.wait_ns = c->wait_ns;
   const cudaError_t e = launch_evict(p, (cudaStream_t)stream);
   return e == cudaSuccess ? KVX_OK : set_cuda_error(e);

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
   constexpr int kEach = (kChunk * kRow + kMovers - 1) / kMovers;  // pieces of a thread
   __shared__ Places ring[kRing];
   __shared__ uint32_t ticket;
-  __shared__ int failed;
+  __shared__ uint32_t failed;
   const int tid = threadIdx.x;
   if (tid == 0) failed = 0;
   __syncthreads();
@@ -444,21 +444,24 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
       }
       if (weighs(m)) wt = p.weights[gi][m.src[tid]];
     };
+    // (the barrier after its use lies before the next unit's)
+    volatile uint32_t *const given_up = &failed;  // one more than the last unit whose wait ran out, or 0
     auto write = [&](const Places &m, const V(&v)[kEach], float wt) {
-      // Units before this one that read what it overwrites.
+      // Units before this one that read what it overwrites. A block that has given up once looks, but
+      // waits no more, so that it ends; only units whose places are still needed stay unwritten.
       for (int c = m.un.wait_from + tid; c < m.un.chunk; c += kMovers) {
         const uint32_t *flag = p.read_done + (m.unit - (uint32_t)(m.un.chunk - c));
         if (ld_acquire(flag)) continue;
         const uint64_t t0 = globaltimer_ns();
         while (!ld_acquire(flag))
-          if (globaltimer_ns() - t0 > p.wait_ns) {
+          if (*given_up || globaltimer_ns() - t0 > p.wait_ns) {
             atomicOr(p.status, KVX_DEV_TIMEOUT);
-            *(volatile int *)&failed = 1;
+            *given_up = m.unit + 1u;
             break;
           }
       }
       bar_sync(kMove, kMovers);
-      if (*(volatile int *)&failed) return;
+      if (*given_up == m.unit + 1u) return;
       const int gi = p.c.head_grp[m.un.bh % p.c.Hkv];
       const CacheGroup &grp = p.c.grp[gi];
 #pragma unroll
@@ -476,7 +479,9 @@ __global__ void __launch_bounds__(kMovers + kScouts) evict_move_kernel(const __g
       if (more) {
         read(m, mine, w_mine);
         bar_sync(kMove, kMovers);  // the block has read its rows and weights
-        if (tid == 0) st_release(p.read_done + m.unit, 1u);
+        // (failure-detection test: the chosen block keeps its first unit's to itself)
+        const bool stall = i == 0 && (int)blockIdx.x == p.stall_block;
+        if (tid == 0 && !stall) st_release(p.read_done + m.unit, 1u);
       }
       if (i > 0) {
         write(before, prev, w_prev);

@@ -109,6 +109,7 @@ struct EvictParams {
   int64_t chunks;       // of all heads
   int64_t chunks_seq;   // of a sequence's heads
   int32_t chunk_off[KVX_MAX_KV_HEADS];  // where a KV head's begin among them
+  int32_t stall_block;                  // failure-detection test (-1: none)
   uint32_t wait_ns;
 };
 // Workspace: header | units | read_done | source.
