@@ -909,11 +909,20 @@ int kvx_read_kv(const kvx_cache *cache, const int32_t *q_start, const int64_t *s
  *                  to one sequence, as for kvx_build_tables.
  *   workspace      >= kvx_window_attn_workspace_bytes(cache, max_q, weights != NULL). With
  *                  weights it holds a score for every query row and token that the page
- *                  tables have room for, 4 * max_q * g bytes a token of a head.
- *   q, max_q, scale, out: as for kvx_tree_attn. 4-bit caches compute with lo + step * code
- *                  unrounded; steps must not be negative (kvx_append_kv makes none that are). A
- *                  token's weight times its step of V is off by at most 2^-22 of itself or 2^-36 of the
- *                  head's largest step, and K's steps and lo have to stay below 2^90 in magnitude.
+ *                  tables have room for. A head's query rows are in row groups of T = floor(R / g)
+ *                  new rows: R is 32 for fp32 caches, else the least of 4, 8 and 16 (bf16: and 32)
+ *                  that holds max_q * g, or the largest. Every one of the B * Hkv heads takes 4 *
+ *                  ceil(max_q / T) * (min(T, max_q) * g, rounded up to a multiple of 4) bytes for each
+ *                  token of the LARGEST page table's room (page_table_stride * page_size, rounded up to
+ *                  64), whatever its own group's table, its length or its window: 16 bytes for one row
+ *                  of up to 4 heads, 512 for 32 rows of 4 (bf16). Room for 32k tokens, 64 sequences of
+ *                  8 heads: 0.27 and 8.6 GB.
+ *   q, max_q, scale, out: as for kvx_tree_attn. 4-bit caches compute with lo + step * code unrounded.
+ *                  There a query row's elements count exactly down to 2^-27 of its largest; smaller ones are
+ *                  off by at most 2^-35 of that, or by what moves no score by more than 2^-45. Steps
+ *                  must be finite and not negative (kvx_append_kv makes no others). A token's weight times its
+ *                  step of V is off by at most 2^-22 of itself or 2^-36 of the head's largest step, and
+ *                  K's steps and lo have to stay below 2^90 in magnitude.
  * The same lengths are out of range, page ids outside a pool read as zero rows
  * (KVX_DEV_BAD_PAGE; their weights are lost), and so much work that (tiles + 1) over all
  * heads and groups of query rows pass 2^31 is refused whole (KVX_DEV_BAD_LENGTH). A call that
