@@ -64,6 +64,19 @@ __device__ __forceinline__ Head load_head(const EvictParams &p, int bh, bool rep
   return hd;
 }
 
+constexpr int kSmallKeys = 4096, kLargeKeys = 16384;  // in a block's shared memory
+
+// Blocks of a head of n tokens, `most` at most: as many as its keys fill, or, where heads are few, as
+// give each kSmallKeys of them. Measured, the call in a graph with 1 / 2 / 4 / 8 blocks a head: 32 heads of 8000
+// tokens 33 / 27 / 25 / 35 us, of 16,000 54 / 39 / 32 / 41, of 32,000 147 / 62 / 46 / 52; 8 heads of 60,000
+// 295 / 138 / 56 / 44; 128 heads of 16,000 82 / 76 / 77 / 112, of 32,000 201 / 130 / 125 / 151, of 60,000
+// 406 / 277 / 210 / 229 (keys past a block's shared memory are read again in every pass).
+__host__ __device__ constexpr uint32_t select_blocks(int n, int heads, uint32_t most) {
+  uint32_t C = 1;
+  while (C < most && (((int64_t)C * heads < 152 && (int64_t)C * kSmallKeys < n) || (int64_t)C * kLargeKeys < n)) C *= 2;
+  return C;
+}
+
 // kThreads threads, kKeys keys of a block's run kept in shared memory (a longer run reads the
 // others again in every pass).
 template <int kThreads, int kKeys>
@@ -84,12 +97,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   SelectSmem<kThreads, kKeys> &sm = *(SelectSmem<kThreads, kKeys> *)smem_raw;
   pdl_launch_dependents();
   pdl_wait();
-  uint32_t C;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
+  uint32_t most;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(most));
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = (int)(blockIdx.x / C);
+  const int bh = (int)(blockIdx.x / most);
   const Head hd = load_head(p, bh, rank == 0 && tid == 0);
+  // The cluster is as large as the page tables' room may ask for; the head's length says how many of
+  // its blocks take part. The others leave at once (nobody reads their shared memory, and the cluster's barrier
+  // waits for the blocks that have not left; a length that rank 0 has already replaced is smaller).
+  const uint32_t C = select_blocks(hd.n, p.c.B * p.c.Hkv, most);
+  if (rank >= C) return;
   const int gi = p.c.head_grp[hd.h], row = p.c.head_row[hd.h];
   const CacheGroup &grp = p.c.grp[gi];
   const int32_t *table = grp.table + (size_t)hd.b * grp.stride;
@@ -544,16 +562,18 @@ cudaError_t launch_select(const EvictParams &p, int C, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
-  // Many short heads: a small block each, many to an SM. Else two blocks to an SM, and a head's
-  // blocks as many as its keys fill, or, where heads are few, as give each 4096 of them. 128 heads of
-  // 8k to 32k tokens: one block a head 122 us (keys past its shared memory are read in every
-  // pass), two 50, four 56, eight 98.
+  // Rooms of page tables are all that is known here. Heads that no table lets pass 4096 tokens, and
+  // many: a small block each, many to an SM (512 heads of 2000 tokens 34 us, in large blocks 42; of 4000 64 and
+  // 70, 256 of them 39 and 37). Else clusters for the longest head that fits; blocks that a head's
+  // length does not need still cost their launch. 512 heads of 1000 to 2500 tokens in tables 1, 4, 8 and 32
+  // times as wide: 37, 41, 56, 75 us (243 with all blocks of the clusters at work); 128 heads of 8k to 32k:
+  // 128, 145, 146, 144 (181).
   const int heads = p.c.B * p.c.Hkv;
-  const int64_t longest = p.chunks / heads * kChunk;  // (their mean room)
-  int C = 1;
-  while (C < 8 && ((C * heads < 152 && C * 4096 < longest) || C * 16384 < longest)) C *= 2;
-  cudaError_t e = longest <= 4096 && heads >= 152 ? launch_select<256, 4096>(p, 1, st)
-                                                  : launch_select<512, 16384>(p, C, st);
+  int room = 0;
+  for (int g = 0; g < p.c.G; ++g) room = p.c.grp[g].tokens > room ? p.c.grp[g].tokens : room;
+  cudaError_t e = room <= kSmallKeys && heads >= 152
+                      ? launch_select<256, kSmallKeys>(p, 1, st)
+                      : launch_select<512, kLargeKeys>(p, (int)select_blocks(room, heads, 8), st);
   if (e != cudaSuccess) return e;
   const bool wide = p.c.D == 128;
   if (p.q4) return wide ? launch_move<uint2, 9, true>(p, st) : launch_move<uint32_t, 9, true>(p, st);
