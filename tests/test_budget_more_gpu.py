@@ -121,3 +121,31 @@ def test_4_bit_rows_that_nobody_sees_hold_anything(D, P, bad, T):
             got = one.upload().run()
             others = [i for i in range(T) if i != row]
             assert np.array_equal(got[others], a[others]) and not np.isfinite(got[row]).any()
+
+
+def test_evictions_and_attention_on_two_streams_at_once():
+    """Two caches, each evicted again and again on a stream of its own, beside attention over a third."""
+    budget = ((3000, 2500, 900),) * 4
+    a, b = (Evict(BCase("bf16", 128, 3, 1, (0, 1, 1), kv=((9000, 5000, 4000),) * 4, T=(0,) * 4, seed=i), budget, "skewed")
+            for i in (1, 2))
+    c = Budget(BCase("bf16", 128, 2, 4, (0, 1), kv=((3000, 1300),), T=(1,), window=(1000, 2 ** 31 - 1))).upload()
+    for s in (a, b):
+        s.upload()
+        s.before = s.snapshot()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                s.evict(4, 64, True)
+                # all of it again: heads already at their budgets stay as they are
+                kvx.kvx_evict(s.cache, s.kv_out, s.dbudget, 4, 64, s.dw, s.dw, s.kv_out, s.ews)
+                if i < 19:  # the rows as they were
+                    for d, x in zip(s.dk + s.dv, s.before[0] + s.before[1]):
+                        d.view(torch.uint8).view(-1).copy_(torch.from_numpy(x.reshape(-1)), non_blocking=True)
+                    for d, w in zip(s.dw, s.w):
+                        d.copy_(torch.from_numpy(w), non_blocking=True)
+        c.attend(stream=streams[2])
+    for s in (a, b):
+        s.check_evicted(4, 64, True, s.before)
+    c.check(c.out.cpu().numpy())
