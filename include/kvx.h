@@ -953,7 +953,7 @@ int kvx_window_attn(const kvx_cache *cache, const void *q, int64_t q_stride,
  *   sinks, recent  host, >= 0.
  *   weights      host array [num_groups] of device fp32 pools, as for kvx_window_attn.
  *   weights_out  likewise: the weights' own pools (all of them), or others that overlap
- *                none, which then receive the weights of all kept tokens.
+ *                none, which then receive the weights of all kept tokens (a -0 may arrive as 0).
  *   kv_len_out   device int32 [B][Hkv]; may be kv_len itself.
  *   workspace    >= kvx_evict_workspace_bytes(cache).
  * A head whose kv_len does not fit its page table, or is negative, or whose budget is

@@ -18,7 +18,8 @@
 // keep all), 419 MB, 128 us: 50 of it the first launch (latency of
 // the loads and the three passes), 80 the second (356 MB, 4.4 TB/s: two blocks an SM, each with two units
 // of 32 KB under way, are bound by the latency of a unit's steps). 512 short heads, half of them
-// cut to an eighth, 61 MB, 36 us: latency.
+// cut to an eighth, 61 MB, 37 us: latency. With the weights in place 122 and 31 us; the 128 heads in fp32 (908 MB)
+// 290, in 4 bits (189 MB) 180. All in page tables as wide as the longest head; launch_evict has wider ones.
 #include <math.h>
 
 #include "ptx.cuh"

@@ -6,8 +6,9 @@
 // 0. A group with a non-finite element, or whose range is not finite, gets step 0 and lo NaN, so that all of it reads as NaN. Four lanes hold a group,
 // sixteen elements (32 bytes in, two 4-byte words of codes out) each; minimum and maximum
 // meet in two shuffles.
-// Measured on one GB300: 44k rows of 8 heads quantised in 75 us (230 MB; instructions bound it: with
+// Measured on one GB300: 43k rows of 8 heads quantised in 75 us (230 MB; instructions bound it: with
 // eight elements a lane, 94 us, 74 % of the issue slots were taken), read back in 47 us (230 MB, 4.9 TB/s).
+// bf16 rows of the same shape are read back in 66 us (352 MB, 5.3 TB/s), fp32 in 117 (701 MB, 6.0 TB/s).
 #include <math.h>
 
 #include "ptx.cuh"

@@ -37,13 +37,17 @@
 // Measured on one GB300 (a call in a graph):
 //  * bf16, 16 sequences of 8k to 32k, one token, two of eight heads unlimited, the others with
 //    windows of 4096: 89 us for 526 MB (6.0 TB/s; the copy rate in the middle, about 10 us of
-//    ramp, last output and merge). 8 x 122k: 587 us for 4.0 GB (6.8 TB/s).
+//    ramp, last output and merge). 8 x 122k without windows: 577 us for 4.0 GB (6.9 TB/s).
 //  * bf16, up to 8 drafts of 5 query heads, windows of 1000 in half of the heads: 210 us for 676 MB.
 //    Fixed instruction latencies bound it: 12 consumer warps an SM (128 registers) issue on 38 % of the
 //    cycles, the tensor pipe is 38 % busy; products in shorter chains gain nothing. 32 rows in one warp took 413, 16 in one of two warps 254.
 //  * 4 bits, 16 sequences of 8k to 32k: 48 us for 121 MB; 8 x 122k 270 us for 1.13 GB (4.2 TB/s).
 //    Instructions bound it: about 760 for 32 tokens, 325 of them on the half-rate integer pipe. Without
 //    any of that work the loads take 177 us, in batches of four stages; stage by stage they took 559.
+//  * 4 bits, several rows of 4 heads, 16 sequences of 8k to 32k (107, 151 and 125 MB): two rows (groups of 8)
+//    49 us, four (16) 136, eight 211. Groups of 16 are the slower ones (255 registers, 108 bytes
+//    spilled at D 128): in groups of 8 four rows take 101 and eight 157; 8 x 122k, four rows, 579
+//    instead of 863. What they have for them is half the row groups against the 2^31 units of a call.
 // Tried and slower: with 4 bits (288 at that time) six consumer warps on stages of 32 tokens (334, 342
 // in single 16-token steps), on as many stages of 64 as warps (505), four on stages of 32 tokens
 // (298), single 16-token steps (297); for 32 rows four blocks an SM (209 -> 219).

@@ -10,7 +10,9 @@
 // not all finite, a separate path skips what a row does not see instead of multiplying it by
 // zero, so that NaN and infinities in unseen rows have no influence.
 // Latency bounds short inputs: two sequences of 37 to 100 tokens 16.5 us with the merge, in a graph (18.6 when
-// every edge tile took the separate path).
+// every edge tile took the separate path). Longer ones are bound by the multiplications, 32 rows
+// whatever the call has: 16 sequences of 8k to 32k, windows of 4096 in six of eight heads, 945 MB, one row of 4
+// heads 887 us (1.1 TB/s), eight rows 990 us.
 #include <math.h>
 
 #include "window_split.cuh"

@@ -5,9 +5,11 @@
 // maximum and sum, which are only known when all of a head's pieces are merged: hence
 // the stored scores and a launch of its own. A token's rows are added in a fixed order, so
 // nothing depends on timing. Blocks take equal parts of all heads' visited tiles.
-// Recomputing the scores instead would read K again, 256 bytes a token where a decode step of
-// four query heads stores and reads 32. Measured on one GB300, the launch alone: 16 sequences of 8k to
-// 32k, one row of 4 heads, about 10 us of the call's 87; 4 sequences, 32 rows (200 MB of scores) 60 us.
+// Recomputing the scores instead would read K again, 256 bytes a token (bf16, D 128), where storing and reading them
+// is 8 a query row: 32 for a decode step of four heads. From 32 rows a head on that reason is gone (32 rows of
+// four heads: 1024 bytes); the form that would recompute them is not built. Measured on one GB300, in a graph: 16
+// sequences of 8k to 32k, one row of 4 heads, 89 us with weights, 71 without (this launch by itself 17); 4 sequences,
+// 32 rows (200 MB of scores) 253 and 155 (60).
 #include <math.h>
 
 #include "window_split.cuh"
@@ -27,7 +29,8 @@ struct Smem {
 // token's scores are one stretch of memory to neighbouring lanes; several tokens in flight.
 // Measured, the call in a graph: a decode step (one lane a token) with two tokens in flight and four
 // blocks an SM 84.7 us, four tokens 86.2, four and no more blocks 89.2; 32 rows voting (eight
-// lanes) 258, 270, 249.
+// lanes) 258, 270, 249. Lanes: as many as a row group has fours of rows; 8 rows with two, four and eight lanes
+// 105, 117, 141 us, 16 rows with four and eight 127, 154 (16 sequences of 8k to 32k).
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads, kLanes == 1 ? 4 : 3) weigh_kernel(const __grid_constant__ WindowParams p,
                                                          int group_tokens) {
